@@ -9,7 +9,9 @@ raises.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
+import functools
 import os
 
 import torch
@@ -24,6 +26,11 @@ __all__ = [
     "mbok_gemvt", "mbok_gemvt_workspace_bytes", "mbok_gemvt_noalloc", "mbok_gemvt_scratch_bytes",
     "mbok_svid_workspace_bytes", "mbok_svid_decompose", "mbok_svid_pack",
     "mbok_svid_gemv_workspace_bytes", "mbok_svid_gemv", "MBOK_MAX_SVID_ITERS",
+    "mbok_gemmt", "mbok_gemmt_workspace_bytes", "mbok_scale_grad",
+    "mbok_scale_grad_workspace_bytes", "MBOK_ACT_SILU", "MBOK_ACT_GELU", "mbok_gated_stack",
+    "mbok_gated_pack", "mbok_gated", "mbok_gated_backward", "mbok_distill_desc",
+    "mbok_distill_desc_init", "mbok_distill", "mbok_distill_backward", "MBOK_MAX_TOP",
+    "MBOK_MAX_VOCAB", "MBOK_MAX_DISTILL_ROWS", "MBOK_DISTILL_STATS",
     "mbok_version", "workspace_for",
     "alpha_torch_dtype", "quantize_and_pack", "allocate_for_budget",
 ]
@@ -36,6 +43,11 @@ MBOK_MAX_T = 65536
 MBOK_LAYOUT_L64 = 1
 MBOK_MAX_REFIT_ROUNDS = 64
 MBOK_MAX_SVID_ITERS = 1000
+MBOK_ACT_SILU, MBOK_ACT_GELU = 0, 1
+MBOK_MAX_TOP = 1024
+MBOK_MAX_VOCAB = 1 << 19
+MBOK_MAX_DISTILL_ROWS = 1 << 24
+MBOK_DISTILL_STATS = 8
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 _LIB = None
@@ -57,6 +69,15 @@ class mbok_desc(ctypes.Structure):
                 f"alpha_dtype={self.alpha_dtype}, layout={self.layout})")
 
 
+class mbok_distill_desc(ctypes.Structure):
+    _fields_ = [("vocab", ctypes.c_int32), ("top", ctypes.c_int32),
+                ("temperature", ctypes.c_float)]
+
+    def __repr__(self):
+        return (f"mbok_distill_desc(vocab={self.vocab}, top={self.top}, "
+                f"temperature={self.temperature})")
+
+
 def library_path() -> str:
     return os.environ.get("MBOK_LIBRARY", os.path.join(_HERE, "libmbok.so"))
 
@@ -73,6 +94,7 @@ def load_library() -> ctypes.CDLL:
     lib = ctypes.CDLL(path)
     P, I32, I64, SZ = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t
     D = ctypes.POINTER(mbok_desc)
+    DD, F = ctypes.POINTER(mbok_distill_desc), ctypes.c_float
     sigs = {
         "mbok_desc_init": (ctypes.c_int, [D, I32, I32, I32, I32]),
         "mbok_packed_bytes": (SZ, [D]),
@@ -95,6 +117,20 @@ def load_library() -> ctypes.CDLL:
         "mbok_svid_pack": (ctypes.c_int, [D, P, P, P, P]),
         "mbok_svid_gemv_workspace_bytes": (SZ, [D]),
         "mbok_svid_gemv": (ctypes.c_int, [D, P, P, P, I32, P, P, P]),
+        "mbok_gemmt": (ctypes.c_int, [D, P, P, I64, I64, P, I64, P, P]),
+        "mbok_gemmt_workspace_bytes": (SZ, [D, I64]),
+        "mbok_scale_grad": (ctypes.c_int, [D, P, P, I64, I64, P, I64, P, I32, P, P]),
+        "mbok_scale_grad_workspace_bytes": (SZ, [D, I64]),
+        "mbok_gated_stack": (ctypes.c_int, [D, D]),
+        "mbok_gated_pack": (ctypes.c_int, [D, P, P, P, P, P, P]),
+        "mbok_gated": (ctypes.c_int, [D, P, P, I32, I64, I64, I32, P, I64, P, I64, P]),
+        "mbok_gated_backward": (ctypes.c_int, [D, P, P, I64, P, I64, I64, I32, P, I64, P, I64, P,
+                                               P]),
+        "mbok_distill_desc_init": (ctypes.c_int, [DD, I32, I32, F]),
+        "mbok_distill": (ctypes.c_int, [DD, P, I32, I64, I64, P, I32, P, I64, P, P, P, P, P, I32,
+                                        I64, P]),
+        "mbok_distill_backward": (ctypes.c_int, [DD, P, I32, I64, I64, P, I32, P, I64, P, P, P, P,
+                                                 P, I32, I64, P]),
         "mbok_status_str": (ctypes.c_char_p, [ctypes.c_int]),
         "mbok_version": (ctypes.c_char_p, []),
     }
@@ -496,6 +532,301 @@ def _gemm_call(name: str, d: mbok_desc, packed: torch.Tensor, X: torch.Tensor, Y
     fn = getattr(load_library(), name)
     _check(fn(ctypes.byref(d), packed.data_ptr(), X.data_ptr(), xd, T, ldx, Y.data_ptr(), ldy,
               _stream(stream)), name)
+
+
+# ------------------------------------- fine-tuning and the gated feed-forward block
+
+_FLOATS = {torch.float32: MBOK_F32, torch.float16: MBOK_F16, torch.bfloat16: MBOK_BF16}
+
+
+@functools.lru_cache(maxsize=4096)
+def _packed_bytes(m: int, n: int, K: int, alpha_dtype: int) -> int:
+    return mbok_packed_bytes(mbok_desc_init(m, n, K, alpha_dtype))
+
+
+@functools.lru_cache(maxsize=4096)
+def _slices_bytes(name: str, m: int, n: int, K: int, alpha_dtype: int, T: int) -> int:
+    d = mbok_desc_init(m, n, K, alpha_dtype)
+    return int(getattr(load_library(), name)(ctypes.byref(d), T))
+
+
+class _on_device:
+    """The device of a call's tensors, made current for its launch when it is
+    not; the raw handle of the call's stream (by default that device's current
+    one)."""
+
+    def __init__(self, dev: int):
+        self.dev, self.guard = dev, None
+        if dev != torch.cuda.current_device():
+            self.guard = torch.cuda.device(dev)
+
+    def __enter__(self):
+        if self.guard is not None:
+            self.guard.__enter__()
+        return self
+
+    def __exit__(self, *exc):
+        if self.guard is not None:
+            self.guard.__exit__(*exc)
+
+    def stream(self, stream) -> int:
+        return torch.cuda.current_stream(self.dev).cuda_stream if stream is None \
+            else _stream(stream)
+
+
+def _one_device(first: torch.Tensor, **others) -> int:
+    dev = first.get_device()
+    for name, t in others.items():
+        if t is not None and _dev(t, name).get_device() != dev:
+            raise ValueError(f"{name} is on another device than the other tensors")
+    return dev
+
+
+def _matrix(t: torch.Tensor, name: str, rows: int, cols: int, dtype) -> int:
+    """Row stride of a [rows, >= cols] matrix with contiguous rows."""
+    if t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.dim() != 2 or t.shape[0] != rows or t.shape[1] < cols:
+        raise ValueError(f"{name} must be [{rows}, >= {cols}], got {tuple(t.shape)}")
+    if t.stride(1) != 1 and t.shape[1] > 1:
+        raise ValueError(f"{name} rows must be contiguous")
+    if rows == 1:
+        # the stride of a single row is arbitrary and never used
+        return (max(cols, t.shape[1]) + 7) // 8 * 8
+    if t.stride(0) < cols:
+        raise ValueError(f"{name} rows must not overlap")
+    return t.stride(0)
+
+
+def _vector(t: torch.Tensor, name: str, count: int, dtype) -> int:
+    if t.dtype != dtype or not t.is_contiguous() or t.numel() < count:
+        raise ValueError(f"{name} must be contiguous {dtype} with {count} elements")
+    return t.data_ptr()
+
+
+def _packed(d: mbok_desc, packed: torch.Tensor, m: int) -> int:
+    if not packed.is_contiguous() or packed.numel() * packed.element_size() < \
+            _packed_bytes(m, d.n, d.K, d.alpha_dtype):
+        raise ValueError("packed must be contiguous and hold the layer")
+    return packed.data_ptr()
+
+
+def _slices(name: str, d: mbok_desc, m: int, T: int, workspace, dev: int, stream):
+    """(pointer, tensor) of the workspace of a call that may split its sum.
+
+    True keeps one per (device, stream) as workspace_for does, except under
+    graph capture: a captured call gets memory of its own from the graph's
+    pool, so that no later call's growth frees it and no two graphs share it."""
+    if workspace is None or workspace is False:
+        return None, None
+    need = _slices_bytes(name, m, d.n, d.K, d.alpha_dtype, T)
+    if need == 0:
+        return None, None
+    if workspace is True:
+        device = torch.device("cuda", dev)
+        if stream is None:
+            target = contextlib.nullcontext()
+        else:
+            target = torch.cuda.stream(
+                stream if isinstance(stream, torch.cuda.Stream)
+                else torch.cuda.ExternalStream(int(stream), device=device))
+        with target:
+            captured = torch.cuda.is_current_stream_capturing()
+            ws = torch.empty(need, dtype=torch.uint8, device=device) if captured else None
+        if not captured:
+            ws = workspace_for(need, device, stream)
+    else:
+        ws = _dev(workspace, "workspace")
+        if ws.get_device() != dev:
+            raise ValueError("workspace is on another device than the other tensors")
+        if not ws.is_contiguous() or ws.numel() * ws.element_size() < need:
+            raise ValueError("workspace must be contiguous and large enough")
+    return ws.data_ptr(), ws
+
+
+def mbok_gemmt_workspace_bytes(d: mbok_desc, T: int) -> int:
+    return int(load_library().mbok_gemmt_workspace_bytes(ctypes.byref(d), T))
+
+
+def mbok_scale_grad_workspace_bytes(d: mbok_desc, T: int) -> int:
+    return int(load_library().mbok_scale_grad_workspace_bytes(ctypes.byref(d), T))
+
+
+def mbok_gemmt(d: mbok_desc, packed: torch.Tensor, dY: torch.Tensor, dX: torch.Tensor,
+               workspace: torch.Tensor | None | bool = True, stream=None) -> None:
+    """dX[T, n] (bf16, overwritten) = dY W_hat for dY bf16 [T, m] (row strides
+    lddx, lddy).
+
+    workspace: True (default) uses a workspace kept for this device and
+    stream (under graph capture one of the graph's own); a tensor is used as
+    given; None/False runs without one."""
+    dev = _one_device(_dev(dY, "dY"), packed=packed, dX=dX)
+    T = dY.shape[0]
+    lddy = _matrix(dY, "dY", T, d.m, torch.bfloat16)
+    lddx = _matrix(dX, "dX", T, d.n, torch.bfloat16)
+    with _on_device(dev) as on:
+        ws, _keep = _slices("mbok_gemmt_workspace_bytes", d, d.m, T, workspace, dev, stream)
+        _check(load_library().mbok_gemmt(
+            ctypes.byref(d), _packed(d, packed, d.m), dY.data_ptr(), T, lddy, dX.data_ptr(), lddx,
+            ws, on.stream(stream)), "mbok_gemmt")
+
+
+def mbok_scale_grad(d: mbok_desc, packed: torch.Tensor, dY: torch.Tensor, X: torch.Tensor,
+                    dalpha: torch.Tensor, accumulate: bool = False,
+                    workspace: torch.Tensor | None | bool = True, stream=None) -> None:
+    """dalpha fp32 [K, m, n/128] = (or, accumulate, +=) sum over each group's
+    columns of B_k (.) (dY^T X), for dY bf16 [T, m] and X bf16 [T, n].
+
+    workspace: as for mbok_gemmt."""
+    dev = _one_device(_dev(dY, "dY"), packed=packed, X=X, dalpha=dalpha)
+    T = dY.shape[0]
+    lddy = _matrix(dY, "dY", T, d.m, torch.bfloat16)
+    ldx = _matrix(X, "X", T, d.n, torch.bfloat16)
+    out = _vector(dalpha, "dalpha", d.K * d.m * (d.n // MBOK_GROUP), torch.float32)
+    with _on_device(dev) as on:
+        ws, _keep = _slices("mbok_scale_grad_workspace_bytes", d, d.m, T, workspace, dev, stream)
+        _check(load_library().mbok_scale_grad(
+            ctypes.byref(d), _packed(d, packed, d.m), dY.data_ptr(), T, lddy, X.data_ptr(), ldx,
+            out, int(bool(accumulate)), ws, on.stream(stream)), "mbok_scale_grad")
+
+
+def mbok_gated_stack(d: mbok_desc) -> mbok_desc:
+    """The descriptor of the stacked layer (8 gate rows, 8 up rows per 16-row
+    tile) of two projections of shape d: 16 ceil(m / 8) rows."""
+    out = mbok_desc()
+    _check(load_library().mbok_gated_stack(ctypes.byref(d), ctypes.byref(out)),
+           "mbok_gated_stack")
+    return out
+
+
+def mbok_gated_pack(d: mbok_desc, signs_gate: torch.Tensor, alpha_gate: torch.Tensor,
+                    signs_up: torch.Tensor, alpha_up: torch.Tensor, packed: torch.Tensor,
+                    stream=None) -> None:
+    """signs int8 [K, m, n] + alpha [K, m, n/128] of both projections -> packed
+    uint8 [mbok_packed_bytes(mbok_gated_stack(d))]."""
+    dev = _one_device(_dev(packed, "packed"), signs_gate=signs_gate, alpha_gate=alpha_gate,
+                      signs_up=signs_up, alpha_up=alpha_up)
+    ns, na = d.K * d.m * d.n, d.K * d.m * (d.n // MBOK_GROUP)
+    at = alpha_torch_dtype(d.alpha_dtype)
+    ptrs = [_vector(signs_gate, "signs_gate", ns, torch.int8),
+            _vector(alpha_gate, "alpha_gate", na, at),
+            _vector(signs_up, "signs_up", ns, torch.int8),
+            _vector(alpha_up, "alpha_up", na, at)]
+    with _on_device(dev) as on:
+        _check(load_library().mbok_gated_pack(
+            ctypes.byref(d), *ptrs, _packed(d, packed, _stacked_rows(d)), on.stream(stream)),
+            "mbok_gated_pack")
+
+
+def _stacked_rows(d: mbok_desc) -> int:
+    return 16 * ((d.m + 7) // 8)
+
+
+def mbok_gated(d: mbok_desc, packed: torch.Tensor, X: torch.Tensor, H: torch.Tensor,
+               pre: torch.Tensor | None = None, act: int = MBOK_ACT_SILU, stream=None) -> None:
+    """H[T, m] (bf16, overwritten) = act(X Wg^T) (.) (X Wu^T) for X bf16 [T, n];
+    d describes one projection, packed is mbok_gated_pack's buffer.  pre bf16
+    [T, 16 ceil(m / 8)] receives the pre-activations in the stacked order."""
+    dev = _one_device(_dev(X, "X"), packed=packed, H=H, pre=pre)
+    T, m2 = X.shape[0], _stacked_rows(d)
+    ldx = _matrix(X, "X", T, d.n, torch.bfloat16)
+    ldh = _matrix(H, "H", T, d.m, torch.bfloat16)
+    ldpre = 0 if pre is None else _matrix(pre, "pre", T, m2, torch.bfloat16)
+    with _on_device(dev) as on:
+        _check(load_library().mbok_gated(
+            ctypes.byref(d), _packed(d, packed, m2), X.data_ptr(), MBOK_BF16, T, ldx, act,
+            H.data_ptr(), ldh, None if pre is None else pre.data_ptr(), ldpre,
+            on.stream(stream)), "mbok_gated")
+
+
+def mbok_gated_backward(d: mbok_desc, packed: torch.Tensor, pre: torch.Tensor, dH: torch.Tensor,
+                        dpre: torch.Tensor, dX: torch.Tensor | None = None,
+                        act: int = MBOK_ACT_SILU,
+                        workspace: torch.Tensor | None | bool = True, stream=None) -> None:
+    """Gradients of the gated block: dpre bf16 [T, 16 ceil(m / 8)] (stacked
+    order; may be pre itself) and, unless None, dX bf16 [T, n], from pre as
+    mbok_gated wrote it and dH bf16 [T, m].
+
+    workspace: as for mbok_gemmt."""
+    dev = _one_device(_dev(dH, "dH"), packed=packed, pre=pre, dpre=dpre, dX=dX)
+    T, m2 = dH.shape[0], _stacked_rows(d)
+    lddh = _matrix(dH, "dH", T, d.m, torch.bfloat16)
+    ldpre = _matrix(pre, "pre", T, m2, torch.bfloat16)
+    lddpre = _matrix(dpre, "dpre", T, m2, torch.bfloat16)
+    lddx = 0 if dX is None else _matrix(dX, "dX", T, d.n, torch.bfloat16)
+    with _on_device(dev) as on:
+        ws = None
+        if dX is not None:
+            ws, _keep = _slices("mbok_gemmt_workspace_bytes", d, m2, T, workspace, dev, stream)
+        _check(load_library().mbok_gated_backward(
+            ctypes.byref(d), _packed(d, packed, m2), pre.data_ptr(), ldpre, dH.data_ptr(), lddh,
+            T, act, dpre.data_ptr(), lddpre, None if dX is None else dX.data_ptr(), lddx, ws,
+            on.stream(stream)), "mbok_gated_backward")
+
+
+def mbok_distill_desc_init(vocab: int, top: int, temperature: float = 1.0) -> mbok_distill_desc:
+    d = mbok_distill_desc()
+    _check(load_library().mbok_distill_desc_init(ctypes.byref(d), vocab, top, temperature),
+           "mbok_distill_desc_init")
+    return d
+
+
+def _distill_args(d, Z, t_logits, t_index, t_lse, weight, dZ):
+    """The arguments both distillation calls share, checked."""
+    T = Z.shape[0]
+    zt, tt = _FLOATS.get(Z.dtype), _FLOATS.get(t_logits.dtype)
+    if zt is None or tt is None:
+        raise ValueError("Z and t_logits must be float32, float16 or bfloat16")
+    ldz = _matrix(Z, "Z", T, d.vocab, Z.dtype)
+    ldt = _matrix(t_index, "t_index", T, d.top, torch.int32)
+    if _matrix(t_logits, "t_logits", T, d.top, t_logits.dtype) != ldt and T > 1:
+        raise ValueError("t_logits and t_index must have the same row stride")
+    lse = None if t_lse is None else _vector(t_lse, "t_lse", T, torch.float32)
+    w = None if weight is None else _vector(weight, "weight", T, torch.float32)
+    if dZ is None:
+        grad = (None, zt, 0)
+    else:
+        if dZ.dtype not in (Z.dtype, torch.bfloat16):
+            raise ValueError("dZ must have the dtype of Z or bfloat16")
+        grad = (dZ.data_ptr(), _FLOATS[dZ.dtype], _matrix(dZ, "dZ", T, d.vocab, dZ.dtype))
+    return T, (Z.data_ptr(), zt, T, ldz, t_logits.data_ptr(), tt, t_index.data_ptr(), ldt, lse,
+               w), grad
+
+
+def mbok_distill(d: mbok_distill_desc, Z: torch.Tensor, t_logits: torch.Tensor,
+                 t_index: torch.Tensor, loss: torch.Tensor, stats: torch.Tensor | None = None,
+                 dZ: torch.Tensor | None = None, t_lse: torch.Tensor | None = None,
+                 weight: torch.Tensor | None = None, stream=None) -> None:
+    """loss[T] (fp32, overwritten) = weight tau^2 KL(teacher || softmax(Z / tau))
+    over the teacher's listed logits t_logits [T, top] at the tokens t_index
+    (int32; negative: no entry), renormalised, or with t_lse [T] as the
+    teacher's own probabilities with the rest as one class.  stats fp32 [T,
+    MBOK_DISTILL_STATS] is what mbok_distill_backward takes; dZ (dtype of Z or
+    bf16; may be Z) receives the gradient of sum(loss) in the same pass."""
+    dev = _one_device(_dev(Z, "Z"), t_logits=t_logits, t_index=t_index, loss=loss, stats=stats,
+                      dZ=dZ, t_lse=t_lse, weight=weight)
+    T, args, grad = _distill_args(d, Z, t_logits, t_index, t_lse, weight, dZ)
+    out = _vector(loss, "loss", T, torch.float32)
+    st = None if stats is None else _vector(stats, "stats", T * MBOK_DISTILL_STATS, torch.float32)
+    with _on_device(dev) as on:
+        _check(load_library().mbok_distill(ctypes.byref(d), *args, out, st, *grad,
+                                           on.stream(stream)), "mbok_distill")
+
+
+def mbok_distill_backward(d: mbok_distill_desc, Z: torch.Tensor, t_logits: torch.Tensor,
+                          t_index: torch.Tensor, stats: torch.Tensor, dloss: torch.Tensor,
+                          dZ: torch.Tensor, t_lse: torch.Tensor | None = None,
+                          weight: torch.Tensor | None = None, stream=None) -> None:
+    """dZ (dtype of Z or bf16; may be Z) = dloss[t] * d loss[t] / d Z[t, :] after
+    mbok_distill with stats on the same inputs; dloss fp32 [T]."""
+    dev = _one_device(_dev(Z, "Z"), t_logits=t_logits, t_index=t_index, stats=stats,
+                      dloss=dloss, dZ=_dev(dZ, "dZ"), t_lse=t_lse, weight=weight)
+    T, args, grad = _distill_args(d, Z, t_logits, t_index, t_lse, weight, dZ)
+    st = _vector(stats, "stats", T * MBOK_DISTILL_STATS, torch.float32)
+    dl = _vector(dloss, "dloss", T, torch.float32)
+    with _on_device(dev) as on:
+        _check(load_library().mbok_distill_backward(ctypes.byref(d), *args, st, dl, *grad,
+                                                    on.stream(stream)), "mbok_distill_backward")
 
 
 # ---------------------------------------------------------------- conveniences

@@ -1,0 +1,524 @@
+// Distillation loss from a teacher's top logits, and its gradient (gfx950).
+//
+// "Highly Efficient and Effective LLMs with Multi-Boolean Architectures",
+// gist.science summaries, training sections: the kernels are finetuned by
+// distillation from the full-precision model.  Per row, with q = softmax(z /
+// tau) over the vocabulary and the teacher's listed (index v_j, logit l_j):
+//     loss = w tau^2 [ sum_j p_j (log p_j - log q_{v_j}) + p_r log(p_r / q_r) ]
+//     dz_v = w tau [ q_v (1 - [v not listed] p_r / q_r) - sum_{j: v_j = v} p_j ]
+// where p is the softmax of the listed l / tau (then p_r = 0), or with t_lse
+// exp(l / tau - t_lse) and p_r = 1 - sum p the mass of what is not listed.
+//
+// Bound: the row of logits, read once and (gradient) written once.  One
+// workgroup takes one row and keeps it in registers as loaded (NV 16-byte
+// vectors per thread), so the maximum, the sum of exponentials and the
+// gradient cost one read.  Rows of more than 16 vectors for each of 1024
+// threads (131072 16-bit logits) are read again for each pass.  Rows start
+// at any element: the 16-byte accesses need no alignment on this part, and
+// the last, partial vector of a row goes element by element.
+//
+// Membership of a token in the list is one bit per token in LDS.  The main
+// pass writes every dz_v as if v had no p_j; after a barrier the threads of
+// the listed entries write theirs again, adding the p of every entry with the
+// same index in list order, so equal indices need no atomics and all writers
+// of an element write the same bits.
+#include <math.h>
+
+#include <type_traits>
+
+#include "mbok_device.h"
+#include "mbok_launch.h"
+
+namespace mbok {
+namespace {
+
+constexpr int kMaxThreads = 1024;
+constexpr float kLn2 = 0.693147180559945309417f;
+
+typedef uint32_t u32x4_any __attribute__((ext_vector_type(4), aligned(2)));
+
+template <typename T>
+__device__ __forceinline__ float to_f32(T v);
+template <>
+__device__ __forceinline__ float to_f32<float>(float v) { return v; }
+template <>
+__device__ __forceinline__ float to_f32<_Float16>(_Float16 v) { return (float)v; }
+template <>
+__device__ __forceinline__ float to_f32<__bf16>(__bf16 v) { return (float)v; }
+
+// A 16-byte vector of logits as loaded.
+template <typename T>
+struct Vec {
+  static constexpr int N = 16 / (int)sizeof(T);
+  T v[N];
+};
+
+// Elements v N .. v N + N - 1 of a row of V; past the end -inf.
+template <typename T>
+__device__ __forceinline__ Vec<T> load_vec(const T* row, int v, int V) {
+  constexpr int N = Vec<T>::N;
+  if ((v + 1) * N <= V)
+    return __builtin_bit_cast(Vec<T>, *reinterpret_cast<const u32x4_any*>(row + v * N));
+  Vec<T> r;
+#pragma unroll
+  for (int e = 0; e < N; ++e) r.v[e] = v * N + e < V ? row[v * N + e] : (T)-INFINITY;
+  return r;
+}
+
+// Vec of the gradient: N values of OT for one vector of logits, 8 to 32 bytes.
+template <typename OT, int N>
+__device__ __forceinline__ void store_vec(OT* row, int v, int V, const float (&d)[N]) {
+  OT o[N];
+#pragma unroll
+  for (int e = 0; e < N; ++e) o[e] = (OT)d[e];
+  if ((v + 1) * N <= V) {
+    constexpr int W = N * (int)sizeof(OT) / 4;  // dwords: 2 or 4
+    typedef uint32_t words __attribute__((ext_vector_type(W)));
+    typedef uint32_t words_any __attribute__((ext_vector_type(W), aligned(2)));
+    words w;
+    __builtin_memcpy(&w, o, sizeof(w));
+    *reinterpret_cast<words_any*>(row + v * N) = w;
+    return;
+  }
+#pragma unroll
+  for (int e = 0; e < N; ++e)
+    if (v * N + e < V) row[v * N + e] = o[e];
+}
+
+struct Sum2 {
+  double a, b;
+};
+
+__device__ __forceinline__ float wave_max(float v) {
+#pragma unroll
+  for (int s = 32; s; s >>= 1) v = fmaxf(v, __shfl_xor(v, s));
+  return v;
+}
+__device__ __forceinline__ double wave_sum(double v) {
+#pragma unroll
+  for (int s = 32; s; s >>= 1) v += __shfl_xor(v, s);
+  return v;
+}
+
+// NaN if either is: fmaxf drops NaN, and a row with a NaN logit has no answer.
+__device__ __forceinline__ float nan_max(float a, float b) {
+  return (a != a || b != b) ? __builtin_nanf("") : fmaxf(a, b);
+}
+
+__device__ __forceinline__ float teacher_logit(const void* l, int dtype, int64_t i) {
+  if (dtype == MBOK_F32) return reinterpret_cast<const float*>(l)[i];
+  if (dtype == MBOK_F16) return (float)reinterpret_cast<const _Float16*>(l)[i];
+  return (float)reinterpret_cast<const __bf16*>(l)[i];
+}
+
+// Statistics of a row, as stats holds them
+struct RowStats {
+  float zmax;    // largest logit
+  float inv_s;   // 1 / sum exp((z - zmax) / tau)
+  float unlist;  // factor of q_v for unlisted v: 1 - p_r / q_r
+  float tmax;    // largest listed teacher logit (no t_lse)
+  float inv_n;   // 1 / sum exp((l - tmax) / tau); 0: no teacher weight
+  float pad[3];
+};
+static_assert(sizeof(RowStats) == MBOK_DISTILL_STATS * sizeof(float), "stats row");
+
+struct DistillRow {
+  int V, top;
+  float tau, c_hi, c_lo;  // log2(e) / tau as an fp32 pair
+};
+
+// exp((x - m) / tau) for the sums: the rounding of the scaled argument is
+// carried to first order, so the sum keeps fp32's accuracy.
+__device__ __forceinline__ float exp_sum(float d, const DistillRow& r) {
+  const float a = d * r.c_hi;
+  const float lo = fmaf(d, r.c_hi, -a) + d * r.c_lo;
+  const float e = __builtin_amdgcn_exp2f(a);
+  return a < -126.f ? 0.f : fmaf(e * kLn2, lo, e);
+}
+
+// The lists of one row in LDS: index (or -1), then p, then one bit per token.
+struct RowLds {
+  int* idx;
+  float* p;
+  uint32_t* bits;
+};
+
+__device__ __forceinline__ RowLds row_lds(void* base, int top) {
+  RowLds s;
+  s.idx = reinterpret_cast<int*>(base);
+  s.p = reinterpret_cast<float*>(s.idx + top);
+  s.bits = reinterpret_cast<uint32_t*>(s.p + top);
+  return s;
+}
+
+// Index of entry j, -1 where there is none
+__device__ __forceinline__ int entry_index(const int32_t* t_index, int64_t at, int V) {
+  const int v = t_index[at];
+  return v >= 0 && v < V ? v : -1;
+}
+
+// Sets the bits of the listed tokens; true for a thread that met a bit set
+// before (an index listed twice).  The bits were cleared before a barrier.
+__device__ __forceinline__ bool mark_entry(uint32_t* bits, int v) {
+  const uint32_t m = 1u << (v & 31);
+  return (atomicOr(&bits[v >> 5], m) & m) != 0;
+}
+
+// The gradient of the listed entries, after the main pass of the same
+// workgroup and a barrier: base scale A = w tau; q = exp((z - zmax) c) inv_s.
+template <typename ZT, typename OT>
+__device__ __forceinline__ void write_entries(const RowLds& s, const DistillRow& r,
+                                              const float* zl, OT* drow, const RowStats& st,
+                                              float A, bool twice) {
+  for (int j = threadIdx.x; j < r.top; j += blockDim.x) {
+    const int v = s.idx[j];
+    if (v < 0) continue;
+    float p = 0.f;
+    if (twice) {
+      for (int i = 0; i < r.top; ++i)
+        if (s.idx[i] == v) p += s.p[i];
+    } else {
+      p = s.p[j];
+    }
+    const float q = __builtin_amdgcn_exp2f((zl[j] - st.zmax) * r.c_hi) * st.inv_s;
+    drow[v] = (OT)((q - p) * A);
+  }
+}
+
+template <typename ZT, typename OT, int NV, bool GRAD>
+__global__ void __launch_bounds__(kMaxThreads) distill_kernel(
+    const ZT* Z, int64_t ldz, const void* __restrict__ t_logits, int t_dtype,
+    const int32_t* __restrict__ t_index, int64_t ldt, const float* __restrict__ t_lse,
+    const float* __restrict__ weight, DistillRow r, float* __restrict__ loss,
+    RowStats* __restrict__ stats, OT* dZ, int64_t lddz) {
+  constexpr int N = Vec<ZT>::N;
+  extern __shared__ __attribute__((aligned(16))) uint32_t smem[];
+  __shared__ float red_f[kMaxThreads / kWave];
+  __shared__ double red_d[2 * kMaxThreads / kWave];
+  __shared__ RowStats sh;
+  __shared__ int twice_any;
+  const int64_t t = blockIdx.x;
+  const int tid = threadIdx.x, nt = blockDim.x;
+  const int lane = tid & (kWave - 1), wave = tid / kWave, nw = nt / kWave;
+  const ZT* row = Z + t * ldz;
+  OT* drow = GRAD ? dZ + t * lddz : nullptr;
+  const float w = weight ? weight[t] : 1.f;
+  const int nvec = (r.V + N - 1) / N;
+
+  if (w == 0.f) {
+    if (GRAD) {
+      const float zero[N] = {};
+      for (int v = tid; v < nvec; v += nt) store_vec<OT, N>(drow, v, r.V, zero);
+    }
+    if (tid == 0) {
+      loss[t] = 0.f;
+      if (stats) stats[t] = RowStats{};
+    }
+    return;
+  }
+
+  // the row
+  Vec<ZT> held[NV > 0 ? NV : 1];
+  if (NV > 0) {
+#pragma unroll
+    for (int u = 0; u < NV; ++u) {
+      const int v = tid + u * nt;
+      if (v < nvec) held[u] = load_vec(row, v, r.V);
+    }
+  }
+  auto each = [&](auto&& f) {
+    if (NV > 0) {
+#pragma unroll
+      for (int u = 0; u < NV; ++u) {
+        const int v = tid + u * nt;
+        if (v < nvec) f(v, held[u]);
+      }
+    } else {
+      for (int v = tid; v < nvec; v += nt) f(v, load_vec(row, v, r.V));
+    }
+  };
+
+  // the lists: index, raw teacher logit (in p's place), student logit
+  const RowLds s = row_lds(smem, r.top);
+  const int nbits = (r.V + 31) / 32;
+  float* zl = reinterpret_cast<float*>(s.bits + nbits);
+  for (int i = tid; i < nbits; i += nt) s.bits[i] = 0u;
+  if (tid == 0) twice_any = 0;
+  for (int j = tid; j < r.top; j += nt) {
+    const int v = entry_index(t_index, t * ldt + j, r.V);
+    s.idx[j] = v;
+    s.p[j] = v < 0 ? -INFINITY : teacher_logit(t_logits, t_dtype, t * ldt + j);
+    zl[j] = v < 0 ? 0.f : to_f32(row[v]);
+  }
+
+  // largest logit
+  float mx = -INFINITY;
+  each([&](int, const Vec<ZT>& x) {
+#pragma unroll
+    for (int e = 0; e < N; ++e) mx = nan_max(mx, to_f32(x.v[e]));
+  });
+  const bool bad = mx != mx;
+  mx = wave_max(mx);
+  if (lane == 0) red_f[wave] = mx;
+  const bool nan_row = __syncthreads_or(bad) != 0;  // also: lists and cleared bits are in LDS
+  mx = red_f[0];
+  for (int i = 1; i < nw; ++i) mx = fmaxf(mx, red_f[i]);
+  if (nan_row) mx = __builtin_nanf("");
+
+  bool twice = false;
+  for (int j = tid; j < r.top; j += nt)
+    if (s.idx[j] >= 0) twice |= mark_entry(s.bits, s.idx[j]);
+  if (twice) twice_any = 1;
+  __syncthreads();
+
+  // sums of exponentials: all, and (with t_lse) the unlisted ones
+  float sa = 0.f, sr = 0.f;
+  const bool rest = t_lse != nullptr;
+  each([&](int v, const Vec<ZT>& x) {
+    uint32_t m = 0;
+    if (rest) m = s.bits[(v * N) >> 5] >> ((v * N) & 31);
+#pragma unroll
+    for (int e = 0; e < N; ++e) {
+      const float ex = exp_sum(to_f32(x.v[e]) - mx, r);
+      sa += ex;
+      if (rest) sr += (m >> e) & 1u ? 0.f : ex;
+    }
+  });
+  {
+    const double da = wave_sum((double)sa), dr = rest ? wave_sum((double)sr) : 0.0;
+    if (lane == 0) {
+      red_d[2 * wave] = da;
+      red_d[2 * wave + 1] = dr;
+    }
+  }
+  __syncthreads();
+
+  // the first wavefront: teacher, loss, statistics
+  if (wave == 0) {
+    double S = 0.0, R = 0.0;
+    for (int i = 0; i < nw; ++i) {
+      S += red_d[2 * i];
+      R += red_d[2 * i + 1];
+    }
+    const double inv_tau = 1.0 / (double)r.tau;
+    RowStats st = {};
+    st.zmax = mx;
+    st.inv_s = (float)(1.0 / S);
+    double log_n, shift, Nsum = 1.0;  // log p_j = (l_j - shift) / tau - log_n
+    if (rest) {
+      shift = 0.0;
+      log_n = (double)t_lse[t];
+      st.inv_n = 1.f;
+    } else {
+      float tm = -INFINITY;
+      for (int j = lane; j < r.top; j += kWave) tm = fmaxf(tm, s.p[j]);
+      tm = wave_max(tm);
+      st.tmax = tm;
+      Nsum = 0.0;
+      if (tm > -INFINITY)
+        for (int j = lane; j < r.top; j += kWave)
+          Nsum += (double)exp_sum(s.p[j] - tm, r);
+      Nsum = wave_sum(Nsum);
+      log_n = log(Nsum);
+      shift = (double)tm;
+      st.inv_n = Nsum > 0.0 ? (float)(1.0 / Nsum) : 0.f;
+    }
+    const double log_s = log(S);
+    double kl = 0.0, psum = 0.0;
+    if (st.inv_n > 0.f || rest) {
+      for (int j = lane; j < r.top; j += kWave) {
+        const float l = s.p[j];
+        double p;
+        double log_p = 0.0;
+        if (rest) {
+          log_p = (double)l * inv_tau - log_n;
+          p = exp(log_p);
+        } else {
+          log_p = ((double)l - shift) * inv_tau - log_n;
+          p = (double)exp_sum(l - st.tmax, r) / Nsum;
+        }
+        if (s.idx[j] < 0) p = 0.0;
+        s.p[j] = (float)p;
+        psum += p;
+        const double log_q = ((double)zl[j] - (double)mx) * inv_tau - log_s;
+        if (p > 0.0 || p != p) kl += p * (log_p - log_q);
+      }
+      kl = wave_sum(kl);
+      psum = wave_sum(psum);
+    } else {
+      for (int j = lane; j < r.top; j += kWave) s.p[j] = 0.f;
+      if (S != S) kl = S;
+    }
+    st.unlist = 1.f;
+    if (rest && R > 0.0) {
+      const double pr = fmax(0.0, 1.0 - psum), qr = R / S;
+      if (pr > 0.0) {
+        kl += pr * log(pr / qr);
+        st.unlist = (float)(1.0 - pr / qr);
+      }
+    }
+    if (lane == 0) {
+      loss[t] = (float)((double)w * (double)r.tau * (double)r.tau * kl);
+      sh = st;
+      if (stats) stats[t] = st;
+    }
+  }
+  if (!GRAD) return;
+  __syncthreads();
+
+  const RowStats st = sh;
+  const float A = w * r.tau;
+  const float Aq = st.inv_n > 0.f ? A * st.inv_s : 0.f;
+  const float Au = Aq * st.unlist;
+  each([&](int v, const Vec<ZT>& x) {
+    float d[N];
+#pragma unroll
+    for (int e = 0; e < N; ++e)
+      d[e] = __builtin_amdgcn_exp2f((to_f32(x.v[e]) - mx) * r.c_hi) * Au;
+    store_vec<OT, N>(drow, v, r.V, d);
+  });
+  __syncthreads();
+  if (st.inv_n > 0.f)
+    write_entries<ZT, OT>(s, r, zl, drow, st, A, twice_any != 0);
+}
+
+template <typename ZT, typename OT>
+__global__ void __launch_bounds__(kMaxThreads) distill_backward_kernel(
+    const ZT* Z, int64_t ldz, const void* __restrict__ t_logits, int t_dtype,
+    const int32_t* __restrict__ t_index, int64_t ldt, const float* __restrict__ t_lse,
+    const float* __restrict__ weight, DistillRow r, const RowStats* __restrict__ stats,
+    const float* __restrict__ dloss, OT* dZ, int64_t lddz) {
+  constexpr int N = Vec<ZT>::N;
+  extern __shared__ __attribute__((aligned(16))) uint32_t smem[];
+  __shared__ int twice_any;
+  const int64_t t = blockIdx.x;
+  const int tid = threadIdx.x, nt = blockDim.x;
+  const ZT* row = Z + t * ldz;
+  OT* drow = dZ + t * lddz;
+  const float w = (weight ? weight[t] : 1.f), dl = dloss[t];
+  const int nvec = (r.V + N - 1) / N;
+  if (w == 0.f || dl == 0.f) {
+    const float zero[N] = {};
+    for (int v = tid; v < nvec; v += nt) store_vec<OT, N>(drow, v, r.V, zero);
+    return;
+  }
+  const RowStats st = stats[t];
+  const RowLds s = row_lds(smem, r.top);
+  const int nbits = (r.V + 31) / 32;
+  float* zl = reinterpret_cast<float*>(s.bits + nbits);
+  for (int i = tid; i < nbits; i += nt) s.bits[i] = 0u;
+  if (tid == 0) twice_any = 0;
+  __syncthreads();
+  bool twice = false;
+  for (int j = tid; j < r.top; j += nt) {
+    const int v = entry_index(t_index, t * ldt + j, r.V);
+    s.idx[j] = v;
+    float p = 0.f;
+    if (v >= 0) {
+      const float l = teacher_logit(t_logits, t_dtype, t * ldt + j);
+      p = t_lse ? (float)exp((double)l / (double)r.tau - (double)t_lse[t])
+                : exp_sum(l - st.tmax, r) * st.inv_n;
+      if (!(st.inv_n > 0.f)) p = 0.f;
+      zl[j] = to_f32(row[v]);
+      twice |= mark_entry(s.bits, v);
+    }
+    s.p[j] = p;
+  }
+  if (twice) twice_any = 1;
+  __syncthreads();
+  const float A = w * r.tau * dl;
+  const float Aq = st.inv_n > 0.f ? A * st.inv_s : 0.f;
+  const float Au = Aq * st.unlist;
+  for (int v = tid; v < nvec; v += nt) {
+    const Vec<ZT> x = load_vec(row, v, r.V);
+    float d[N];
+#pragma unroll
+    for (int e = 0; e < N; ++e)
+      d[e] = __builtin_amdgcn_exp2f((to_f32(x.v[e]) - st.zmax) * r.c_hi) * Au;
+    store_vec<OT, N>(drow, v, r.V, d);
+  }
+  __syncthreads();
+  if (st.inv_n > 0.f)
+    write_entries<ZT, OT>(s, r, zl, drow, st, A, twice_any != 0);
+}
+
+DistillRow row_of(const mbok_distill_desc* d) {
+  const double c = 1.4426950408889634074 / (double)d->temperature;
+  const float hi = (float)c;
+  return DistillRow{d->vocab, d->top, d->temperature, hi, (float)(c - (double)hi)};
+}
+
+size_t row_lds_bytes(const mbok_distill_desc* d) {
+  return ((size_t)d->top * 3 + ((size_t)d->vocab + 31) / 32) * 4;
+}
+
+template <typename ZT, typename OT>
+int launch_rows(const mbok_distill_desc* d, const DistillArgs& a, float* loss, float* stats,
+                hipStream_t stream) {
+  const int nvec = (d->vocab + Vec<ZT>::N - 1) / Vec<ZT>::N;
+  const size_t lds = row_lds_bytes(d);
+  const DistillRow r = row_of(d);
+  int threads = 256;
+  while (threads < kMaxThreads && threads * 8 < nvec) threads *= 2;
+  const int per = (nvec + threads - 1) / threads;
+  auto go = [&](auto kernel) {
+    hipLaunchKernelGGL(kernel, dim3((unsigned)a.T), dim3(threads), lds, stream,
+                       reinterpret_cast<const ZT*>(a.Z), a.ldz, a.t_logits, a.t_dtype, a.t_index,
+                       a.ldt, a.t_lse, a.weight, r, loss, reinterpret_cast<RowStats*>(stats),
+                       reinterpret_cast<OT*>(a.dZ), a.lddz);
+  };
+  auto by_nv = [&](auto grad) {
+    constexpr bool G = decltype(grad)::value;
+    if (per <= 2) go(distill_kernel<ZT, OT, 2, G>);
+    else if (per <= 4) go(distill_kernel<ZT, OT, 4, G>);
+    else if (per <= 8) go(distill_kernel<ZT, OT, 8, G>);
+    else if (per <= 16) go(distill_kernel<ZT, OT, 16, G>);
+    else go(distill_kernel<ZT, OT, 0, G>);
+  };
+  if (a.dZ) by_nv(std::true_type{});
+  else by_nv(std::false_type{});
+  return hipGetLastError() == hipSuccess ? MBOK_OK : MBOK_ERR_HIP;
+}
+
+template <typename ZT, typename OT>
+int launch_rows_backward(const mbok_distill_desc* d, const DistillArgs& a, const float* stats,
+                         const float* dloss, hipStream_t stream) {
+  const int nvec = (d->vocab + Vec<ZT>::N - 1) / Vec<ZT>::N;
+  int threads = 256;
+  while (threads < kMaxThreads && threads * 4 < nvec) threads *= 2;
+  hipLaunchKernelGGL((distill_backward_kernel<ZT, OT>), dim3((unsigned)a.T), dim3(threads),
+                     row_lds_bytes(d), stream, reinterpret_cast<const ZT*>(a.Z), a.ldz,
+                     a.t_logits, a.t_dtype, a.t_index, a.ldt, a.t_lse, a.weight, row_of(d),
+                     reinterpret_cast<const RowStats*>(stats), dloss,
+                     reinterpret_cast<OT*>(a.dZ), a.lddz);
+  return hipGetLastError() == hipSuccess ? MBOK_OK : MBOK_ERR_HIP;
+}
+
+// calls f with the logit and gradient types of the call
+template <typename F>
+int by_types(const DistillArgs& a, F&& f) {
+  const bool same = !a.dZ || a.dz_dtype == a.z_dtype;
+  switch (a.z_dtype) {
+    case MBOK_F32: return same ? f(float{}, float{}) : f(float{}, __bf16{});
+    case MBOK_F16: return same ? f(_Float16{}, _Float16{}) : f(_Float16{}, __bf16{});
+    default: return f(__bf16{}, __bf16{});
+  }
+}
+
+}  // namespace
+
+int launch_distill(const mbok_distill_desc* d, const DistillArgs& a, float* loss, float* stats,
+                   hipStream_t stream) {
+  return by_types(a, [&](auto z, auto o) {
+    return launch_rows<decltype(z), decltype(o)>(d, a, loss, stats, stream);
+  });
+}
+
+int launch_distill_backward(const mbok_distill_desc* d, const DistillArgs& a, const float* stats,
+                            const float* dloss, hipStream_t stream) {
+  return by_types(a, [&](auto z, auto o) {
+    return launch_rows_backward<decltype(z), decltype(o)>(d, a, stats, dloss, stream);
+  });
+}
+
+}  // namespace mbok

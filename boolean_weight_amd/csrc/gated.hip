@@ -1,0 +1,87 @@
+// The gated feed-forward block's entry points below the C ABI: the forward's
+// dispatch and the backward pass (gfx950).
+//
+// With H = act(g) (.) u and s the gradient of H:
+//     dg = s u act'(g),  du = s act(g),  dX = dg Wg + du Wu.
+// The first two are one pass over pre and dH (bound by memory: 2 + 1 values
+// read and 2 written per output); dX is the transposed product of the stacked
+// layer, whose rows are the columns of dpre = (dg, du) in the stacked order.
+// dg and du are rounded to bf16 once: they are the matrix-core operand of dX
+// and of the scale gradients, and the gradients a caller keeps.
+#include "mbok_device.h"
+#include "mbok_gated.h"
+#include "mbok_launch.h"
+
+namespace mbok {
+namespace {
+
+typedef __attribute__((ext_vector_type(4))) uint32_t u32x4;
+typedef __attribute__((ext_vector_type(4), aligned(2))) uint32_t u32x4_any;  // dH rows start anywhere
+
+__device__ __forceinline__ float lane_value(const u32x4& v, int e) {
+  return bf16_bits_to_f32((e & 1) ? v[e >> 1] >> 16 : v[e >> 1] & 0xffffu);
+}
+
+// One thread: 8 outputs of one token, i.e. one 16-column tile of pre and dpre.
+__global__ void __launch_bounds__(256) gated_backward_kernel(
+    const uint16_t* pre, int64_t ldpre, const uint16_t* __restrict__ dH, int64_t lddh,
+    uint16_t* dpre, int64_t lddpre, int m, int64_t items, int act) {
+  const int tiles = (m + 7) / 8;
+  const int64_t idx = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (idx >= items) return;
+  const int64_t t = idx / tiles;
+  const int tile = (int)(idx - t * tiles);
+  const u32x4* p = reinterpret_cast<const u32x4*>(pre + t * ldpre + 16 * tile);
+  const u32x4 gv = p[0], uv = p[1];
+  const uint16_t* h = dH + t * lddh + 8 * tile;
+  const int live = min(8, m - 8 * tile);
+  u32x4 sv;
+  if (live == 8) {
+    sv = *reinterpret_cast<const u32x4_any*>(h);
+  } else {
+    uint32_t e[8];
+#pragma unroll
+    for (int c = 0; c < 8; ++c) e[c] = c < live ? h[c] : 0u;
+    sv = u32x4{e[0] | e[1] << 16, e[2] | e[3] << 16, e[4] | e[5] << 16, e[6] | e[7] << 16};
+  }
+  uint32_t dg[8], du[8];
+#pragma unroll
+  for (int c = 0; c < 8; ++c) {
+    const float s = lane_value(sv, c), g = lane_value(gv, c), u = lane_value(uv, c);
+    float slope;
+    const float a = activation<true>(act, g, slope);
+    dg[c] = c < live ? to_bf16(s * u * slope) : 0u;
+    du[c] = c < live ? to_bf16(s * a) : 0u;
+  }
+  u32x4* o = reinterpret_cast<u32x4*>(dpre + t * lddpre + 16 * tile);
+  o[0] = u32x4{dg[0] | dg[1] << 16, dg[2] | dg[3] << 16, dg[4] | dg[5] << 16, dg[6] | dg[7] << 16};
+  o[1] = u32x4{du[0] | du[1] << 16, du[2] | du[3] << 16, du[4] | du[5] << 16, du[6] | du[7] << 16};
+}
+
+}  // namespace
+
+int launch_gated(const mbok_desc* d, const void* packed, const void* X, int64_t T, int64_t ldx,
+                 int act, void* H, int64_t ldh, void* pre, int64_t ldpre, hipStream_t stream) {
+  const mbok_desc stacked = gated_stacked(d);
+  const GatedOut out = {reinterpret_cast<uint16_t*>(H), ldh, reinterpret_cast<uint16_t*>(pre),
+                        ldpre, d->m, act};
+  return launch_gated_stacked(&stacked, packed, X, T, ldx, out, stream);
+}
+
+int launch_gated_backward(const mbok_desc* d, const void* packed, const void* pre, int64_t ldpre,
+                          const void* dH, int64_t lddh, int64_t T, int act, void* dpre,
+                          int64_t lddpre, void* dX, int64_t lddx, void* ws, hipStream_t stream) {
+  const int64_t items = T * ((d->m + 7) / 8);
+  const int64_t blocks = (items + 255) / 256;
+  if (blocks > 0x7fffffff) return MBOK_ERR_SHAPE;
+  hipLaunchKernelGGL(gated_backward_kernel, dim3((unsigned)blocks), dim3(256), 0, stream,
+                     reinterpret_cast<const uint16_t*>(pre), ldpre,
+                     reinterpret_cast<const uint16_t*>(dH), lddh,
+                     reinterpret_cast<uint16_t*>(dpre), lddpre, d->m, items, act);
+  if (hipGetLastError() != hipSuccess) return MBOK_ERR_HIP;
+  if (!dX) return MBOK_OK;
+  const mbok_desc stacked = gated_stacked(d);
+  return launch_gemmt(&stacked, packed, dpre, T, lddpre, dX, lddx, ws, stream);
+}
+
+}  // namespace mbok

@@ -27,18 +27,15 @@
 #include <string.h>
 
 #include <atomic>
+#include <type_traits>
 
 #include "mbok_device.h"
+#include "mbok_gated.h"
 #include "mbok_launch.h"
+#include "mbok_levels.h"
 
 namespace mbok {
 namespace {
-
-typedef __attribute__((ext_vector_type(8))) __bf16 bf16x8;
-typedef __attribute__((ext_vector_type(16))) float f32x16;
-// a native vector type keeps the activation staging in registers (a uint4
-// struct member went through scratch memory)
-typedef __attribute__((ext_vector_type(4))) uint32_t u32x4;
 
 constexpr int BT = 256;         // tokens per workgroup tile
 constexpr int BN = 256;         // output rows per workgroup tile
@@ -46,116 +43,6 @@ constexpr int BK = 64;          // input columns per step
 constexpr int LDS_STRIDE = 72;  // bf16 elements per LDS row (64 + 8 padding)
 constexpr int TILE_ELEMS = 256 * LDS_STRIDE;
 constexpr int GEMM_THREADS = 256;
-
-__device__ __forceinline__ uint32_t bf16_pair(float a, float b) {
-  const __bf16 ha = (__bf16)a, hb = (__bf16)b;  // nearest-even
-  return (uint32_t)__builtin_bit_cast(uint16_t, ha) |
-         ((uint32_t)__builtin_bit_cast(uint16_t, hb) << 16);
-}
-
-// Byte-planar bf16 levels of one (row, group): lo_a/hi_a hold the low/high
-// bytes of levels 0..3, lo_b/hi_b of levels 4..7.  Level index bit k-1 is the
-// sign bit of kernel k (1 = +alpha_k).
-struct Levels {
-  uint32_t lo_a, lo_b, hi_a, hi_b;
-};
-
-// What is left of an fp32 value after its rounding to bf16.  The difference
-// is exact in fp32 (it is v's own low significand bits) and at most half a
-// bf16 ulp of v, so hi + bf16(lo) carries 16 significant bits of v.
-__device__ __forceinline__ float bf16_residue(float v) { return v - (float)(__bf16)v; }
-
-// LO = false: the levels rounded to bf16 (the default product).  LO = true:
-// the bf16 rounding of each level's residue, for the second pass of the
-// two-pass product (hi + lo levels, ~2^-16 relative error per weight).
-template <int K, bool LO = false>
-__device__ __forceinline__ Levels make_levels(const float* a) {
-  float l[8];
-#pragma unroll
-  for (int idx = 0; idx < 8; ++idx) {
-    float v = (idx & 1) ? a[0] : -a[0];
-    if (K >= 2) v += (idx & 2) ? a[1] : -a[1];
-    if (K >= 3) v += (idx & 4) ? a[2] : -a[2];
-    l[idx] = LO ? bf16_residue(v) : v;
-  }
-  const uint32_t p01 = bf16_pair(l[0], l[1]), p23 = bf16_pair(l[2], l[3]);
-  const uint32_t p45 = bf16_pair(l[4], l[5]), p67 = bf16_pair(l[6], l[7]);
-  Levels L;
-  // v_perm_b32(s0, s1, sel): selector byte 0..3 picks s1 bytes, 4..7 s0 bytes
-  L.lo_a = __builtin_amdgcn_perm(p23, p01, 0x06040200u);
-  L.hi_a = __builtin_amdgcn_perm(p23, p01, 0x07050301u);
-  L.lo_b = __builtin_amdgcn_perm(p67, p45, 0x06040200u);
-  L.hi_b = __builtin_amdgcn_perm(p67, p45, 0x07050301u);
-  return L;
-}
-
-// Unpack one 32-column sign word per kernel (w[k]) into 32 bf16 weights in
-// natural column order: out[2q], out[2q+1] hold columns 4q..4q+3.
-template <int K>
-__device__ __forceinline__ void unpack_word(const uint32_t* w, const Levels& L, uint32_t* out) {
-  constexpr uint32_t M = 0x11111111u;
-#pragma unroll
-  for (int b = 0; b < 4; ++b) {
-    // nibble j = 2e + a of V holds the level index of quad q = 4a + b, element e
-    uint32_t V = (w[0] >> b) & M;
-    if (K >= 2) V |= ((w[1] >> b) & M) << 1;
-    if (K >= 3) V |= ((w[2] >> b) & M) << 2;
-#pragma unroll
-    for (int a = 0; a < 2; ++a) {
-      const int q = 4 * a + b;
-      const uint32_t sel = (a ? (V >> 4) : V) & 0x0f0f0f0fu;
-      const uint32_t lo = __builtin_amdgcn_perm(L.lo_b, L.lo_a, sel);
-      const uint32_t hi = __builtin_amdgcn_perm(L.hi_b, L.hi_a, sel);
-      out[2 * q] = __builtin_amdgcn_perm(hi, lo, 0x05010400u);
-      out[2 * q + 1] = __builtin_amdgcn_perm(hi, lo, 0x07030602u);
-    }
-  }
-}
-
-// K = 4 (16 levels): direct fp32 sums, then bf16 (LO: their residues).
-template <bool LO = false>
-__device__ __forceinline__ void unpack_word_k4(const uint32_t* w, const float* a, uint32_t* out) {
-#pragma unroll
-  for (int q = 0; q < 8; ++q) {
-    float v[4];
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      float s = 0.f;
-#pragma unroll
-      for (int k = 0; k < 4; ++k) s += ((w[k] >> (8 * e + q)) & 1u) ? a[k] : -a[k];
-      v[e] = LO ? bf16_residue(s) : s;
-    }
-    out[2 * q] = bf16_pair(v[0], v[1]);
-    out[2 * q + 1] = bf16_pair(v[2], v[3]);
-  }
-}
-
-// Selector words of one 32-column sign word per kernel: V[b] nibble 2e + a is
-// the level index of quad q = 4a + b, element e (see unpack_word).
-template <int K>
-__device__ __forceinline__ void word_selectors(const uint32_t* w, uint32_t* V) {
-  constexpr uint32_t M = 0x11111111u;
-#pragma unroll
-  for (int b = 0; b < 4; ++b) {
-    uint32_t v = (w[0] >> b) & M;
-    if (K >= 2) v |= ((w[1] >> b) & M) << 1;
-    if (K >= 3) v |= ((w[2] >> b) & M) << 2;
-    V[b] = v;
-  }
-}
-
-// Quads 4a .. 4a+3 of a word (16 columns 16a .. 16a+15) as 8 bf16 pairs.
-__device__ __forceinline__ void unpack_quads(const uint32_t* V, int a, const Levels& L,
-                                             uint32_t* out) {
-#pragma unroll
-  for (int b = 0; b < 4; ++b) {
-    const uint32_t sel = (a ? (V[b] >> 4) : V[b]) & 0x0f0f0f0fu;
-    const uint32_t lo = __builtin_amdgcn_perm(L.lo_b, L.lo_a, sel);
-    const uint32_t hi = __builtin_amdgcn_perm(L.hi_b, L.hi_a, sel);
-    out[2 * b] = __builtin_amdgcn_perm(hi, lo, 0x05010400u);
-    out[2 * b + 1] = __builtin_amdgcn_perm(hi, lo, 0x07030602u);
-  }
-}
 
 // Output element of a tile: the first pass (or the one-pass product) stores
 // its sum; the residue pass adds its sum to what the first pass stored.
@@ -378,29 +265,23 @@ __global__ void __launch_bounds__(GEMM_THREADS) gemm_mfma_kernel(
 // covers 32 rows, and the final round takes about half as long.
 constexpr int GEMM8_THREADS = 512;
 
-__device__ __forceinline__ void unpack_two_quads(const uint32_t* V, int a, int b0, const Levels& L,
-                                                 uint32_t* out) {
-#pragma unroll
-  for (int bb = 0; bb < 2; ++bb) {
-    const int b = b0 + bb;
-    const uint32_t sel = (a ? (V[b] >> 4) : V[b]) & 0x0f0f0f0fu;
-    const uint32_t lo = __builtin_amdgcn_perm(L.lo_b, L.lo_a, sel);
-    const uint32_t hi = __builtin_amdgcn_perm(L.hi_b, L.hi_a, sel);
-    out[2 * bb] = __builtin_amdgcn_perm(hi, lo, 0x05010400u);
-    out[2 * bb + 1] = __builtin_amdgcn_perm(hi, lo, 0x07030602u);
-  }
-}
-
 // The body of one workgroup: JB = 2 for a whole 256-row tile, 1 for one
 // 128-row half of a tile of the partial final round (a compile-time constant,
 // so the loop has no branches on it).
-template <typename AT, int K, int JB, bool LO>
+//
+// Out is how the tile is stored.  With GatedOut the layer is the gated block's
+// stacked one, whose 16-row tiles hold 8 gate rows and the same 8 up rows:
+// the unpacking thread of stacked row 64 b + 16 u + 8 h + r writes its weights
+// to LDS row 64 b + 32 h + 8 u + r, so that a wavefront's two 32-row blocks are
+// 32 gate rows and the same 32 up rows, and a lane holds both values of an
+// output.
+template <typename AT, int K, int JB, bool LO, typename Out>
 __device__ __forceinline__ void mfma8_tile(const uint32_t* __restrict__ bits,
                                            const AT* __restrict__ scales,
                                            const uint16_t* __restrict__ X, int64_t ldx,
-                                           float* __restrict__ Y, int64_t ldy, int T, int m,
-                                           int m_pad, int G, int ntx, int tile, int half,
-                                           uint16_t* smem) {
+                                           const Out& out, int T, int m, int m_pad, int G,
+                                           int ntx, int tile, int half, uint16_t* smem) {
+  constexpr bool GATED = std::is_same<Out, GatedOut>::value;
   // buffer b: activations at smem + 2b * TILE_ELEMS, weights right after
   const int tid = threadIdx.x;
   const int lane = tid & 63;
@@ -421,9 +302,12 @@ __device__ __forceinline__ void mfma8_tile(const uint32_t* __restrict__ bits,
   // n0 + tid/4, columns 16 (tid % 4) .., so that every wavefront unpacks)
   constexpr int TPR = JB == 2 ? 2 : 4;
   static_assert(GEMM8_THREADS / TPR == tile_rows, "one row per TPR threads");
-  const int urow = tid / TPR, upart = tid % TPR;
+  const int trow = tid / TPR, upart = tid % TPR;
   const int uword = JB == 2 ? upart : upart >> 1;  // 32-column word of the step
-  const int row = n0 + urow;
+  const int row = n0 + trow;
+  // LDS row of the thread's weights
+  const int urow = GATED ? (trow & ~63) + 32 * ((trow >> 3) & 1) + 8 * ((trow >> 4) & 3) + (trow & 7)
+                         : trow;
   const int rowc = row < m_pad ? row : m_pad - 1;
   const uint32_t row_chunk = (uint32_t)(rowc / kRowBlock) * (uint32_t)(G * K * kRowBlock) +
                              (uint32_t)(rowc % kRowBlock);
@@ -592,37 +476,37 @@ __device__ __forceinline__ void mfma8_tile(const uint32_t* __restrict__ bits,
 
   // C layout: lane l, register r -> token 8(r/4) + 4(l/32) + r%4, row l%32
 #pragma unroll
-  for (int i = 0; i < TI; ++i)
-#pragma unroll
-    for (int j = 0; j < TJ; ++j) {
-      const int n = n0 + wn * 32 * TJ + j * 32 + lrow;
-      if (n >= m) continue;
+  for (int i = 0; i < TI; ++i) {
+    const int tb = t0 + wt * 32 * TI + i * 32 + 4 * (lane >> 5);
+    if constexpr (GATED) {
+      const int orow = (n0 + wn * 32 * TJ) / 2 + lrow;  // the output of the lane's pair
+      if (orow >= m / 2) continue;
 #pragma unroll
       for (int r = 0; r < 16; ++r) {
-        const int t = t0 + wt * 32 * TI + i * 32 + 8 * (r >> 2) + 4 * (lane >> 5) + (r & 3);
-        if (t < T) store_out<LO>(Y + (int64_t)t * ldy + n, acc[i][j][r]);
+        const int t = tb + 8 * (r >> 2) + (r & 3);
+        if (t < T) out.put(t, orow, acc[i][0][r], acc[i][1][r]);
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < TJ; ++j) {
+        const int n = n0 + wn * 32 * TJ + j * 32 + lrow;
+        if (n >= m) continue;
+#pragma unroll
+        for (int r = 0; r < 16; ++r) {
+          const int t = tb + 8 * (r >> 2) + (r & 3);
+          if (t < T) store_out<LO>(out.y + (int64_t)t * out.ldy + n, acc[i][j][r]);
+        }
       }
     }
+  }
 }
 
-// Tile at position p of the XCD-blocked order: pairs of token tiles, sweeping
-// the row tiles (p -> token tile 2q + d, row tile tx), the last token tile
-// alone when their count is odd.  Workgroup b runs on XCD b % 8, so giving
-// XCD x the positions x * nfull / 8 .. of the full round puts ~16 row tiles
-// x 2 token tiles on each XCD: its L2 holds those activations and weights
-// instead of every XCD streaming every token tile.
-__device__ __forceinline__ int tile_at(int p, int ntx, int nty) {
-  const int q = p / (2 * ntx);
-  const int rem = p - q * 2 * ntx;
-  if (2 * q + 1 < nty) return (2 * q + (rem & 1)) * ntx + (rem >> 1);
-  return 2 * q * ntx + rem;
-}
-
-template <typename AT, int K, bool LO>
-__global__ void __launch_bounds__(GEMM8_THREADS) gemm_mfma8_kernel(
-    const uint32_t* __restrict__ bits, const AT* __restrict__ scales,
-    const uint16_t* __restrict__ X, int64_t ldx, float* __restrict__ Y, int64_t ldy, int T, int m,
-    int m_pad, int G, int ntx, int nfull, int xcd_order) {
+template <typename AT, int K, bool LO, typename Out>
+__device__ __forceinline__ void mfma8_body(const uint32_t* __restrict__ bits,
+                                           const AT* __restrict__ scales,
+                                           const uint16_t* __restrict__ X, int64_t ldx,
+                                           const Out& out, int T, int m, int m_pad, int G,
+                                           int ntx, int nfull, int xcd_order) {
   extern __shared__ __attribute__((aligned(16))) uint16_t smem[];
   const int b = blockIdx.x;
   const int nty = (T + BT - 1) / BT;
@@ -630,13 +514,31 @@ __global__ void __launch_bounds__(GEMM8_THREADS) gemm_mfma8_kernel(
     int p = b;
     if (xcd_order && (nfull & 7) == 0) p = (b & 7) * (nfull >> 3) + (b >> 3);
     const int tile = xcd_order ? tile_at(p, ntx, nty) : p;
-    mfma8_tile<AT, K, 2, LO>(bits, scales, X, ldx, Y, ldy, T, m, m_pad, G, ntx, tile, 0, smem);
+    mfma8_tile<AT, K, 2, LO>(bits, scales, X, ldx, out, T, m, m_pad, G, ntx, tile, 0, smem);
   } else {
     const int p = nfull + ((b - nfull) >> 1);
     const int tile = xcd_order ? tile_at(p, ntx, nty) : p;
-    mfma8_tile<AT, K, 1, LO>(bits, scales, X, ldx, Y, ldy, T, m, m_pad, G, ntx, tile,
-                         (b - nfull) & 1, smem);
+    mfma8_tile<AT, K, 1, LO>(bits, scales, X, ldx, out, T, m, m_pad, G, ntx, tile,
+                             (b - nfull) & 1, smem);
   }
+}
+
+template <typename AT, int K, bool LO>
+__global__ void __launch_bounds__(GEMM8_THREADS) gemm_mfma8_kernel(
+    const uint32_t* __restrict__ bits, const AT* __restrict__ scales,
+    const uint16_t* __restrict__ X, int64_t ldx, float* __restrict__ Y, int64_t ldy, int T, int m,
+    int m_pad, int G, int ntx, int nfull, int xcd_order) {
+  mfma8_body<AT, K, LO>(bits, scales, X, ldx, RowsOut{Y, ldy, m}, T, m, m_pad, G, ntx, nfull,
+                        xcd_order);
+}
+
+// the gated feed-forward block; m is the stacked layer's
+template <typename AT, int K>
+__global__ void __launch_bounds__(GEMM8_THREADS) gated_mfma8_kernel(
+    const uint32_t* __restrict__ bits, const AT* __restrict__ scales,
+    const uint16_t* __restrict__ X, int64_t ldx, GatedOut out, int T, int m, int m_pad, int G,
+    int ntx, int nfull, int xcd_order) {
+  mfma8_body<AT, K, false>(bits, scales, X, ldx, out, T, m, m_pad, G, ntx, nfull, xcd_order);
 }
 
 // Compute units of the current device (queried once per device; host
@@ -664,7 +566,8 @@ int gemm_xcd_order() {
 
 template <typename AT, int K, bool LO>
 void launch_mfma8_k(const Geom& geo, const uint32_t* bits, const AT* scales, const uint16_t* Xb,
-                    int64_t T, int64_t ldx, float* Y, int64_t ldy, hipStream_t stream) {
+                    int64_t T, int64_t ldx, float* Y, int64_t ldy, hipStream_t stream,
+                    const GatedOut* gated = nullptr) {
   const size_t lds = 4 * TILE_ELEMS * sizeof(uint16_t);
   const int ntx = (geo.m + BN - 1) / BN;
   const int64_t ntiles = (int64_t)ntx * ((T + BT - 1) / BT);
@@ -672,6 +575,14 @@ void launch_mfma8_k(const Geom& geo, const uint32_t* bits, const AT* scales, con
   const int ncu = compute_units();
   const int64_t rem = ntiles % ncu;
   const int64_t nfull = ntiles - rem;
+  if constexpr (!LO) {
+    if (gated) {
+      hipLaunchKernelGGL((gated_mfma8_kernel<AT, K>), dim3((unsigned)(nfull + 2 * rem)),
+                         dim3(GEMM8_THREADS), lds, stream, bits, scales, Xb, ldx, *gated, (int)T,
+                         geo.m, geo.RB * kRowBlock, geo.G, ntx, (int)nfull, gemm_xcd_order());
+      return;
+    }
+  }
   hipLaunchKernelGGL((gemm_mfma8_kernel<AT, K, LO>), dim3((unsigned)(nfull + 2 * rem)),
                      dim3(GEMM8_THREADS), lds, stream, bits, scales, Xb, ldx, Y, ldy, (int)T,
                      geo.m, geo.RB * kRowBlock, geo.G, ntx, (int)nfull, gemm_xcd_order());
@@ -679,16 +590,16 @@ void launch_mfma8_k(const Geom& geo, const uint32_t* bits, const AT* scales, con
 
 template <typename AT, bool LO>
 void launch_mfma8(const Geom& geo, const void* packed, const void* X, int64_t T, int64_t ldx,
-                  float* Y, int64_t ldy, hipStream_t stream) {
+                  float* Y, int64_t ldy, hipStream_t stream, const GatedOut* gated = nullptr) {
   const uint32_t* bits = reinterpret_cast<const uint32_t*>(packed);
   const AT* scales = reinterpret_cast<const AT*>(reinterpret_cast<const char*>(packed) +
                                                  geo.bits_bytes);
   const uint16_t* Xb = reinterpret_cast<const uint16_t*>(X);
   switch (geo.K) {
-    case 1: launch_mfma8_k<AT, 1, LO>(geo, bits, scales, Xb, T, ldx, Y, ldy, stream); break;
-    case 2: launch_mfma8_k<AT, 2, LO>(geo, bits, scales, Xb, T, ldx, Y, ldy, stream); break;
-    case 3: launch_mfma8_k<AT, 3, LO>(geo, bits, scales, Xb, T, ldx, Y, ldy, stream); break;
-    default: launch_mfma8_k<AT, 4, LO>(geo, bits, scales, Xb, T, ldx, Y, ldy, stream); break;
+    case 1: launch_mfma8_k<AT, 1, LO>(geo, bits, scales, Xb, T, ldx, Y, ldy, stream, gated); break;
+    case 2: launch_mfma8_k<AT, 2, LO>(geo, bits, scales, Xb, T, ldx, Y, ldy, stream, gated); break;
+    case 3: launch_mfma8_k<AT, 3, LO>(geo, bits, scales, Xb, T, ldx, Y, ldy, stream, gated); break;
+    default: launch_mfma8_k<AT, 4, LO>(geo, bits, scales, Xb, T, ldx, Y, ldy, stream, gated); break;
   }
 }
 
@@ -781,6 +692,18 @@ TokenKernel token_kernel(const mbok_desc* d, int64_t T) {
   return kTokSkinny;
 }
 
+// the gated block's kernel by the same rule (d: the stacked layer); its
+// one-token form is always the matrix-core decode kernel
+int launch_gated_stacked(const mbok_desc* d, const void* packed, const void* X, int64_t T,
+                         int64_t ldx, const GatedOut& out, hipStream_t stream) {
+  if (T > skinny_max_tokens()) return launch_gated_mfma(d, packed, X, T, ldx, out, stream);
+  if (T == 1) return launch_gated_f4(d, packed, X, T, ldx, out, stream);
+  if ((T - 1) * ldx + d->n <= INT32_MAX && token_kernel(d, T) != kTokSkinny &&
+      T <= gated_f4_max_tokens())
+    return launch_gated_f4(d, packed, X, T, ldx, out, stream);
+  return launch_gated_skinny(d, packed, X, T, ldx, out, stream);
+}
+
 int launch_gemm(const mbok_desc* d, const void* packed, const void* X, int64_t T, int64_t ldx,
                 float* Y, int64_t ldy, int passes, hipStream_t stream) {
   const Geom geo = make_geom(d);
@@ -797,6 +720,30 @@ int launch_gemm(const mbok_desc* d, const void* packed, const void* X, int64_t T
   if (d->alpha_dtype == MBOK_F16)
     return launch_mfma<uint16_t>(geo, packed, X, T, ldx, Y, ldy, passes, stream);
   return launch_mfma<float>(geo, packed, X, T, ldx, Y, ldy, passes, stream);
+}
+
+// T > 16 rows of the gated block (d: the stacked layer).  The kernel indexes
+// activations with 32-bit offsets, so very long inputs go in several launches
+// of whole token tiles.
+int launch_gated_mfma(const mbok_desc* d, const void* packed, const void* X, int64_t T,
+                      int64_t ldx, const GatedOut& out, hipStream_t stream) {
+  const Geom geo = make_geom(d);
+  if (geo.bits_bytes / 4 >= (int64_t(1) << 32)) return MBOK_ERR_SHAPE;
+  int64_t chunk = ((int64_t(1) << 32) - 1) / ldx / BT * BT;
+  if (chunk < BT) return MBOK_ERR_INVALID_ARG;
+  for (int64_t t = 0; t < T; t += chunk) {
+    const int64_t rows = T - t < chunk ? T - t : chunk;
+    const uint16_t* x = reinterpret_cast<const uint16_t*>(X) + t * ldx;
+    GatedOut o = out;
+    o.H += t * out.ldh;
+    if (o.pre) o.pre += t * out.ldpre;
+    if (d->alpha_dtype == MBOK_F16)
+      launch_mfma8<uint16_t, false>(geo, packed, x, rows, ldx, nullptr, 0, stream, &o);
+    else
+      launch_mfma8<float, false>(geo, packed, x, rows, ldx, nullptr, 0, stream, &o);
+    if (hipGetLastError() != hipSuccess) return MBOK_ERR_HIP;
+  }
+  return MBOK_OK;
 }
 
 }  // namespace mbok

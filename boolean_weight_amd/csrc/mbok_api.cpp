@@ -27,6 +27,10 @@ int check_desc(const mbok_desc* d) {
   return MBOK_OK;
 }
 
+// largest leading dimension of the fine-tuning calls: T rows of it stay far
+// inside 63-bit element offsets
+constexpr int64_t kMaxLd = int64_t(1) << 32;
+
 size_t alpha_size(int32_t dt) { return dt == MBOK_F16 ? 2 : 4; }
 
 }  // namespace
@@ -237,6 +241,173 @@ int mbok_gemm(const mbok_desc* d, const void* packed, const void* X, int32_t x_d
 int mbok_gemm_precise(const mbok_desc* d, const void* packed, const void* X, int32_t x_dtype,
                       int64_t T, int64_t ldx, float* Y, int64_t ldy, void* stream) {
   return gemm_checked(d, packed, X, x_dtype, T, ldx, Y, ldy, 2, stream);
+}
+
+int mbok_gemmt(const mbok_desc* d, const void* packed, const void* dY, int64_t T, int64_t lddy,
+               void* dX, int64_t lddx, void* workspace, void* stream) {
+  int st = check_desc(d);
+  if (st != MBOK_OK) return st;
+  if (!packed || !dY || !dX) return MBOK_ERR_INVALID_ARG;
+  if (T < 1 || T > MBOK_MAX_T) return MBOK_ERR_SHAPE;
+  if (lddy < d->m || lddx < d->n || lddy > kMaxLd || lddx > kMaxLd) return MBOK_ERR_INVALID_ARG;
+  if (!aligned(packed, 16) || !aligned(dY, 2) || !aligned(dX, 16) || (lddx % 8) != 0 ||
+      (workspace && !aligned(workspace, 256)))
+    return MBOK_ERR_ALIGN;
+  return mbok::launch_gemmt(d, packed, dY, T, lddy, dX, lddx, workspace, (hipStream_t)stream);
+}
+
+size_t mbok_gemmt_workspace_bytes(const mbok_desc* d, int64_t T) {
+  if (check_desc(d) != MBOK_OK || T < 1 || T > MBOK_MAX_T) return 0;
+  return mbok::gemmt_workspace_bytes(d, T);
+}
+
+int mbok_scale_grad(const mbok_desc* d, const void* packed, const void* dY, int64_t T,
+                    int64_t lddy, const void* X, int64_t ldx, float* dalpha, int32_t accumulate,
+                    void* workspace, void* stream) {
+  int st = check_desc(d);
+  if (st != MBOK_OK) return st;
+  if (!packed || !dY || !X || !dalpha) return MBOK_ERR_INVALID_ARG;
+  if (T < 1 || T > MBOK_MAX_T) return MBOK_ERR_SHAPE;
+  if (lddy < d->m || ldx < d->n || lddy > kMaxLd || ldx > kMaxLd) return MBOK_ERR_INVALID_ARG;
+  if (!aligned(packed, 16) || !aligned(dY, 2) || !aligned(X, 16) || (ldx % 8) != 0 ||
+      !aligned(dalpha, 4) || (workspace && !aligned(workspace, 256)))
+    return MBOK_ERR_ALIGN;
+  return mbok::launch_scale_grad(d, packed, dY, T, lddy, X, ldx, dalpha, accumulate != 0,
+                                 workspace, (hipStream_t)stream);
+}
+
+size_t mbok_scale_grad_workspace_bytes(const mbok_desc* d, int64_t T) {
+  if (check_desc(d) != MBOK_OK || T < 1 || T > MBOK_MAX_T) return 0;
+  return mbok::scale_grad_workspace_bytes(d, T);
+}
+
+int mbok_gated_stack(const mbok_desc* d, mbok_desc* stacked) {
+  int st = check_desc(d);
+  if (st != MBOK_OK) return st;
+  if (!stacked) return MBOK_ERR_INVALID_ARG;
+  if (d->m > (1 << 23)) return MBOK_ERR_SHAPE;
+  *stacked = mbok::gated_stacked(d);
+  return MBOK_OK;
+}
+
+int mbok_gated_pack(const mbok_desc* d, const int8_t* signs_gate, const void* alpha_gate,
+                    const int8_t* signs_up, const void* alpha_up, void* packed, void* stream) {
+  mbok_desc stacked;
+  int st = mbok_gated_stack(d, &stacked);
+  if (st != MBOK_OK) return st;
+  if (!signs_gate || !alpha_gate || !signs_up || !alpha_up || !packed)
+    return MBOK_ERR_INVALID_ARG;
+  if (!aligned(signs_gate, 16) || !aligned(alpha_gate, 16) || !aligned(signs_up, 16) ||
+      !aligned(alpha_up, 16) || !aligned(packed, 16))
+    return MBOK_ERR_ALIGN;
+  return mbok::launch_gated_pack(d, signs_gate, alpha_gate, signs_up, alpha_up, packed,
+                                 (hipStream_t)stream);
+}
+
+int mbok_gated(const mbok_desc* d, const void* packed, const void* X, int32_t x_dtype, int64_t T,
+               int64_t ldx, int32_t act, void* H, int64_t ldh, void* pre, int64_t ldpre,
+               void* stream) {
+  mbok_desc stacked;
+  int st = mbok_gated_stack(d, &stacked);
+  if (st != MBOK_OK) return st;
+  if (!packed || !X || !H) return MBOK_ERR_INVALID_ARG;
+  if (T < 1 || T > MBOK_MAX_T) return MBOK_ERR_SHAPE;
+  if (act != MBOK_ACT_SILU && act != MBOK_ACT_GELU) return MBOK_ERR_INVALID_ARG;
+  if (ldx < d->n || ldh < d->m || ldx > kMaxLd || ldh > kMaxLd) return MBOK_ERR_INVALID_ARG;
+  if (pre && (ldpre < stacked.m || ldpre > kMaxLd)) return MBOK_ERR_INVALID_ARG;
+  if (x_dtype != MBOK_BF16) return MBOK_ERR_DTYPE;
+  if (!aligned(packed, 16) || !aligned(X, 16) || (ldx % 8) != 0 || !aligned(H, 2) ||
+      (pre && (!aligned(pre, 16) || (ldpre % 8) != 0)))
+    return MBOK_ERR_ALIGN;
+  return mbok::launch_gated(d, packed, X, T, ldx, act, H, ldh, pre, ldpre, (hipStream_t)stream);
+}
+
+int mbok_gated_backward(const mbok_desc* d, const void* packed, const void* pre, int64_t ldpre,
+                        const void* dH, int64_t lddh, int64_t T, int32_t act, void* dpre,
+                        int64_t lddpre, void* dX, int64_t lddx, void* workspace, void* stream) {
+  mbok_desc stacked;
+  int st = mbok_gated_stack(d, &stacked);
+  if (st != MBOK_OK) return st;
+  if (!packed || !pre || !dH || !dpre) return MBOK_ERR_INVALID_ARG;
+  if (T < 1 || T > MBOK_MAX_T) return MBOK_ERR_SHAPE;
+  if (act != MBOK_ACT_SILU && act != MBOK_ACT_GELU) return MBOK_ERR_INVALID_ARG;
+  if (ldpre < stacked.m || lddpre < stacked.m || lddh < d->m || ldpre > kMaxLd ||
+      lddpre > kMaxLd || lddh > kMaxLd)
+    return MBOK_ERR_INVALID_ARG;
+  if (dX && (lddx < d->n || lddx > kMaxLd)) return MBOK_ERR_INVALID_ARG;
+  if (dpre == pre && lddpre != ldpre) return MBOK_ERR_INVALID_ARG;
+  if (!aligned(packed, 16) || !aligned(pre, 16) || !aligned(dpre, 16) || (ldpre % 8) != 0 ||
+      (lddpre % 8) != 0 || !aligned(dH, 2) ||
+      (dX && (!aligned(dX, 16) || (lddx % 8) != 0)) || (workspace && !aligned(workspace, 256)))
+    return MBOK_ERR_ALIGN;
+  return mbok::launch_gated_backward(d, packed, pre, ldpre, dH, lddh, T, act, dpre, lddpre, dX,
+                                     lddx, workspace, (hipStream_t)stream);
+}
+
+static int check_distill(const mbok_distill_desc* d) {
+  if (!d || !std::isfinite(d->temperature) || !(d->temperature > 0.f))
+    return MBOK_ERR_INVALID_ARG;
+  if (d->vocab < 1 || d->vocab > MBOK_MAX_VOCAB || d->top < 1 || d->top > MBOK_MAX_TOP)
+    return MBOK_ERR_SHAPE;
+  return MBOK_OK;
+}
+
+int mbok_distill_desc_init(mbok_distill_desc* d, int32_t vocab, int32_t top, float temperature) {
+  if (!d) return MBOK_ERR_INVALID_ARG;
+  const mbok_distill_desc t = {vocab, top, temperature};
+  const int st = check_distill(&t);
+  if (st != MBOK_OK) return st;
+  *d = t;
+  return MBOK_OK;
+}
+
+static bool float_dtype(int32_t t) { return t == MBOK_F32 || t == MBOK_F16 || t == MBOK_BF16; }
+
+// what mbok_distill and mbok_distill_backward check alike
+static int check_distill_args(const mbok_distill_desc* d, const mbok::DistillArgs& a) {
+  const int st = check_distill(d);
+  if (st != MBOK_OK) return st;
+  if (!a.Z || !a.t_logits || !a.t_index) return MBOK_ERR_INVALID_ARG;
+  if (a.T < 1 || a.T > MBOK_MAX_DISTILL_ROWS) return MBOK_ERR_SHAPE;
+  if (a.ldz < d->vocab || a.ldt < d->top || a.ldz > kMaxLd || a.ldt > kMaxLd)
+    return MBOK_ERR_INVALID_ARG;
+  if (a.dZ && (a.lddz < d->vocab || a.lddz > kMaxLd)) return MBOK_ERR_INVALID_ARG;
+  if (!float_dtype(a.z_dtype) || !float_dtype(a.t_dtype)) return MBOK_ERR_DTYPE;
+  if (a.dZ && a.dz_dtype != a.z_dtype && a.dz_dtype != MBOK_BF16) return MBOK_ERR_DTYPE;
+  if (a.dZ == a.Z && (a.dz_dtype != a.z_dtype || a.lddz != a.ldz)) return MBOK_ERR_INVALID_ARG;
+  auto size = [](int32_t t) { return t == MBOK_F32 ? 4 : 2; };
+  if (!aligned(a.Z, size(a.z_dtype)) || !aligned(a.t_logits, size(a.t_dtype)) ||
+      !aligned(a.t_index, 4) || !aligned(a.t_lse, 4) || !aligned(a.weight, 4) ||
+      (a.dZ && !aligned(a.dZ, size(a.dz_dtype))))
+    return MBOK_ERR_ALIGN;
+  return MBOK_OK;
+}
+
+int mbok_distill(const mbok_distill_desc* d, const void* Z, int32_t z_dtype, int64_t T,
+                 int64_t ldz, const void* t_logits, int32_t t_dtype, const int32_t* t_index,
+                 int64_t ldt, const float* t_lse, const float* weight, float* loss, float* stats,
+                 void* dZ, int32_t dz_dtype, int64_t lddz, void* stream) {
+  const mbok::DistillArgs a = {Z, z_dtype, T, ldz, t_logits, t_dtype, t_index, ldt,
+                               t_lse, weight, dZ, dz_dtype, lddz};
+  const int st = check_distill_args(d, a);
+  if (st != MBOK_OK) return st;
+  if (!loss) return MBOK_ERR_INVALID_ARG;
+  if (!aligned(loss, 4) || (stats && !aligned(stats, 16))) return MBOK_ERR_ALIGN;
+  return mbok::launch_distill(d, a, loss, stats, (hipStream_t)stream);
+}
+
+int mbok_distill_backward(const mbok_distill_desc* d, const void* Z, int32_t z_dtype, int64_t T,
+                          int64_t ldz, const void* t_logits, int32_t t_dtype,
+                          const int32_t* t_index, int64_t ldt, const float* t_lse,
+                          const float* weight, const float* stats, const float* dloss, void* dZ,
+                          int32_t dz_dtype, int64_t lddz, void* stream) {
+  const mbok::DistillArgs a = {Z, z_dtype, T, ldz, t_logits, t_dtype, t_index, ldt,
+                               t_lse, weight, dZ, dz_dtype, lddz};
+  const int st = check_distill_args(d, a);
+  if (st != MBOK_OK) return st;
+  if (!stats || !dloss || !dZ) return MBOK_ERR_INVALID_ARG;
+  if (!aligned(stats, 16) || !aligned(dloss, 4)) return MBOK_ERR_ALIGN;
+  return mbok::launch_distill_backward(d, a, stats, dloss, (hipStream_t)stream);
 }
 
 const char* mbok_status_str(int status) {

@@ -41,6 +41,22 @@ __device__ __forceinline__ int tile16_of(int b, int tiles) {
   return (((j >> 2) << 3) + xcd) * 4 + (j & 3);
 }
 
+// Where the decode and few-token kernels' finished 16-row tiles go.  An Out
+// splits a tile of one token into kItems items; item(token, tile, e, sum)
+// writes item e, taking the sums of the tile rows it needs from sum(row).
+// RowsOut: the rows themselves, fp32.
+struct RowsOut {
+  static constexpr int kItems = 16;
+  float* __restrict__ y;
+  int64_t ldy;
+  int m;
+  template <typename Sum>
+  __device__ __forceinline__ void item(int token, int tile, int e, Sum&& sum) const {
+    const int i = tile * 16 + e;
+    if (i < m) y[token * ldy + i] = sum(e);
+  }
+};
+
 // ----------------------------------------------------------- conversions
 
 __device__ __forceinline__ float bf16_bits_to_f32(uint32_t b) {

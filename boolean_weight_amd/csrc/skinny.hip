@@ -37,7 +37,10 @@
 #include <stdlib.h>
 #include <string.h>
 
+#include <type_traits>
+
 #include "mbok_exact.h"
+#include "mbok_gated.h"
 #include "mbok_lanes.h"
 #include "mbok_launch.h"
 
@@ -75,11 +78,27 @@ __device__ __forceinline__ float scale_value<uint16_t>(uint32_t b) {
   return f16_bits_to_f32((uint16_t)b);
 }
 
-template <typename AT, int K>
-__global__ void __launch_bounds__(1024) gemm_skinny_kernel(
-    const u32x4* __restrict__ bits, const AT* __restrict__ scales,
-    const uint16_t* __restrict__ X, int64_t ldx, float* __restrict__ Y, int64_t ldy, int T,
-    int m, int G) {
+// Item e of the tile's token: sum(token, row) over the wavefronts.  Items
+// run over the threads with the row fastest, then tokens 0, 4, 8, 12, 1, ...
+// (the order of the partial sums in LDS).
+template <typename Out, typename Sum>
+__device__ __forceinline__ void skinny_item(const Out& out, int idx, int T, int tile, Sum&& sum) {
+  const int q = idx / Out::kItems;
+  const int tok = 4 * (q & 3) + (q >> 2);
+  if (tok < T)
+    out.item(tok, tile, idx % Out::kItems, [&](int row) { return sum(tok, row); });
+}
+
+// index of (token, row) in a tile's 256 partial sums
+__device__ __forceinline__ int skinny_part(int tok, int row) {
+  return (tok & 3) * 64 + (tok >> 2) * 16 + row;
+}
+
+template <typename AT, int K, typename Out>
+__device__ __forceinline__ void skinny_body(const u32x4* __restrict__ bits,
+                                            const AT* __restrict__ scales,
+                                            const uint16_t* __restrict__ X, int64_t ldx,
+                                            const Out& out, int T, int G) {
   extern __shared__ float red[];  // [NW][4][64] partial sums
   const int lane = threadIdx.x & 63;
   const int wave = threadIdx.x >> 6;
@@ -150,14 +169,28 @@ __global__ void __launch_bounds__(1024) gemm_skinny_kernel(
 #pragma unroll
   for (int r = 0; r < 4; ++r) red[(wave * 4 + r) * 64 + lane] = yacc[r];
   __syncthreads();
-  for (int idx = threadIdx.x; idx < 256; idx += blockDim.x) {
-    float sum = 0.f;
-    for (int w = 0; w < NW; ++w) sum += red[w * 256 + idx];
-    const int l = idx & 63, r = idx >> 6;
-    const int tok = 4 * (l >> 4) + r;
-    const int row = tile * 16 + (l & 15);
-    if (tok < T && row < m) Y[(int64_t)tok * ldy + row] = sum;
-  }
+  for (int idx = threadIdx.x; idx < 16 * Out::kItems; idx += blockDim.x)
+    skinny_item(out, idx, T, tile, [&](int tok, int row) {
+      float sum = 0.f;
+      for (int w = 0; w < NW; ++w) sum += red[w * 256 + skinny_part(tok, row)];
+      return sum;
+    });
+}
+
+template <typename AT, int K>
+__global__ void __launch_bounds__(1024) gemm_skinny_kernel(
+    const u32x4* __restrict__ bits, const AT* __restrict__ scales,
+    const uint16_t* __restrict__ X, int64_t ldx, float* __restrict__ Y, int64_t ldy, int T,
+    int m, int G) {
+  skinny_body<AT, K>(bits, scales, X, ldx, RowsOut{Y, ldy, m}, T, G);
+}
+
+// the gated feed-forward block on its stacked layer
+template <typename AT, int K>
+__global__ void __launch_bounds__(1024) gated_skinny_kernel(
+    const u32x4* __restrict__ bits, const AT* __restrict__ scales,
+    const uint16_t* __restrict__ X, int64_t ldx, int T, int G, GatedOut out) {
+  skinny_body<AT, K>(bits, scales, X, ldx, out, T, G);
 }
 
 // Streaming form (the default): one persistent workgroup per compute unit.
@@ -226,12 +259,12 @@ __device__ __forceinline__ void svid_block_fragments(const void* __restrict__ x,
 // (bits 0..3, one more for workgroups below tw >> 8) | wavefronts (bits
 // 4..7) are arguments, so no address waits on a dispatch-packet load and
 // nothing is divided.
-template <typename AT, int K, int JMAX, bool SV>
-__global__ void __launch_bounds__(512) gemm_skinny_stream_kernel(
+template <typename AT, int K, int JMAX, bool SV, typename Out>
+__device__ __forceinline__ void skinny_stream_body(
     const u32x4* __restrict__ bits, const AT* __restrict__ scales,
     const uint16_t* __restrict__ X, int64_t ldx, int T, int G, int slab_groups, int tiles,
-    int grid, int tw, float* __restrict__ Y, int64_t ldy, int m, const void* __restrict__ sv_x,
-    int sv_xf32, const AT* __restrict__ sv_sin) {
+    int grid, int tw, const Out& out, const void* __restrict__ sv_x, int sv_xf32,
+    const AT* __restrict__ sv_sin) {
   extern __shared__ float red[];  // [JMAX][NW][4][64] partial sums
   const int lane = threadIdx.x & 63;
   const int wave = threadIdx.x >> 6;
@@ -364,19 +397,40 @@ __global__ void __launch_bounds__(512) gemm_skinny_stream_kernel(
         sum += part;
       }
       const int row = tile16_of((int)blockIdx.x + t * grid, tiles) * 16 + ri;
-      if (row < m) Y[row] = sum;
+      if (row < out.m) out.y[row] = sum;
     }
   } else {
-    for (int idx = threadIdx.x; idx < ntl * 256; idx += NW * 64) {
-      const int t = idx >> 8, e = idx & 255;
-      float sum = 0.f;
-      for (int w = 0; w < NW; ++w) sum += red[(t * NW + w) * 256 + e];
-      const int l = e & 63, r = e >> 6;
-      const int tok = 4 * (l >> 4) + r;
-      const int row = tile16_of((int)blockIdx.x + t * grid, tiles) * 16 + (l & 15);
-      if (tok < T && row < m) Y[(int64_t)tok * ldy + row] = sum;
+    for (int idx = threadIdx.x; idx < ntl * 16 * Out::kItems; idx += NW * 64) {
+      const int t = idx / (16 * Out::kItems);
+      skinny_item(out, idx % (16 * Out::kItems), T,
+                  tile16_of((int)blockIdx.x + t * grid, tiles), [&](int tok, int row) {
+                    float sum = 0.f;
+                    for (int w = 0; w < NW; ++w)
+                      sum += red[(t * NW + w) * 256 + skinny_part(tok, row)];
+                    return sum;
+                  });
     }
   }
+}
+
+template <typename AT, int K, int JMAX, bool SV>
+__global__ void __launch_bounds__(512) gemm_skinny_stream_kernel(
+    const u32x4* __restrict__ bits, const AT* __restrict__ scales,
+    const uint16_t* __restrict__ X, int64_t ldx, int T, int G, int slab_groups, int tiles,
+    int grid, int tw, float* __restrict__ Y, int64_t ldy, int m, const void* __restrict__ sv_x,
+    int sv_xf32, const AT* __restrict__ sv_sin) {
+  skinny_stream_body<AT, K, JMAX, SV>(bits, scales, X, ldx, T, G, slab_groups, tiles, grid, tw,
+                                      RowsOut{Y, ldy, m}, sv_x, sv_xf32, sv_sin);
+}
+
+// the gated feed-forward block on its stacked layer
+template <typename AT, int K, int JMAX>
+__global__ void __launch_bounds__(512) gated_skinny_stream_kernel(
+    const u32x4* __restrict__ bits, const AT* __restrict__ scales,
+    const uint16_t* __restrict__ X, int64_t ldx, int T, int G, int slab_groups, int tiles,
+    int grid, int tw, GatedOut out) {
+  skinny_stream_body<AT, K, JMAX, false>(bits, scales, X, ldx, T, G, slab_groups, tiles, grid, tw,
+                                         out, nullptr, 0, (const AT*)nullptr);
 }
 
 int env_int(const char* name, int fallback) {
@@ -386,8 +440,14 @@ int env_int(const char* name, int fallback) {
 
 template <typename AT, int K>
 void launch_k(const Geom& geo, const u32x4* bits, const AT* scales, const uint16_t* X,
-              int64_t ldx, float* Y, int64_t ldy, int T, int NW, hipStream_t stream) {
+              int64_t ldx, float* Y, int64_t ldy, int T, int NW, const GatedOut* gated,
+              hipStream_t stream) {
   const size_t lds = (size_t)NW * 256 * sizeof(float);
+  if (gated) {
+    hipLaunchKernelGGL((gated_skinny_kernel<AT, K>), dim3(geo.RB * 4), dim3(64 * NW), lds, stream,
+                       bits, scales, X, ldx, T, geo.G, *gated);
+    return;
+  }
   hipLaunchKernelGGL((gemm_skinny_kernel<AT, K>), dim3(geo.RB * 4), dim3(64 * NW), lds, stream,
                      bits, scales, X, ldx, Y, ldy, T, geo.m, geo.G);
 }
@@ -397,7 +457,8 @@ constexpr int kSkinnyJ = 8;  // tiles per persistent workgroup (registers)
 template <typename AT, int K, bool SV = false>
 void launch_stream_k(const Geom& geo, const u32x4* bits, const AT* scales, const uint16_t* X,
                      int64_t ldx, float* Y, int64_t ldy, int T, hipStream_t stream,
-                     const void* sv_x = nullptr, int sv_xf32 = 0, const AT* sv_sin = nullptr) {
+                     const void* sv_x = nullptr, int sv_xf32 = 0, const AT* sv_sin = nullptr,
+                     const GatedOut* gated = nullptr) {
   // slabs of at most 32 groups: one wavefront per block of 4 groups, at most 8
   const int nslabs = (geo.G + 31) / 32;
   const int slab = (geo.G + nslabs - 1) / nslabs;
@@ -409,6 +470,11 @@ void launch_stream_k(const Geom& geo, const u32x4* bits, const AT* scales, const
   if (SV) lds += (size_t)NW * 4 * K * 2 * kGroup * sizeof(uint16_t);
   static_assert(kSkinnyJ <= 15, "tiles per workgroup are packed in 4 bits");
   const int tw = tiles / grid | NW << 4 | (tiles % grid) << 8;
+  if (gated) {
+    hipLaunchKernelGGL((gated_skinny_stream_kernel<AT, K, kSkinnyJ>), dim3(grid), dim3(64 * NW),
+                       lds, stream, bits, scales, X, ldx, T, geo.G, slab, tiles, grid, tw, *gated);
+    return;
+  }
   hipLaunchKernelGGL((gemm_skinny_stream_kernel<AT, K, kSkinnyJ, SV>), dim3(grid), dim3(64 * NW), lds,
                      stream, bits, scales, X, ldx, T, geo.G, slab, tiles, grid, tw, Y, ldy, geo.m,
                      sv_x, sv_xf32, sv_sin);
@@ -416,7 +482,7 @@ void launch_stream_k(const Geom& geo, const u32x4* bits, const AT* scales, const
 
 template <typename AT>
 int launch_at(const Geom& geo, const void* packed, const void* X, int64_t ldx, float* Y,
-              int64_t ldy, int T, hipStream_t stream) {
+              int64_t ldy, int T, const GatedOut* gated, hipStream_t stream) {
   const u32x4* bits = reinterpret_cast<const u32x4*>(packed);
   const AT* scales = reinterpret_cast<const AT*>(reinterpret_cast<const char*>(packed) +
                                                  geo.bits_bytes);
@@ -429,11 +495,15 @@ int launch_at(const Geom& geo, const void* packed, const void* X, int64_t ldx, f
   if (v && strcmp(v, "blocks") == 0) streaming = false;
   if (v && strcmp(v, "stream") == 0) streaming = true;
   if (streaming) {
+    auto stream_k = [&](auto k) {
+      launch_stream_k<AT, decltype(k)::value>(geo, bits, scales, Xb, ldx, Y, ldy, T, stream,
+                                              nullptr, 0, nullptr, gated);
+    };
     switch (geo.K) {
-      case 1: launch_stream_k<AT, 1>(geo, bits, scales, Xb, ldx, Y, ldy, T, stream); break;
-      case 2: launch_stream_k<AT, 2>(geo, bits, scales, Xb, ldx, Y, ldy, T, stream); break;
-      case 3: launch_stream_k<AT, 3>(geo, bits, scales, Xb, ldx, Y, ldy, T, stream); break;
-      default: launch_stream_k<AT, 4>(geo, bits, scales, Xb, ldx, Y, ldy, T, stream); break;
+      case 1: stream_k(std::integral_constant<int, 1>{}); break;
+      case 2: stream_k(std::integral_constant<int, 2>{}); break;
+      case 3: stream_k(std::integral_constant<int, 3>{}); break;
+      default: stream_k(std::integral_constant<int, 4>{}); break;
     }
     return hipGetLastError() == hipSuccess ? MBOK_OK : MBOK_ERR_HIP;
   }
@@ -445,10 +515,10 @@ int launch_at(const Geom& geo, const void* packed, const void* X, int64_t ldx, f
   if (NW > geo.G) NW = geo.G;
   if (NW < 1) NW = 1;
   switch (geo.K) {
-    case 1: launch_k<AT, 1>(geo, bits, scales, Xb, ldx, Y, ldy, T, NW, stream); break;
-    case 2: launch_k<AT, 2>(geo, bits, scales, Xb, ldx, Y, ldy, T, NW, stream); break;
-    case 3: launch_k<AT, 3>(geo, bits, scales, Xb, ldx, Y, ldy, T, NW, stream); break;
-    default: launch_k<AT, 4>(geo, bits, scales, Xb, ldx, Y, ldy, T, NW, stream); break;
+    case 1: launch_k<AT, 1>(geo, bits, scales, Xb, ldx, Y, ldy, T, NW, gated, stream); break;
+    case 2: launch_k<AT, 2>(geo, bits, scales, Xb, ldx, Y, ldy, T, NW, gated, stream); break;
+    case 3: launch_k<AT, 3>(geo, bits, scales, Xb, ldx, Y, ldy, T, NW, gated, stream); break;
+    default: launch_k<AT, 4>(geo, bits, scales, Xb, ldx, Y, ldy, T, NW, gated, stream); break;
   }
   return hipGetLastError() == hipSuccess ? MBOK_OK : MBOK_ERR_HIP;
 }
@@ -493,8 +563,18 @@ int launch_skinny(const mbok_desc* d, const void* packed, const void* X, int64_t
   if (T < 1 || T > kMaxSkinnyTokens) return MBOK_ERR_SHAPE;
   const Geom geo = make_geom(d);
   if (d->alpha_dtype == MBOK_F16)
-    return launch_at<uint16_t>(geo, packed, X, ldx, Y, ldy, (int)T, stream);
-  return launch_at<float>(geo, packed, X, ldx, Y, ldy, (int)T, stream);
+    return launch_at<uint16_t>(geo, packed, X, ldx, Y, ldy, (int)T, nullptr, stream);
+  return launch_at<float>(geo, packed, X, ldx, Y, ldy, (int)T, nullptr, stream);
+}
+
+// d: the stacked layer
+int launch_gated_skinny(const mbok_desc* d, const void* packed, const void* X, int64_t T,
+                        int64_t ldx, const GatedOut& out, hipStream_t stream) {
+  if (T < 1 || T > kMaxSkinnyTokens) return MBOK_ERR_SHAPE;
+  const Geom geo = make_geom(d);
+  if (d->alpha_dtype == MBOK_F16)
+    return launch_at<uint16_t>(geo, packed, X, ldx, nullptr, 0, (int)T, &out, stream);
+  return launch_at<float>(geo, packed, X, ldx, nullptr, 0, (int)T, &out, stream);
 }
 
 }  // namespace mbok

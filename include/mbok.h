@@ -494,6 +494,235 @@ int mbok_gemm_precise(const mbok_desc* d, const void* packed, const void* X,
                       int32_t x_dtype, int64_t T, int64_t ldx, float* Y,
                       int64_t ldy, void* stream);
 
+/* ------------------------------------------------------------------------
+ * Fine-tuning a Boolean-kernel model against a teacher, and the gated
+ * feed-forward block ([GS] Dutch summary, Methodologie 3, and the Spanish
+ * summary's training section: the kernels are finetuned by distillation from
+ * the full-precision model, gradients flowing through the Boolean weights;
+ * [RN] 训练策略: the last kernel and the scales are tuned).
+ * ------------------------------------------------------------------------ */
+
+/*
+ * Transposed product for T gradient rows, the activation gradient of a layer
+ * (mbok_gemvt is the one-row form with fp32 terms):
+ *     dX[t, j] = sum_i dY[t, i] * W_hat[i, j]
+ * Each tile of W_hat is formed as sum_k alpha_k b_k in fp32, rounded to bf16
+ * (nearest-even) and contracted with dY on the matrix cores with fp32
+ * accumulation; dX is the sum rounded once to bf16 (the gradient of bf16
+ * activations, and what the layer below takes as its dY).  Row sums run in a
+ * fixed order: results are bit-reproducible for a given workspace choice.
+ *  packed    device, MBOK_LAYOUT_L64 buffer of this descriptor.
+ *  dY        device bf16 [T, lddy], lddy >= m, 2-byte aligned.
+ *  T         1 .. MBOK_MAX_T.
+ *  dX        device bf16 [T, lddx], lddx >= n, lddx % 8 == 0; overwritten.
+ *            Must not overlap dY.
+ *  workspace device, mbok_gemmt_workspace_bytes(d, T) bytes, 256-byte
+ *            aligned, or NULL.  With it the rows of W_hat are split into
+ *            slices when the output alone gives too few tiles, and a second
+ *            kernel adds the slices' partial sums in a fixed order; with NULL
+ *            every tile walks all rows (correct, slower for few tokens).  Its
+ *            contents need no initialisation; calls that may run at the same
+ *            time need distinct workspaces.
+ * A non-finite dY element makes its whole row of dX NaN or infinite.
+ * Errors: INVALID_ARG (NULL, lddy < m, lddx < n), SHAPE (T), ALIGN (packed
+ * and dX 16 bytes, lddx % 8, dY 2 bytes, workspace 256 bytes), HIP, and the
+ * descriptor's.
+ */
+int mbok_gemmt(const mbok_desc* d, const void* packed, const void* dY, int64_t T,
+               int64_t lddy, void* dX, int64_t lddx, void* workspace, void* stream);
+
+/* Bytes of the workspace mbok_gemmt uses for this layer and T rows (0 when it
+ * needs none).  Host only; 0 for a NULL or invalid descriptor or T. */
+size_t mbok_gemmt_workspace_bytes(const mbok_desc* d, int64_t T);
+
+/*
+ * Gradient of the scales ([RN] 关键设计: W_hat = sum_k alpha_k (.) B_k, so a
+ * scale's derivative is the weight gradient contracted with its signs):
+ *     dalpha_k[i, g] = sum_{j in group g} b_k[i, j] * sum_t dY[t, i] X[t, j]
+ * The m x n weight gradient is formed tile by tile on the matrix cores (exact
+ * bf16 products, fp32 sums), contracted with the signs in fp32 and never
+ * stored.
+ *  packed     device, the layer's buffer (its signs are read, not its scales).
+ *  dY         device bf16 [T, lddy], lddy >= m, 2-byte aligned.
+ *  X          device bf16 [T, ldx], ldx >= n, ldx % 8 == 0, 16-byte aligned.
+ *  T          1 .. MBOK_MAX_T.
+ *  dalpha     device fp32 [K][m][n/128] (the order of mbok_pack's alpha).
+ *  accumulate 0 overwrites dalpha; otherwise the result is added to it
+ *             (gradient accumulation over several calls).
+ *  workspace  device, mbok_scale_grad_workspace_bytes(d, T) bytes, 256-byte
+ *             aligned, or NULL.  With it the tokens are split into slices when
+ *             the layer alone gives too few tiles; the partial sums are added
+ *             in a fixed order.  As for mbok_gemmt.
+ * A non-finite value of dY or X reaches every scale it contributes to.
+ * Errors: INVALID_ARG (NULL, lddy < m, ldx < n), SHAPE (T), ALIGN (packed and
+ * X 16 bytes, ldx % 8, dY 2 bytes, dalpha 4 bytes, workspace 256 bytes), HIP,
+ * and the descriptor's.
+ */
+int mbok_scale_grad(const mbok_desc* d, const void* packed, const void* dY, int64_t T,
+                    int64_t lddy, const void* X, int64_t ldx, float* dalpha,
+                    int32_t accumulate, void* workspace, void* stream);
+
+/* Bytes of the workspace mbok_scale_grad uses (0 when it needs none).  Host
+ * only; 0 for a NULL or invalid descriptor or T. */
+size_t mbok_scale_grad_workspace_bytes(const mbok_desc* d, int64_t T);
+
+/* Activations of the gated block. */
+enum {
+  MBOK_ACT_SILU = 0, /* x / (1 + exp(-x)) */
+  MBOK_ACT_GELU = 1  /* x (1 + tanh(sqrt(2/pi) (x + 0.044715 x^3))) / 2 */
+};
+
+/*
+ * Gated feed-forward block H = act(X Wg^T) (.) (X Wu^T) with both projections
+ * as Boolean kernels.  The two projections have one shape `d` (m outputs, n
+ * inputs, K kernels each) and are kept as ONE layer in MBOK_LAYOUT_L64, the
+ * stacked layer, of 16 ceil(m / 8) rows in which every 16-row tile holds 8
+ * gate rows and then the same 8 up rows:
+ *     stacked row 16 u + r     = gate row 8 u + r      (r = 0..7)
+ *     stacked row 16 u + 8 + r = up   row 8 u + r
+ * Rows past m are zero (bits and scales).  So both values of an output meet in
+ * one tile and every call here takes one pass over one buffer.  The stacked
+ * layer is an ordinary one: mbok_gemm, mbok_gemmt and mbok_scale_grad take it
+ * with the descriptor that mbok_gated_stack fills.
+ */
+
+/* Fills *stacked with the descriptor of the stacked layer of two projections
+ * of shape *d (the pointers may be equal).  Host only.  Errors: the
+ * descriptor's, INVALID_ARG (NULL), SHAPE (more than 2^24 stacked rows). */
+int mbok_gated_stack(const mbok_desc* d, mbok_desc* stacked);
+
+/*
+ * Packs the two projections into the stacked layer.
+ *  signs_gate, signs_up  device int8 [K][m][n], as for mbok_pack.
+ *  alpha_gate, alpha_up  device [K][m][n/128] of d->alpha_dtype.
+ *  packed                device, mbok_packed_bytes of the stacked descriptor;
+ *                        fully overwritten, padding included.
+ * Errors: INVALID_ARG (NULL), ALIGN (16 bytes), HIP, mbok_gated_stack's.
+ */
+int mbok_gated_pack(const mbok_desc* d, const int8_t* signs_gate, const void* alpha_gate,
+                    const int8_t* signs_up, const void* alpha_up, void* packed,
+                    void* stream);
+
+/*
+ * H[t, i] = act(g) * u with g = sum_j Wg[i, j] X[t, j], u = sum_j Wu[i, j]
+ * X[t, j].  One kernel: both products in fp32 as mbok_gemm computes them for
+ * T rows of the stacked layer, activation and product in fp32, one rounding
+ * to bf16.
+ *  packed  device, the buffer of mbok_gated_pack.
+ *  X       device bf16 [T, ldx], ldx >= n, ldx % 8 == 0, 16-byte aligned.
+ *  T       1 .. MBOK_MAX_T.
+ *  act     MBOK_ACT_SILU or MBOK_ACT_GELU.
+ *  H       device bf16 [T, ldh], ldh >= m, 2-byte aligned; overwritten.
+ *  pre     device bf16 [T, ldpre] or NULL; ldpre >= 16 ceil(m / 8): g and u,
+ *          each rounded once to bf16, in the stacked order (padding columns
+ *          are written as 0), for mbok_gated_backward.  16-byte aligned,
+ *          ldpre % 8 == 0.
+ * For T <= 16 a non-finite activation of a token makes its H (and pre) NaN on
+ * the matrix-core paths; larger T follow IEEE arithmetic.
+ * Errors: INVALID_ARG (NULL, act, leading dimensions), SHAPE (T; a stacked
+ * layer of 2^32 or more sign words for T > 16), DTYPE (x_dtype other than
+ * MBOK_BF16), ALIGN, HIP, mbok_gated_stack's.
+ */
+int mbok_gated(const mbok_desc* d, const void* packed, const void* X, int32_t x_dtype,
+               int64_t T, int64_t ldx, int32_t act, void* H, int64_t ldh, void* pre,
+               int64_t ldpre, void* stream);
+
+/*
+ * Backward of the gated block.  With g, u from pre and s = dH:
+ *     dg = s u act'(g),  du = s act(g)      (fp32, rounded once to bf16)
+ *     dX = dg Wg + du Wu                    (mbok_gemmt of the stacked layer)
+ *  pre   device bf16 [T, ldpre], as mbok_gated wrote it (padding columns are
+ *        not read).
+ *  dH    device bf16 [T, lddh], lddh >= m, 2-byte aligned.
+ *  dpre  device bf16 [T, lddpre]; overwritten with dg and du in the stacked
+ *        order, padding columns 0: the dY of mbok_scale_grad on the stacked
+ *        layer.  May be pre itself (same leading dimension).
+ *  dX    device bf16 [T, lddx] or NULL (then only dpre is computed).
+ *  workspace  device, mbok_gemmt_workspace_bytes(stacked, T) bytes or NULL,
+ *        as for mbok_gemmt.
+ * Errors: INVALID_ARG (NULL, act, leading dimensions), SHAPE (T), ALIGN
+ * (packed, pre, dpre, dX 16 bytes, ldpre, lddpre, lddx % 8, dH 2 bytes,
+ * workspace 256 bytes), HIP, mbok_gated_stack's.
+ */
+int mbok_gated_backward(const mbok_desc* d, const void* packed, const void* pre,
+                        int64_t ldpre, const void* dH, int64_t lddh, int64_t T, int32_t act,
+                        void* dpre, int64_t lddpre, void* dX, int64_t lddx, void* workspace,
+                        void* stream);
+
+/* Largest number of listed teacher entries and largest vocabulary of
+ * mbok_distill, its most rows, and floats of statistics per row. */
+#define MBOK_MAX_TOP 1024
+#define MBOK_MAX_VOCAB (1 << 19)
+#define MBOK_MAX_DISTILL_ROWS (1 << 24)
+#define MBOK_DISTILL_STATS 8
+
+/* Shape of one distillation loss.  Fill it with mbok_distill_desc_init. */
+typedef struct mbok_distill_desc {
+  int32_t vocab;     /* V, 1 .. MBOK_MAX_VOCAB */
+  int32_t top;       /* listed entries per row, 1 .. MBOK_MAX_TOP */
+  float temperature; /* tau, finite and > 0 */
+} mbok_distill_desc;
+
+/* Host only.  Errors: INVALID_ARG (NULL, temperature), SHAPE (vocab, top). */
+int mbok_distill_desc_init(mbok_distill_desc* d, int32_t vocab, int32_t top,
+                           float temperature);
+
+/*
+ * Distillation from a teacher's top logits ([GS] summaries' training
+ * sections: knowledge distillation on the logits of the full-precision
+ * model, of which a corpus keeps the `top` largest per row).  Per row, with
+ * q = softmax(z / tau) over the vocabulary and the listed entries (v_j, l_j):
+ *   t_lse NULL:  p_j = exp(l_j / tau) / sum of the listed exp(l / tau)
+ *                loss = w tau^2 sum_j p_j (log p_j - log q_{v_j})
+ *                dz_v = w tau (q_v - sum_{j: v_j = v} p_j)
+ *   t_lse given: p_j = exp(l_j / tau - t_lse) (the teacher's own
+ *                probabilities); what is not listed is one more class of
+ *                mass p_r = max(0, 1 - sum_j p_j), q_r = sum of the other q_v:
+ *                loss += w tau^2 p_r log(p_r / q_r), and for unlisted v
+ *                dz_v = w tau q_v (1 - p_r / q_r)
+ *                (no such class when every token is listed or q_r is 0)
+ * An entry whose index is negative or >= V is not there (rows with fewer
+ * entries); an index listed twice counts twice.  A row whose listed entries
+ * carry no teacher weight (none there, or all l = -inf) has, without t_lse,
+ * loss 0 and gradient 0.  A row of weight 0 is not read: loss 0, gradient 0.
+ * A p_j of 0 contributes nothing; q_{v_j} = 0 with p_j > 0 gives +inf; NaN
+ * logits, +inf logits and rows of only -inf give NaN.
+ * Row maxima, sums and logarithms are at least fp32 (the sums of a row and
+ * the loss in float64 at the end).
+ *  Z        device [T, ldz] of z_dtype (MBOK_F32, MBOK_F16, MBOK_BF16).
+ *  T        1 .. MBOK_MAX_DISTILL_ROWS.
+ *  t_logits device [T, ldt] of t_dtype (any of the three), l.
+ *  t_index  device int32 [T, ldt], v; ldt >= top for both.
+ *  t_lse    device fp32 [T] or NULL: log sum exp(teacher logits / tau).
+ *  weight   device fp32 [T] or NULL (all 1): w.
+ *  loss     device fp32 [T]; overwritten.
+ *  stats    device fp32 [T][MBOK_DISTILL_STATS] or NULL; overwritten: what
+ *           mbok_distill_backward needs of this pass.  16-byte aligned.
+ *  dZ       device [T, lddz] of dz_dtype (z_dtype or MBOK_BF16), or NULL for
+ *           the loss alone: the gradient of sum_t loss[t], in the same pass
+ *           over Z.  May be Z itself (same dtype and leading dimension).
+ * Errors: INVALID_ARG (NULL, leading dimensions), SHAPE (T, the descriptor's),
+ * DTYPE, ALIGN (Z, dZ and t_logits to their element, t_index, t_lse, weight and
+ * loss 4 bytes, stats 16 bytes), HIP.
+ */
+int mbok_distill(const mbok_distill_desc* d, const void* Z, int32_t z_dtype, int64_t T,
+                 int64_t ldz, const void* t_logits, int32_t t_dtype, const int32_t* t_index,
+                 int64_t ldt, const float* t_lse, const float* weight, float* loss,
+                 float* stats, void* dZ, int32_t dz_dtype, int64_t lddz, void* stream);
+
+/*
+ * The gradient alone, after mbok_distill with stats on the same inputs:
+ * dZ[t, v] = dloss[t] * d loss[t] / d Z[t, v].
+ *  dloss  device fp32 [T], the gradient arriving at the loss.
+ * A row whose weight or dloss is 0 is written as 0.  Everything else as for
+ * mbok_distill (dZ may be Z itself).
+ */
+int mbok_distill_backward(const mbok_distill_desc* d, const void* Z, int32_t z_dtype,
+                          int64_t T, int64_t ldz, const void* t_logits, int32_t t_dtype,
+                          const int32_t* t_index, int64_t ldt, const float* t_lse,
+                          const float* weight, const float* stats, const float* dloss,
+                          void* dZ, int32_t dz_dtype, int64_t lddz, void* stream);
+
 /* Static description of a status code ("unknown status" for others). */
 const char* mbok_status_str(int status);
 
