@@ -537,6 +537,13 @@ def _gemm_call(name: str, d: mbok_desc, packed: torch.Tensor, X: torch.Tensor, Y
 # ------------------------------------- fine-tuning and the gated feed-forward block
 
 _FLOATS = {torch.float32: MBOK_F32, torch.float16: MBOK_F16, torch.bfloat16: MBOK_BF16}
+# These calls take a few microseconds on the GPU at their smallest, so what
+# Python adds to a launch counts: the raw stream handle and current device
+# come from the C functions behind torch.cuda.current_stream() and
+# current_device() (together 1.3 us less per call), tensors are asked for each
+# attribute once, and layer sizes are remembered by shape.
+_raw_stream = torch._C._cuda_getCurrentRawStream
+_current_device = torch._C._cuda_getDevice
 
 
 @functools.lru_cache(maxsize=4096)
@@ -550,68 +557,71 @@ def _slices_bytes(name: str, m: int, n: int, K: int, alpha_dtype: int, T: int) -
     return int(getattr(load_library(), name)(ctypes.byref(d), T))
 
 
-class _on_device:
-    """The device of a call's tensors, made current for its launch when it is
-    not; the raw handle of the call's stream (by default that device's current
-    one)."""
-
-    def __init__(self, dev: int):
-        self.dev, self.guard = dev, None
-        if dev != torch.cuda.current_device():
-            self.guard = torch.cuda.device(dev)
-
-    def __enter__(self):
-        if self.guard is not None:
-            self.guard.__enter__()
-        return self
-
-    def __exit__(self, *exc):
-        if self.guard is not None:
-            self.guard.__exit__(*exc)
-
-    def stream(self, stream) -> int:
-        return torch.cuda.current_stream(self.dev).cuda_stream if stream is None \
-            else _stream(stream)
+def _launch(fn, name: str, dev: int, stream, *args) -> None:
+    """fn(*args, stream) with the tensors' device current."""
+    if dev == _current_device():
+        status = fn(*args, _raw_stream(dev) if stream is None else _stream(stream))
+    else:
+        with torch.cuda.device(dev):
+            status = fn(*args, _raw_stream(dev) if stream is None else _stream(stream))
+    if status:
+        raise MbokError(status, name)
 
 
-def _one_device(first: torch.Tensor, **others) -> int:
-    dev = first.get_device()
-    for name, t in others.items():
-        if t is not None and _dev(t, name).get_device() != dev:
-            raise ValueError(f"{name} is on another device than the other tensors")
+def _first(t: torch.Tensor, name: str) -> int:
+    """The device of a call's first tensor; the others have to be on it."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    dev = t.get_device()
+    if dev < 0:
+        raise ValueError(f"{name} must be on the GPU (the library takes device pointers)")
     return dev
 
 
-def _matrix(t: torch.Tensor, name: str, rows: int, cols: int, dtype) -> int:
+def _elsewhere(t, name: str):
+    _dev(t, name)
+    raise ValueError(f"{name} is on another device than the other tensors")
+
+
+def _matrix(t: torch.Tensor, name: str, dev: int, rows: int, cols: int, dtype) -> int:
     """Row stride of a [rows, >= cols] matrix with contiguous rows."""
+    if not isinstance(t, torch.Tensor) or t.get_device() != dev:
+        _elsewhere(t, name)
     if t.dtype != dtype:
         raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.dim() != 2 or t.shape[0] != rows or t.shape[1] < cols:
-        raise ValueError(f"{name} must be [{rows}, >= {cols}], got {tuple(t.shape)}")
-    if t.stride(1) != 1 and t.shape[1] > 1:
+    shape = t.shape
+    if len(shape) != 2 or shape[0] != rows or shape[1] < cols:
+        raise ValueError(f"{name} must be [{rows}, >= {cols}], got {tuple(shape)}")
+    ld, step = t.stride()
+    if step != 1 and shape[1] > 1:
         raise ValueError(f"{name} rows must be contiguous")
     if rows == 1:
         # the stride of a single row is arbitrary and never used
-        return (max(cols, t.shape[1]) + 7) // 8 * 8
-    if t.stride(0) < cols:
+        return (shape[1] + 7) // 8 * 8
+    if ld < cols:
         raise ValueError(f"{name} rows must not overlap")
-    return t.stride(0)
+    return ld
 
 
-def _vector(t: torch.Tensor, name: str, count: int, dtype) -> int:
+def _vector(t: torch.Tensor, name: str, dev: int, count: int, dtype) -> int:
+    if not isinstance(t, torch.Tensor) or t.get_device() != dev:
+        _elsewhere(t, name)
     if t.dtype != dtype or not t.is_contiguous() or t.numel() < count:
         raise ValueError(f"{name} must be contiguous {dtype} with {count} elements")
     return t.data_ptr()
 
 
-def _packed(d: mbok_desc, packed: torch.Tensor, m: int) -> int:
-    if not packed.is_contiguous() or packed.numel() * packed.element_size() < \
-            _packed_bytes(m, d.n, d.K, d.alpha_dtype):
+def _packed(packed: torch.Tensor, dev: int, m: int, n: int, K: int, alpha_dtype: int) -> int:
+    if not isinstance(packed, torch.Tensor) or packed.get_device() != dev:
+        _elsewhere(packed, "packed")
+    if not packed.is_contiguous() or \
+            packed.numel() * packed.itemsize < _packed_bytes(m, n, K, alpha_dtype):
         raise ValueError("packed must be contiguous and hold the layer")
     return packed.data_ptr()
 
 
-def _slices(name: str, d: mbok_desc, m: int, T: int, workspace, dev: int, stream):
+def _slices(name: str, m: int, n: int, K: int, alpha_dtype: int, T: int, workspace, dev: int,
+            stream):
     """(pointer, tensor) of the workspace of a call that may split its sum.
 
     True keeps one per (device, stream) as workspace_for does, except under
@@ -619,28 +629,31 @@ def _slices(name: str, d: mbok_desc, m: int, T: int, workspace, dev: int, stream
     pool, so that no later call's growth frees it and no two graphs share it."""
     if workspace is None or workspace is False:
         return None, None
-    need = _slices_bytes(name, m, d.n, d.K, d.alpha_dtype, T)
+    need = _slices_bytes(name, m, n, K, alpha_dtype, T)
     if need == 0:
         return None, None
-    if workspace is True:
-        device = torch.device("cuda", dev)
-        if stream is None:
-            target = contextlib.nullcontext()
-        else:
-            target = torch.cuda.stream(
-                stream if isinstance(stream, torch.cuda.Stream)
-                else torch.cuda.ExternalStream(int(stream), device=device))
-        with target:
-            captured = torch.cuda.is_current_stream_capturing()
-            ws = torch.empty(need, dtype=torch.uint8, device=device) if captured else None
-        if not captured:
-            ws = workspace_for(need, device, stream)
-    else:
-        ws = _dev(workspace, "workspace")
-        if ws.get_device() != dev:
-            raise ValueError("workspace is on another device than the other tensors")
-        if not ws.is_contiguous() or ws.numel() * ws.element_size() < need:
+    if workspace is not True:
+        ws = workspace
+        if not isinstance(ws, torch.Tensor) or ws.get_device() != dev:
+            _elsewhere(ws, "workspace")
+        if not ws.is_contiguous() or ws.numel() * ws.itemsize < need:
             raise ValueError("workspace must be contiguous and large enough")
+        return ws.data_ptr(), ws
+    device = torch.device("cuda", dev)
+    if stream is None:
+        handle, target = _raw_stream(dev), contextlib.nullcontext()
+    else:
+        handle = _stream(stream)
+        target = torch.cuda.stream(
+            stream if isinstance(stream, torch.cuda.Stream)
+            else torch.cuda.ExternalStream(handle, device=device))
+    with target:
+        if torch.cuda.is_current_stream_capturing():
+            ws = torch.empty(need, dtype=torch.uint8, device=device)
+            return ws.data_ptr(), ws
+    ws = _WORKSPACES.get((dev, handle))
+    if ws is None or ws.numel() < need:
+        ws = workspace_for(need, device, handle)
     return ws.data_ptr(), ws
 
 
@@ -660,15 +673,15 @@ def mbok_gemmt(d: mbok_desc, packed: torch.Tensor, dY: torch.Tensor, dX: torch.T
     workspace: True (default) uses a workspace kept for this device and
     stream (under graph capture one of the graph's own); a tensor is used as
     given; None/False runs without one."""
-    dev = _one_device(_dev(dY, "dY"), packed=packed, dX=dX)
+    dev = _first(dY, "dY")
+    m, n, K, at = d.m, d.n, d.K, d.alpha_dtype
     T = dY.shape[0]
-    lddy = _matrix(dY, "dY", T, d.m, torch.bfloat16)
-    lddx = _matrix(dX, "dX", T, d.n, torch.bfloat16)
-    with _on_device(dev) as on:
-        ws, _keep = _slices("mbok_gemmt_workspace_bytes", d, d.m, T, workspace, dev, stream)
-        _check(load_library().mbok_gemmt(
-            ctypes.byref(d), _packed(d, packed, d.m), dY.data_ptr(), T, lddy, dX.data_ptr(), lddx,
-            ws, on.stream(stream)), "mbok_gemmt")
+    lddy = _matrix(dY, "dY", dev, T, m, torch.bfloat16)
+    lddx = _matrix(dX, "dX", dev, T, n, torch.bfloat16)
+    pp = _packed(packed, dev, m, n, K, at)
+    ws, _keep = _slices("mbok_gemmt_workspace_bytes", m, n, K, at, T, workspace, dev, stream)
+    _launch(load_library().mbok_gemmt, "mbok_gemmt", dev, stream, ctypes.byref(d), pp,
+            dY.data_ptr(), T, lddy, dX.data_ptr(), lddx, ws)
 
 
 def mbok_scale_grad(d: mbok_desc, packed: torch.Tensor, dY: torch.Tensor, X: torch.Tensor,
@@ -678,16 +691,16 @@ def mbok_scale_grad(d: mbok_desc, packed: torch.Tensor, dY: torch.Tensor, X: tor
     columns of B_k (.) (dY^T X), for dY bf16 [T, m] and X bf16 [T, n].
 
     workspace: as for mbok_gemmt."""
-    dev = _one_device(_dev(dY, "dY"), packed=packed, X=X, dalpha=dalpha)
+    dev = _first(dY, "dY")
+    m, n, K, at = d.m, d.n, d.K, d.alpha_dtype
     T = dY.shape[0]
-    lddy = _matrix(dY, "dY", T, d.m, torch.bfloat16)
-    ldx = _matrix(X, "X", T, d.n, torch.bfloat16)
-    out = _vector(dalpha, "dalpha", d.K * d.m * (d.n // MBOK_GROUP), torch.float32)
-    with _on_device(dev) as on:
-        ws, _keep = _slices("mbok_scale_grad_workspace_bytes", d, d.m, T, workspace, dev, stream)
-        _check(load_library().mbok_scale_grad(
-            ctypes.byref(d), _packed(d, packed, d.m), dY.data_ptr(), T, lddy, X.data_ptr(), ldx,
-            out, int(bool(accumulate)), ws, on.stream(stream)), "mbok_scale_grad")
+    lddy = _matrix(dY, "dY", dev, T, m, torch.bfloat16)
+    ldx = _matrix(X, "X", dev, T, n, torch.bfloat16)
+    out = _vector(dalpha, "dalpha", dev, K * m * (n // MBOK_GROUP), torch.float32)
+    pp = _packed(packed, dev, m, n, K, at)
+    ws, _keep = _slices("mbok_scale_grad_workspace_bytes", m, n, K, at, T, workspace, dev, stream)
+    _launch(load_library().mbok_scale_grad, "mbok_scale_grad", dev, stream, ctypes.byref(d), pp,
+            dY.data_ptr(), T, lddy, X.data_ptr(), ldx, out, int(bool(accumulate)), ws)
 
 
 def mbok_gated_stack(d: mbok_desc) -> mbok_desc:
@@ -704,22 +717,16 @@ def mbok_gated_pack(d: mbok_desc, signs_gate: torch.Tensor, alpha_gate: torch.Te
                     stream=None) -> None:
     """signs int8 [K, m, n] + alpha [K, m, n/128] of both projections -> packed
     uint8 [mbok_packed_bytes(mbok_gated_stack(d))]."""
-    dev = _one_device(_dev(packed, "packed"), signs_gate=signs_gate, alpha_gate=alpha_gate,
-                      signs_up=signs_up, alpha_up=alpha_up)
-    ns, na = d.K * d.m * d.n, d.K * d.m * (d.n // MBOK_GROUP)
-    at = alpha_torch_dtype(d.alpha_dtype)
-    ptrs = [_vector(signs_gate, "signs_gate", ns, torch.int8),
-            _vector(alpha_gate, "alpha_gate", na, at),
-            _vector(signs_up, "signs_up", ns, torch.int8),
-            _vector(alpha_up, "alpha_up", na, at)]
-    with _on_device(dev) as on:
-        _check(load_library().mbok_gated_pack(
-            ctypes.byref(d), *ptrs, _packed(d, packed, _stacked_rows(d)), on.stream(stream)),
-            "mbok_gated_pack")
-
-
-def _stacked_rows(d: mbok_desc) -> int:
-    return 16 * ((d.m + 7) // 8)
+    dev = _first(packed, "packed")
+    m, n, K = d.m, d.n, d.K
+    ns, na, at = K * m * n, K * m * (n // MBOK_GROUP), alpha_torch_dtype(d.alpha_dtype)
+    ptrs = [_vector(signs_gate, "signs_gate", dev, ns, torch.int8),
+            _vector(alpha_gate, "alpha_gate", dev, na, at),
+            _vector(signs_up, "signs_up", dev, ns, torch.int8),
+            _vector(alpha_up, "alpha_up", dev, na, at)]
+    pp = _packed(packed, dev, 16 * ((m + 7) // 8), n, K, d.alpha_dtype)
+    _launch(load_library().mbok_gated_pack, "mbok_gated_pack", dev, stream, ctypes.byref(d),
+            *ptrs, pp)
 
 
 def mbok_gated(d: mbok_desc, packed: torch.Tensor, X: torch.Tensor, H: torch.Tensor,
@@ -727,16 +734,18 @@ def mbok_gated(d: mbok_desc, packed: torch.Tensor, X: torch.Tensor, H: torch.Ten
     """H[T, m] (bf16, overwritten) = act(X Wg^T) (.) (X Wu^T) for X bf16 [T, n];
     d describes one projection, packed is mbok_gated_pack's buffer.  pre bf16
     [T, 16 ceil(m / 8)] receives the pre-activations in the stacked order."""
-    dev = _one_device(_dev(X, "X"), packed=packed, H=H, pre=pre)
-    T, m2 = X.shape[0], _stacked_rows(d)
-    ldx = _matrix(X, "X", T, d.n, torch.bfloat16)
-    ldh = _matrix(H, "H", T, d.m, torch.bfloat16)
-    ldpre = 0 if pre is None else _matrix(pre, "pre", T, m2, torch.bfloat16)
-    with _on_device(dev) as on:
-        _check(load_library().mbok_gated(
-            ctypes.byref(d), _packed(d, packed, m2), X.data_ptr(), MBOK_BF16, T, ldx, act,
-            H.data_ptr(), ldh, None if pre is None else pre.data_ptr(), ldpre,
-            on.stream(stream)), "mbok_gated")
+    dev = _first(X, "X")
+    m, n = d.m, d.n
+    T, m2 = X.shape[0], 16 * ((m + 7) // 8)
+    ldx = _matrix(X, "X", dev, T, n, torch.bfloat16)
+    ldh = _matrix(H, "H", dev, T, m, torch.bfloat16)
+    pre_ptr, ldpre = None, 0
+    if pre is not None:
+        ldpre = _matrix(pre, "pre", dev, T, m2, torch.bfloat16)
+        pre_ptr = pre.data_ptr()
+    _launch(load_library().mbok_gated, "mbok_gated", dev, stream, ctypes.byref(d),
+            _packed(packed, dev, m2, n, d.K, d.alpha_dtype), X.data_ptr(), MBOK_BF16, T, ldx, act,
+            H.data_ptr(), ldh, pre_ptr, ldpre)
 
 
 def mbok_gated_backward(d: mbok_desc, packed: torch.Tensor, pre: torch.Tensor, dH: torch.Tensor,
@@ -748,20 +757,20 @@ def mbok_gated_backward(d: mbok_desc, packed: torch.Tensor, pre: torch.Tensor, d
     mbok_gated wrote it and dH bf16 [T, m].
 
     workspace: as for mbok_gemmt."""
-    dev = _one_device(_dev(dH, "dH"), packed=packed, pre=pre, dpre=dpre, dX=dX)
-    T, m2 = dH.shape[0], _stacked_rows(d)
-    lddh = _matrix(dH, "dH", T, d.m, torch.bfloat16)
-    ldpre = _matrix(pre, "pre", T, m2, torch.bfloat16)
-    lddpre = _matrix(dpre, "dpre", T, m2, torch.bfloat16)
-    lddx = 0 if dX is None else _matrix(dX, "dX", T, d.n, torch.bfloat16)
-    with _on_device(dev) as on:
-        ws = None
-        if dX is not None:
-            ws, _keep = _slices("mbok_gemmt_workspace_bytes", d, m2, T, workspace, dev, stream)
-        _check(load_library().mbok_gated_backward(
-            ctypes.byref(d), _packed(d, packed, m2), pre.data_ptr(), ldpre, dH.data_ptr(), lddh,
-            T, act, dpre.data_ptr(), lddpre, None if dX is None else dX.data_ptr(), lddx, ws,
-            on.stream(stream)), "mbok_gated_backward")
+    dev = _first(dH, "dH")
+    m, n, K, at = d.m, d.n, d.K, d.alpha_dtype
+    T, m2 = dH.shape[0], 16 * ((m + 7) // 8)
+    lddh = _matrix(dH, "dH", dev, T, m, torch.bfloat16)
+    ldpre = _matrix(pre, "pre", dev, T, m2, torch.bfloat16)
+    lddpre = _matrix(dpre, "dpre", dev, T, m2, torch.bfloat16)
+    dx_ptr, lddx, ws, _keep = None, 0, None, None
+    if dX is not None:
+        lddx = _matrix(dX, "dX", dev, T, n, torch.bfloat16)
+        dx_ptr = dX.data_ptr()
+        ws, _keep = _slices("mbok_gemmt_workspace_bytes", m2, n, K, at, T, workspace, dev, stream)
+    _launch(load_library().mbok_gated_backward, "mbok_gated_backward", dev, stream,
+            ctypes.byref(d), _packed(packed, dev, m2, n, K, at), pre.data_ptr(), ldpre,
+            dH.data_ptr(), lddh, T, act, dpre.data_ptr(), lddpre, dx_ptr, lddx, ws)
 
 
 def mbok_distill_desc_init(vocab: int, top: int, temperature: float = 1.0) -> mbok_distill_desc:
@@ -771,26 +780,31 @@ def mbok_distill_desc_init(vocab: int, top: int, temperature: float = 1.0) -> mb
     return d
 
 
-def _distill_args(d, Z, t_logits, t_index, t_lse, weight, dZ):
-    """The arguments both distillation calls share, checked."""
-    T = Z.shape[0]
-    zt, tt = _FLOATS.get(Z.dtype), _FLOATS.get(t_logits.dtype)
+def _distill_args(d, dev, Z, t_logits, t_index, t_lse, weight):
+    """(T, vocabulary, the arguments both distillation calls begin with), checked."""
+    vocab, top, T = d.vocab, d.top, Z.shape[0]
+    dz, dt = Z.dtype, t_logits.dtype
+    zt, tt = _FLOATS.get(dz), _FLOATS.get(dt)
     if zt is None or tt is None:
         raise ValueError("Z and t_logits must be float32, float16 or bfloat16")
-    ldz = _matrix(Z, "Z", T, d.vocab, Z.dtype)
-    ldt = _matrix(t_index, "t_index", T, d.top, torch.int32)
-    if _matrix(t_logits, "t_logits", T, d.top, t_logits.dtype) != ldt and T > 1:
+    ldz = _matrix(Z, "Z", dev, T, vocab, dz)
+    ldt = _matrix(t_index, "t_index", dev, T, top, torch.int32)
+    if _matrix(t_logits, "t_logits", dev, T, top, dt) != ldt and T > 1:
         raise ValueError("t_logits and t_index must have the same row stride")
-    lse = None if t_lse is None else _vector(t_lse, "t_lse", T, torch.float32)
-    w = None if weight is None else _vector(weight, "weight", T, torch.float32)
-    if dZ is None:
-        grad = (None, zt, 0)
-    else:
-        if dZ.dtype not in (Z.dtype, torch.bfloat16):
-            raise ValueError("dZ must have the dtype of Z or bfloat16")
-        grad = (dZ.data_ptr(), _FLOATS[dZ.dtype], _matrix(dZ, "dZ", T, d.vocab, dZ.dtype))
-    return T, (Z.data_ptr(), zt, T, ldz, t_logits.data_ptr(), tt, t_index.data_ptr(), ldt, lse,
-               w), grad
+    return T, vocab, (
+        ctypes.byref(d), Z.data_ptr(), zt, T, ldz, t_logits.data_ptr(), tt, t_index.data_ptr(),
+        ldt, None if t_lse is None else _vector(t_lse, "t_lse", dev, T, torch.float32),
+        None if weight is None else _vector(weight, "weight", dev, T, torch.float32))
+
+
+def _distill_grad(dZ, dev, T, vocab, z_dtype):
+    if not isinstance(dZ, torch.Tensor):
+        raise TypeError("dZ must be a torch.Tensor")
+    dt = dZ.dtype
+    if dt != z_dtype and dt != torch.bfloat16:
+        raise ValueError("dZ must have the dtype of Z or bfloat16")
+    ld = _matrix(dZ, "dZ", dev, T, vocab, dt)
+    return dZ.data_ptr(), _FLOATS[dt], ld
 
 
 def mbok_distill(d: mbok_distill_desc, Z: torch.Tensor, t_logits: torch.Tensor,
@@ -803,14 +817,14 @@ def mbok_distill(d: mbok_distill_desc, Z: torch.Tensor, t_logits: torch.Tensor,
     teacher's own probabilities with the rest as one class.  stats fp32 [T,
     MBOK_DISTILL_STATS] is what mbok_distill_backward takes; dZ (dtype of Z or
     bf16; may be Z) receives the gradient of sum(loss) in the same pass."""
-    dev = _one_device(_dev(Z, "Z"), t_logits=t_logits, t_index=t_index, loss=loss, stats=stats,
-                      dZ=dZ, t_lse=t_lse, weight=weight)
-    T, args, grad = _distill_args(d, Z, t_logits, t_index, t_lse, weight, dZ)
-    out = _vector(loss, "loss", T, torch.float32)
-    st = None if stats is None else _vector(stats, "stats", T * MBOK_DISTILL_STATS, torch.float32)
-    with _on_device(dev) as on:
-        _check(load_library().mbok_distill(ctypes.byref(d), *args, out, st, *grad,
-                                           on.stream(stream)), "mbok_distill")
+    dev = _first(Z, "Z")
+    _first(t_logits, "t_logits")
+    T, vocab, args = _distill_args(d, dev, Z, t_logits, t_index, t_lse, weight)
+    grad = (None, args[2], 0) if dZ is None else _distill_grad(dZ, dev, T, vocab, Z.dtype)
+    _launch(load_library().mbok_distill, "mbok_distill", dev, stream, *args,
+            _vector(loss, "loss", dev, T, torch.float32),
+            None if stats is None else _vector(stats, "stats", dev, T * MBOK_DISTILL_STATS,
+                                               torch.float32), *grad)
 
 
 def mbok_distill_backward(d: mbok_distill_desc, Z: torch.Tensor, t_logits: torch.Tensor,
@@ -819,14 +833,13 @@ def mbok_distill_backward(d: mbok_distill_desc, Z: torch.Tensor, t_logits: torch
                           weight: torch.Tensor | None = None, stream=None) -> None:
     """dZ (dtype of Z or bf16; may be Z) = dloss[t] * d loss[t] / d Z[t, :] after
     mbok_distill with stats on the same inputs; dloss fp32 [T]."""
-    dev = _one_device(_dev(Z, "Z"), t_logits=t_logits, t_index=t_index, stats=stats,
-                      dloss=dloss, dZ=_dev(dZ, "dZ"), t_lse=t_lse, weight=weight)
-    T, args, grad = _distill_args(d, Z, t_logits, t_index, t_lse, weight, dZ)
-    st = _vector(stats, "stats", T * MBOK_DISTILL_STATS, torch.float32)
-    dl = _vector(dloss, "dloss", T, torch.float32)
-    with _on_device(dev) as on:
-        _check(load_library().mbok_distill_backward(ctypes.byref(d), *args, st, dl, *grad,
-                                                    on.stream(stream)), "mbok_distill_backward")
+    dev = _first(Z, "Z")
+    _first(t_logits, "t_logits")
+    T, vocab, args = _distill_args(d, dev, Z, t_logits, t_index, t_lse, weight)
+    _launch(load_library().mbok_distill_backward, "mbok_distill_backward", dev, stream, *args,
+            _vector(stats, "stats", dev, T * MBOK_DISTILL_STATS, torch.float32),
+            _vector(dloss, "dloss", dev, T, torch.float32),
+            *_distill_grad(dZ, dev, T, vocab, Z.dtype))
 
 
 # ---------------------------------------------------------------- conveniences
