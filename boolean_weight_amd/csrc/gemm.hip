@@ -174,7 +174,7 @@ __global__ void __launch_bounds__(GEMM_THREADS) gemm_mfma_kernel(
           for (int k = 0; k < K; ++k) w[k] = (kk >> 1) ? R.w[k].y : R.w[k].x;
           word_selectors<K>(w, V);
         }
-        unpack_quads(V, kk & 1, L, out);
+        unpack_quads<K>(V, kk & 1, L, out);
       } else {
         uint32_t w[K], o32[16];
 #pragma unroll
@@ -412,9 +412,9 @@ __device__ __forceinline__ void mfma8_tile(const uint32_t* __restrict__ bits,
         uint32_t out[4];
         if (K <= 3) {
           if (JB == 2)
-            unpack_two_quads(V, kk >> 1, 2 * (kk & 1), L, out);
+            unpack_two_quads<K>(V, kk >> 1, 2 * (kk & 1), L, out);
           else
-            unpack_two_quads(V, h, 2 * kk, L, out);
+            unpack_two_quads<K>(V, h, 2 * kk, L, out);
         } else {
           uint32_t o32[16];
           float af[K];

@@ -35,8 +35,8 @@ typedef __attribute__((ext_vector_type(4))) __bf16 bf16x4;
 
 constexpr int kBN = 256;       // columns per workgroup tile
 constexpr int kThreads = 512;  // 8 wavefronts
-constexpr int kAStride = 72;   // bf16 elements per LDS row of dY (64 + 8)
-constexpr int kWStride = 272;  // bf16 elements per LDS row of W_hat (256 + 16)
+constexpr int kAStride = kRowBlock;  // bf16 elements per LDS row of dY
+constexpr int kWStride = kBN;        // and of W_hat
 
 // Token rows of a tile and how the 8 wavefronts share it: WT wavefronts along
 // the tokens, 8 / WT along the columns, each TI x TJ blocks of 32 x 32.
@@ -49,15 +49,16 @@ struct Tile {
   static constexpr size_t kLds = 2 * (size_t)(kA + kW) * sizeof(uint16_t);
 };
 
-// 8 rows (k0 .. k0 + 7) of one column per lane: two transposing reads
-__device__ __forceinline__ bf16x8 read_tr(const uint16_t* p) {
+// 8 rows (k0 .. k0 + 7) of one column per lane: two transposing reads, of rows
+// k0 .. k0 + 3 and k0 + 4 .. k0 + 7
+__device__ __forceinline__ bf16x8 read_tr(const uint16_t* p, const uint16_t* p4) {
   typedef __attribute__((address_space(3))) i16x4 lds_i16x4;
   const i16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4*)p);
-  const i16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4*)(p + 4 * kWStride));
+  const i16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4*)p4);
   return __builtin_bit_cast(bf16x8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
 }
 
-template <typename AT, int K, typename TL, bool PART>
+template <typename AT, int K, typename TL, bool PART, bool ALIGNED>
 __global__ void __launch_bounds__(kThreads) gemmt_kernel(
     const uint32_t* __restrict__ bits, const AT* __restrict__ scales,
     const uint16_t* __restrict__ dY, int64_t lddy, uint16_t* __restrict__ dX, int64_t lddx,
@@ -87,50 +88,71 @@ __global__ void __launch_bounds__(kThreads) gemmt_kernel(
   // unpack role: row `lane` of the step's block, 32-column word `wave` of the tile
   const int gw = min(j0 / kGroup + (wave >> 2), G - 1);
   const int uword = wave & 3;
-  // dY copy role: piece u = token tid / 8 + 64 u, rows 8 (tid % 8) ..
-  const int apart = tid & 7;
-  const bool a_live = BT * 8 >= kThreads || tid < BT * 8;
-  const uint16_t* arow[NA];
+  // dY copy role: piece u = token tid / 8 + 64 u, at LDS position tid % 8 of
+  // its row, which holds the 8 rows apart = position ^ (token / 2 & 7) ..
+  const int arow8 = tid >> 3;
+  const int apart = (tid & 7) ^ ((arow8 >> 1) & 7);
+  const bool a_live = BT * 8 >= kThreads || wave < BT * 8 / kWave;  // whole wavefronts
+  // byte offsets inside the tile's tokens (ALIGNED: 32 bits hold them)
+  const uint16_t* tile_dy = dY + (int64_t)t0 * lddy;
+  typename std::conditional<ALIGNED, uint32_t, int64_t>::type arow[NA];
 #pragma unroll
   for (int u = 0; u < NA; ++u) {
-    const int t = min(t0 + (tid >> 3) + 64 * u, T - 1);  // extra tokens are never stored
-    arow[u] = dY + (int64_t)t * lddy + 8 * apart;
+    const int t = min(arow8 + 64 * u, T - 1 - t0);  // extra tokens are never stored
+    arow[u] = (int64_t)t * lddy * 2 + 16 * apart;
   }
+  auto dy_at = [&](int u, int rb) {
+    return reinterpret_cast<const uint16_t*>(reinterpret_cast<const char*>(tile_dy) + arow[u]) +
+           (int64_t)rb * kRowBlock;
+  };
+  auto abuf = [&](int b) { return smem + b * (TL::kA + TL::kW); };
+  auto wbuf = [&](int b) { return smem + b * (TL::kA + TL::kW) + TL::kA; };
 
   struct StepRegs {
-    u32x4 x[NA];
+    u32x4 x[ALIGNED ? 1 : NA];
     uint32_t w[K];
     AT a[K];
   };
   StepRegs R0, R1;
   auto load_w = [&](int rb, StepRegs& R) {
+    // the wavefront's chunks: uniform bases, so only 32-bit lane offsets are vectors
     const int64_t c = ((int64_t)rb * G + gw) * K * kRowBlock;
+    const uint32_t* wb = bits + c * 4 + uword;
+    const AT* sb = scales + c;
 #pragma unroll
     for (int k = 0; k < K; ++k) {
-      R.w[k] = bits[(c + k * kRowBlock + lane) * 4 + uword];
-      R.a[k] = scales[c + k * kRowBlock + lane];
+      R.w[k] = wb[(uint32_t)(lane + k * kRowBlock) * 4u];
+      R.a[k] = sb[(uint32_t)(lane + k * kRowBlock)];
     }
   };
-  auto load = [&](int rb, StepRegs& R) {
+  // dY of a whole row block, to its LDS buffer: straight from memory when its
+  // rows are 16-byte aligned (the copy is in flight until the next barrier),
+  // else by way of registers
+  auto load_a = [&](int rb, int b, StepRegs& R) {
     if (a_live) {
 #pragma unroll
-      for (int u = 0; u < NA; ++u)
-        R.x[u] = *reinterpret_cast<const u32x4_any*>(arow[u] + (int64_t)rb * kRowBlock);
+      for (int u = 0; u < NA; ++u) {
+        if constexpr (ALIGNED) {
+          copy_to_lds(tile_dy + (int64_t)rb * kRowBlock, arow[u],
+                      abuf(b) + (u * kThreads + wave * 64) * 8);
+        } else {
+          R.x[u] = *reinterpret_cast<const u32x4_any*>(dy_at(u, rb));
+        }
+      }
     }
-    load_w(rb, R);
   };
   // the partial last block: dY element by element inside its m columns
-  auto load_tail = [&](int rb, StepRegs& R) {
+  auto store_a_tail = [&](int rb, int b) {
+    if (!a_live) return;
     const int i0 = rb * kRowBlock + 8 * apart;
 #pragma unroll
     for (int u = 0; u < NA; ++u) {
       uint32_t e[8];
 #pragma unroll
-      for (int q = 0; q < 8; ++q)
-        e[q] = a_live && i0 + q < m ? arow[u][(int64_t)rb * kRowBlock + q] : 0u;
-      R.x[u] = u32x4{e[0] | e[1] << 16, e[2] | e[3] << 16, e[4] | e[5] << 16, e[6] | e[7] << 16};
+      for (int q = 0; q < 8; ++q) e[q] = i0 + q < m ? dy_at(u, rb)[q] : 0u;
+      *reinterpret_cast<u32x4*>(abuf(b) + (u * kThreads + tid) * 8) =
+          u32x4{e[0] | e[1] << 16, e[2] | e[3] << 16, e[4] | e[5] << 16, e[6] | e[7] << 16};
     }
-    load_w(rb, R);
   };
 
   f32x16 acc[TI][TJ];
@@ -142,99 +164,168 @@ __global__ void __launch_bounds__(kThreads) gemmt_kernel(
       for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.f;
 
   const int wt = wave / TL::WN, wn = wave % TL::WN;
-  // dY operand: token lane % 32, rows 8 (lane / 32) ..; W_hat operand: see read_tr
-  const int aoff = (wt * 32 * TI + (lane & 31)) * kAStride + (lane >> 5) * 8;
-  const int woff = (8 * (lane >> 5) + ((lane & 15) >> 2)) * kWStride + wn * 32 * TJ +
-                   16 * ((lane >> 4) & 1) + 4 * (lane & 3);
-  auto abuf = [&](int b) { return smem + b * (TL::kA + TL::kW); };
-  auto wbuf = [&](int b) { return smem + b * (TL::kA + TL::kW) + TL::kA; };
-
-  Levels L;
-  uint32_t V[4];
-  auto begin_store = [&](const StepRegs& R) {
-    if (K <= 3) {
-      float af[K];
-#pragma unroll
-      for (int k = 0; k < K; ++k) af[k] = alpha_to_f32<AT>(R.a[k]);
-      L = make_levels<K, false>(af);
-      word_selectors<K>(R.w, V);
-    }
+  // LDS positions.  A dY row is 8 pieces of 16 bytes, piece c of token r at
+  // position c ^ (r / 2 & 7); a W_hat row is 32 pieces, piece c of row r at c ^
+  // (4 (r & 3) + (r / 4 & 3)).  The 64 banks of LDS are 16 such positions, and
+  // the 16 lanes of a 16-byte access (32 of an 8-byte one) then meet each once.
+  // dY operand: token lane % 32, rows 16 q + 8 (lane / 32) ..; W_hat operand: see
+  // read_tr, rows 16 q + 8 (lane / 32) + 4 h ..
+  const int arr = (wt * 32 * TI + (lane & 31)) * kAStride;
+  const int wrow = (8 * (lane >> 5) + ((lane & 15) >> 2)) * kWStride + 4 * (lane & 1);
+  const int wpiece = (2 * ((lane >> 4) & 1) + ((lane & 3) >> 1)) ^
+                     (4 * ((lane & 15) >> 2) + 2 * (lane >> 5));
+  auto aoff = [&](int q) { return arr + 8 * ((2 * q + (lane >> 5)) ^ ((lane >> 1) & 7)); };
+  auto woff = [&](int j, int h) {
+    return wrow + 4 * h * kWStride + 8 * ((wn * 4 * TJ + 4 * j) ^ wpiece ^ h);
   };
-  // quarter q of a step's stores: 8 columns of W_hat, up to one dY piece
-  auto store = [&](int b, const StepRegs& R, int q) {
-    if (q < NA && a_live)
-      *reinterpret_cast<u32x4*>(abuf(b) + ((tid >> 3) + 64 * q) * kAStride + 8 * apart) = R.x[q];
-    uint32_t out[4];
-    if (K <= 3) {
-      unpack_two_quads(V, q >> 1, 2 * (q & 1), L, out);
-    } else {
-      float af[K];
-      uint32_t o32[16];
+
+  // One step's W_hat, from its signs and scales to LDS, in kChunks pieces of a
+  // few vector instructions each (K = 4: in four): levels, selectors, then
+  // half a quad at a time.
+  constexpr int kChunks = 24;
+  float af[K];
+  uint32_t pairs[2], V[4], lo = 0, hi = 0, out[4];
+  Levels L;
+  auto w_piece = [&](int b, int q) {
+    const int piece = (wave * 4 + q) ^ (4 * (lane & 3) + ((lane >> 2) & 3));
+    *reinterpret_cast<u32x4*>(wbuf(b) + lane * kWStride + 8 * piece) =
+        u32x4{out[0], out[1], out[2], out[3]};
+  };
+  auto form = [&](int b, const StepRegs& R, int c) {
+    if (c == 0) {
 #pragma unroll
       for (int k = 0; k < K; ++k) af[k] = alpha_to_f32<AT>(R.a[k]);
+    }
+    if constexpr (!ALIGNED) {
+      if (c < 4 && c < NA && a_live)
+        *reinterpret_cast<u32x4*>(abuf(b) + (c * kThreads + tid) * 8) = R.x[c];
+    }
+    if constexpr (K <= 3) {
+      if (c < 2) pairs[c] = upper_pair<K>(af, c);
+      if (c == 2) L = pack_levels<K>(pairs[0], pairs[1]);
+      if (c >= 3 && c < 6) word_selectors_part<K>(R.w, V, c - 3);
+      if (c >= 8) {
+        const int quad = (c - 8) >> 1;  // of the word; piece quad / 2
+        if ((c & 1) == 0) {
+          const uint32_t sel = quad_selector<K>(V, quad >> 2, quad & 3);
+          lo = quad_low(L, sel);
+          hi = quad_high(L, sel);
+        } else {
+          quad_pairs(lo, hi, out + 2 * (quad & 1));
+          if (quad & 1) w_piece(b, quad >> 1);
+        }
+      }
+    } else if (c >= 8 && (c & 3) == 0) {
+      uint32_t o32[16];
+      const int q = (c - 8) >> 2;
       unpack_word_k4<false>(R.w, af, o32);
 #pragma unroll
       for (int e = 0; e < 4; ++e) out[e] = o32[4 * q + e];
-    }
-    *reinterpret_cast<u32x4*>(wbuf(b) + lane * kWStride + wave * 32 + 8 * q) =
-        u32x4{out[0], out[1], out[2], out[3]};
-  };
-  // products of buffer b; between(q) runs after sub-step q
-  auto mma = [&](int b, auto&& between) {
-    const uint16_t* as = abuf(b) + aoff;
-    const uint16_t* ws = wbuf(b) + woff;
-    bf16x8 pa[2][TI], pb[2][TJ];
-    auto frags = [&](int q) {
-#pragma unroll
-      for (int i = 0; i < TI; ++i)
-        pa[q & 1][i] = *reinterpret_cast<const bf16x8*>(as + i * 32 * kAStride + 16 * q);
-#pragma unroll
-      for (int j = 0; j < TJ; ++j) pb[q & 1][j] = read_tr(ws + 16 * q * kWStride + 32 * j);
-    };
-    frags(0);
-#pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      if (q < 3) frags(q + 1);
-#pragma unroll
-      for (int j = 0; j < TJ; ++j)
-#pragma unroll
-        for (int i = 0; i < TI; ++i)
-          acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(pa[q & 1][i], pb[q & 1][j],
-                                                              acc[i][j], 0, 0, 0);
-      between(q);
+      w_piece(b, q);
     }
   };
-  auto store_all = [&](int b, const StepRegs& R) {
-    begin_store(R);
+  auto form_all = [&](int b, const StepRegs& R) {
 #pragma unroll
-    for (int q = 0; q < 4; ++q) store(b, R, q);
+    for (int c = 0; c < kChunks; ++c) form(b, R, c);
+  };
+
+  bf16x8 pa[2][TI], pb[2][TJ];
+  auto read_a = [&](int b, int q, int i) {
+    pa[q & 1][i] = *reinterpret_cast<const bf16x8*>(abuf(b) + aoff(q) + i * 32 * kAStride);
+  };
+  auto read_w = [&](int b, int q, int j) {
+    pb[q & 1][j] = read_tr(wbuf(b) + woff(j, 0) + 16 * q * kWStride,
+                           wbuf(b) + woff(j, 1) + 16 * q * kWStride);
+  };
+  // Products of sub-step q (16 rows), one at a time; after product x the
+  // operands of sub-step q + 1 whose turn it is are read from buffer b (next
+  // sub-step's or the next step's), and work(x) runs.  Each product takes the
+  // matrix core 32 cycles, in which the wavefront issues up to 8 other vector
+  // instructions; the fences keep the compiler from gathering those (it put
+  // 40 in a row, and the wavefronts of a SIMD, in step after a barrier, then
+  // left the matrix core idle: 4096 x 11008, 2048 tokens, 228 -> 210 us).
+  constexpr int NX = TI * TJ;
+  auto products = [&](int q, int b, int nq, auto&& work) {
+#pragma unroll
+    for (int x = 0; x < NX; ++x) {
+      const int i = x % TI, j = x / TI;
+      acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(pa[q & 1][i], pb[q & 1][j], acc[i][j], 0,
+                                                          0, 0);
+      if (nq >= 0) {
+        if (x < TJ) read_w(b, nq, x);
+        if (x < TI) read_a(b, nq, x);
+        if (x == NX - 1) {
+#pragma unroll
+          for (int y = NX; y < TI; ++y) read_a(b, nq, y);
+        }
+      }
+      work(x);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+  };
+  auto first_operands = [&](int b) {
+#pragma unroll
+    for (int j = 0; j < TJ; ++j) read_w(b, 0, j);
+#pragma unroll
+    for (int i = 0; i < TI; ++i) read_a(b, 0, i);
   };
 
   if (S > 0) {
     const int last = full_end - 1;
-    load(rb0, R0);
-    load(min(rb0 + 1, last), R1);
-    store_all(0, R0);
+    auto at = [&](int s) { return min(rb0 + s, last); };  // the extra steps at the end are unused
+    load_a(at(0), 0, R0);
+    load_w(at(0), R0);
+    if constexpr (!ALIGNED) load_a(at(1), 1, R1);
+    load_w(at(1), R1);
+    form_all(0, R0);
+    copies_done();
     __syncthreads();
-    // step s is multiplied from buffer s % 2 while step s + 1 is stored and
-    // step s + 2 loaded (indices clamped at the end; the extras are unused)
+    load_a(ALIGNED ? at(1) : at(2), 1, R0);
+    load_w(at(2), R0);
+    first_operands(0);
+    // Step s: its products from buffer b = s % 2, while W_hat of step s + 1 is
+    // formed from R in the other buffer.  The barrier stands before the last
+    // quarter of the products, whose operands are in registers by then: the
+    // next step's first operands, and the copies and loads of the steps
+    // after it, are in flight during that quarter.
+    auto step = [&](int s, int b, StepRegs& R) {
+#pragma unroll
+      for (int q = 0; q < 3; ++q)
+        products(q, b, q + 1, [&](int x) {
+          const int y = q * NX + x;
+#pragma unroll
+          for (int c = 0; c < kChunks; ++c)
+            if (c * 3 * NX / kChunks == y) form(b ^ 1, R, c);
+        });
+      copies_done();
+      __syncthreads();
+      load_a(ALIGNED ? at(s + 2) : at(s + 3), b, R);
+      load_w(at(s + 3), R);
+      __builtin_amdgcn_sched_barrier(0);
+      products(3, b ^ 1, 0, [](int) {});
+    };
     for (int s = 0; s < S; s += 2) {
-      load(min(rb0 + s + 2, last), R0);
-      begin_store(R1);
-      mma(0, [&](int q) { store(1, R1, q); });
-      __syncthreads();
+      step(s, 0, R1);
       if (s + 1 >= S) break;
-      load(min(rb0 + s + 3, last), R1);
-      begin_store(R0);
-      mma(1, [&](int q) { store(0, R0, q); });
-      __syncthreads();
+      step(s + 1, 1, R0);
     }
+    copies_done();
   }
   if (tail) {
-    load_tail(full_end, R0);
-    store_all(0, R0);
     __syncthreads();
-    mma(0, [](int) {});
+    load_w(full_end, R0);
+    store_a_tail(full_end, 0);
+    if constexpr (!ALIGNED) {
+      // form() stores the registers' dY too: here it is what is in place already
+#pragma unroll
+      for (int u = 0; u < NA; ++u)
+        if (a_live) R0.x[u] = *reinterpret_cast<const u32x4*>(abuf(0) + (u * kThreads + tid) * 8);
+    }
+    form_all(0, R0);
+    __syncthreads();
+    first_operands(0);
+#pragma unroll
+    for (int q = 0; q < 4; ++q) products(q, 0, q < 3 ? q + 1 : -1, [](int) {});
   }
 
   // C layout: lane l, register r -> token 8 (r / 4) + 4 (l / 32) + r % 4, column l % 32
@@ -300,6 +391,9 @@ int gemmt_slices(const Geom& geo, int64_t T) {
 template <typename AT, int K>
 int launch_k(const Geom& geo, const void* packed, const uint16_t* dY, int64_t T, int64_t lddy,
              uint16_t* dX, int64_t lddx, float* part, int slices, hipStream_t stream) {
+  // straight copies to LDS take 16-byte aligned rows at 32-bit offsets
+  const bool aligned =
+      ((uintptr_t)dY & 15) == 0 && (lddy % 8) == 0 && lddy < (int64_t(1) << 32) / 512;
   const uint32_t* bits = reinterpret_cast<const uint32_t*>(packed);
   const AT* scales = reinterpret_cast<const AT*>(reinterpret_cast<const char*>(packed) +
                                                  geo.bits_bytes);
@@ -307,9 +401,12 @@ int launch_k(const Geom& geo, const void* packed, const uint16_t* dY, int64_t T,
     using TL = decltype(tl);
     constexpr bool P = decltype(partial)::value;
     const int64_t blocks = (int64_t)((geo.n + kBN - 1) / kBN) * ((T + TL::BT - 1) / TL::BT) * slices;
-    hipLaunchKernelGGL((gemmt_kernel<AT, K, TL, P>), dim3((unsigned)blocks), dim3(kThreads),
-                       TL::kLds, stream, bits, scales, dY, lddy, dX, lddx, part, (int)T, geo.m,
-                       geo.n, geo.RB, slices);
+    auto launch = [&](auto kernel) {
+      hipLaunchKernelGGL(kernel, dim3((unsigned)blocks), dim3(kThreads), TL::kLds, stream, bits,
+                         scales, dY, lddy, dX, lddx, part, (int)T, geo.m, geo.n, geo.RB, slices);
+    };
+    if (aligned) launch(gemmt_kernel<AT, K, TL, P, true>);
+    else launch(gemmt_kernel<AT, K, TL, P, false>);
   };
   auto by_tile = [&](auto partial) {
     switch (tile_tokens(T)) {

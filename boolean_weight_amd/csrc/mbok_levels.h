@@ -14,6 +14,24 @@ typedef __attribute__((ext_vector_type(16))) float f32x16;
 // struct member went through scratch memory)
 typedef __attribute__((ext_vector_type(4))) uint32_t u32x4;
 
+// Copies 16 bytes per lane from memory to LDS without passing registers: lane l
+// of the wavefront writes dst + 16 l (dst is the wavefront's).  The copy is in
+// flight until copies_done(); a barrier after that shows it to the workgroup.
+// (The compiler's builtin for this makes it wait for the copy before the next
+// transposing LDS read of any buffer, i.e. at once.)  The wait counts the
+// compiler inserts for its own loads stay right: loads return in order, so
+// an uncounted copy in flight only makes a wait longer.
+// The source is base (the wavefront's) + off bytes (the lane's).
+__device__ __forceinline__ void copy_to_lds(const void* base, uint32_t off, const uint16_t* dst) {
+  const uint32_t at =
+      (uint32_t)(uintptr_t)(const __attribute__((address_space(3))) uint16_t*)dst;
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2"
+               :
+               : "s"(__builtin_amdgcn_readfirstlane(at)), "v"(off), "s"(base)
+               : "memory");
+}
+__device__ __forceinline__ void copies_done() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
+
 __device__ __forceinline__ uint32_t bf16_pair(float a, float b) {
   const __bf16 ha = (__bf16)a, hb = (__bf16)b;  // nearest-even
   return (uint32_t)__builtin_bit_cast(uint16_t, ha) |
@@ -35,48 +53,114 @@ __device__ __forceinline__ float bf16_residue(float v) { return v - (float)(__bf
 // LO = false: the levels rounded to bf16 (the default product).  LO = true:
 // the bf16 rounding of each level's residue, for the second pass of the
 // two-pass product (hi + lo levels, ~2^-16 relative error per weight).
+//
+// Flipping every sign negates a level: only those with the highest kernel's
+// sign set (+) are summed and rounded, and the others are their bytes in
+// reverse order with the sign bit flipped (rounding is symmetric).
+
+// Levels 2 p and 2 p + 1 of the upper half (K = 3: p = 0, 1 for levels 4 .. 7;
+// K = 2: levels 2, 3; K = 1: level 1 twice) as a bf16 pair.
+template <int K, bool LO = false>
+__device__ __forceinline__ uint32_t upper_pair(const float* a, int p) {
+  float l[2];
+  if (K == 1) {
+    l[0] = l[1] = a[0];
+  } else {
+    const float s = K == 2 ? a[1] : (p ? a[2] + a[1] : a[2] - a[1]);
+    l[0] = s - a[0];
+    l[1] = s + a[0];
+  }
+  return LO ? bf16_pair(bf16_residue(l[0]), bf16_residue(l[1])) : bf16_pair(l[0], l[1]);
+}
+// v_perm_b32(s0, s1, sel): selector byte 0..3 picks s1 bytes, 4..7 s0 bytes
+template <int K>
+__device__ __forceinline__ Levels pack_levels(uint32_t p0, uint32_t p1) {
+  Levels L;
+  if (K == 3) {  // p0 = levels 4, 5; p1 = levels 6, 7
+    L.lo_b = __builtin_amdgcn_perm(p1, p0, 0x06040200u);
+    L.hi_b = __builtin_amdgcn_perm(p1, p0, 0x07050301u);
+    L.lo_a = __builtin_amdgcn_perm(p1, p0, 0x00020406u);
+    L.hi_a = __builtin_amdgcn_perm(p1, p0, 0x01030507u) ^ 0x80808080u;
+  } else {  // p0 = levels 2, 3 (K = 1: level 1 twice)
+    L.lo_a = __builtin_amdgcn_perm(p0, p0, K == 2 ? 0x02000002u : 0x00000000u);
+    L.hi_a = __builtin_amdgcn_perm(p0, p0, K == 2 ? 0x03010103u : 0x01010101u) ^
+             (K == 2 ? 0x00008080u : 0x00000080u);
+    L.lo_b = L.hi_b = 0u;
+  }
+  return L;
+}
 template <int K, bool LO = false>
 __device__ __forceinline__ Levels make_levels(const float* a) {
-  float l[8];
+  return pack_levels<K>(upper_pair<K, LO>(a, 0), K == 3 ? upper_pair<K, LO>(a, 1) : 0u);
+}
+
+// Selector words of one 32-column sign word per kernel: bits 0 .. K - 1 of
+// V[b]'s nibble 2e + a are the level index of quad q = 4a + b, element e (the
+// nibble's other bits are other quads').  Two words are merged for two b at a
+// time.
+__device__ __forceinline__ uint32_t bit_select(uint32_t mask, uint32_t a, uint32_t b) {
+  return (a & mask) | (b & ~mask);  // one v_bfi_b32
+}
+// part 0, 1, 2 in turn (V holds what is between them)
+template <int K>
+__device__ __forceinline__ void word_selectors_part(const uint32_t* w, uint32_t* V, int part) {
+  if (K == 1) {
+    if (part == 0) {
 #pragma unroll
-  for (int idx = 0; idx < 8; ++idx) {
-    float v = (idx & 1) ? a[0] : -a[0];
-    if (K >= 2) v += (idx & 2) ? a[1] : -a[1];
-    if (K >= 3) v += (idx & 4) ? a[2] : -a[2];
-    l[idx] = LO ? bf16_residue(v) : v;
+      for (int b = 0; b < 4; ++b) V[b] = w[0] >> b;
+    }
+    return;
   }
-  const uint32_t p01 = bf16_pair(l[0], l[1]), p23 = bf16_pair(l[2], l[3]);
-  const uint32_t p45 = bf16_pair(l[4], l[5]), p67 = bf16_pair(l[6], l[7]);
-  Levels L;
-  // v_perm_b32(s0, s1, sel): selector byte 0..3 picks s1 bytes, 4..7 s0 bytes
-  L.lo_a = __builtin_amdgcn_perm(p23, p01, 0x06040200u);
-  L.hi_a = __builtin_amdgcn_perm(p23, p01, 0x07050301u);
-  L.lo_b = __builtin_amdgcn_perm(p67, p45, 0x06040200u);
-  L.hi_b = __builtin_amdgcn_perm(p67, p45, 0x07050301u);
-  return L;
+  if (part == 0) {
+    V[0] = bit_select(0x55555555u, w[0], w[1] << 1);  // b = 0, 2
+    V[1] = bit_select(0x55555555u, w[0] >> 1, w[1]);  // b = 1, 3
+  }
+  if (part == 1) {
+    V[2] = K == 3 ? bit_select(0x33333333u, V[0] >> 2, w[2]) : V[0] >> 2;
+    if (K == 3) V[0] = bit_select(0x33333333u, V[0], w[2] << 2);
+  }
+  if (part == 2) {
+    V[3] = K == 3 ? bit_select(0x33333333u, V[1] >> 2, w[2] >> 1) : V[1] >> 2;
+    if (K == 3) V[1] = bit_select(0x33333333u, V[1], w[2] << 1);
+  }
+}
+template <int K>
+__device__ __forceinline__ void word_selectors(const uint32_t* w, uint32_t* V) {
+#pragma unroll
+  for (int p = 0; p < 3; ++p) word_selectors_part<K>(w, V, p);
+}
+
+// Level indices of quad 4 a + b, one per byte
+template <int K>
+__device__ __forceinline__ uint32_t quad_selector(const uint32_t* V, int a, int b) {
+  return (a ? V[b] >> 4 : V[b]) & (K == 1 ? 0x01010101u : K == 2 ? 0x03030303u : 0x07070707u);
+}
+// Low and high bytes of the quad's 4 columns, and the columns as two bf16 pairs
+__device__ __forceinline__ uint32_t quad_low(const Levels& L, uint32_t sel) {
+  return __builtin_amdgcn_perm(L.lo_b, L.lo_a, sel);
+}
+__device__ __forceinline__ uint32_t quad_high(const Levels& L, uint32_t sel) {
+  return __builtin_amdgcn_perm(L.hi_b, L.hi_a, sel);
+}
+__device__ __forceinline__ void quad_pairs(uint32_t lo, uint32_t hi, uint32_t* out) {
+  out[0] = __builtin_amdgcn_perm(hi, lo, 0x05010400u);
+  out[1] = __builtin_amdgcn_perm(hi, lo, 0x07030602u);
+}
+template <int K>
+__device__ __forceinline__ void unpack_quad(const uint32_t* V, int a, int b, const Levels& L,
+                                            uint32_t* out) {
+  const uint32_t sel = quad_selector<K>(V, a, b);
+  quad_pairs(quad_low(L, sel), quad_high(L, sel), out);
 }
 
 // Unpack one 32-column sign word per kernel (w[k]) into 32 bf16 weights in
 // natural column order: out[2q], out[2q+1] hold columns 4q..4q+3.
 template <int K>
 __device__ __forceinline__ void unpack_word(const uint32_t* w, const Levels& L, uint32_t* out) {
-  constexpr uint32_t M = 0x11111111u;
+  uint32_t V[4];
+  word_selectors<K>(w, V);
 #pragma unroll
-  for (int b = 0; b < 4; ++b) {
-    // nibble j = 2e + a of V holds the level index of quad q = 4a + b, element e
-    uint32_t V = (w[0] >> b) & M;
-    if (K >= 2) V |= ((w[1] >> b) & M) << 1;
-    if (K >= 3) V |= ((w[2] >> b) & M) << 2;
-#pragma unroll
-    for (int a = 0; a < 2; ++a) {
-      const int q = 4 * a + b;
-      const uint32_t sel = (a ? (V >> 4) : V) & 0x0f0f0f0fu;
-      const uint32_t lo = __builtin_amdgcn_perm(L.lo_b, L.lo_a, sel);
-      const uint32_t hi = __builtin_amdgcn_perm(L.hi_b, L.hi_a, sel);
-      out[2 * q] = __builtin_amdgcn_perm(hi, lo, 0x05010400u);
-      out[2 * q + 1] = __builtin_amdgcn_perm(hi, lo, 0x07030602u);
-    }
-  }
+  for (int q = 0; q < 8; ++q) unpack_quad<K>(V, q >> 2, q & 3, L, out + 2 * q);
 }
 
 // K = 4 (16 levels): direct fp32 sums, then bf16 (LO: their residues).
@@ -97,44 +181,19 @@ __device__ __forceinline__ void unpack_word_k4(const uint32_t* w, const float* a
   }
 }
 
-// Selector words of one 32-column sign word per kernel: V[b] nibble 2e + a is
-// the level index of quad q = 4a + b, element e (see unpack_word).
-template <int K>
-__device__ __forceinline__ void word_selectors(const uint32_t* w, uint32_t* V) {
-  constexpr uint32_t M = 0x11111111u;
-#pragma unroll
-  for (int b = 0; b < 4; ++b) {
-    uint32_t v = (w[0] >> b) & M;
-    if (K >= 2) v |= ((w[1] >> b) & M) << 1;
-    if (K >= 3) v |= ((w[2] >> b) & M) << 2;
-    V[b] = v;
-  }
-}
-
 // Quads 4a .. 4a+3 of a word (16 columns 16a .. 16a+15) as 8 bf16 pairs.
+template <int K>
 __device__ __forceinline__ void unpack_quads(const uint32_t* V, int a, const Levels& L,
                                              uint32_t* out) {
 #pragma unroll
-  for (int b = 0; b < 4; ++b) {
-    const uint32_t sel = (a ? (V[b] >> 4) : V[b]) & 0x0f0f0f0fu;
-    const uint32_t lo = __builtin_amdgcn_perm(L.lo_b, L.lo_a, sel);
-    const uint32_t hi = __builtin_amdgcn_perm(L.hi_b, L.hi_a, sel);
-    out[2 * b] = __builtin_amdgcn_perm(hi, lo, 0x05010400u);
-    out[2 * b + 1] = __builtin_amdgcn_perm(hi, lo, 0x07030602u);
-  }
+  for (int b = 0; b < 4; ++b) unpack_quad<K>(V, a, b, L, out + 2 * b);
 }
 
+template <int K>
 __device__ __forceinline__ void unpack_two_quads(const uint32_t* V, int a, int b0, const Levels& L,
                                                  uint32_t* out) {
 #pragma unroll
-  for (int bb = 0; bb < 2; ++bb) {
-    const int b = b0 + bb;
-    const uint32_t sel = (a ? (V[b] >> 4) : V[b]) & 0x0f0f0f0fu;
-    const uint32_t lo = __builtin_amdgcn_perm(L.lo_b, L.lo_a, sel);
-    const uint32_t hi = __builtin_amdgcn_perm(L.hi_b, L.hi_a, sel);
-    out[2 * bb] = __builtin_amdgcn_perm(hi, lo, 0x05010400u);
-    out[2 * bb + 1] = __builtin_amdgcn_perm(hi, lo, 0x07030602u);
-  }
+  for (int bb = 0; bb < 2; ++bb) unpack_quad<K>(V, a, b0 + bb, L, out + 2 * bb);
 }
 
 // Tile at position p of the XCD-blocked order: pairs of token tiles, sweeping

@@ -10,7 +10,8 @@
 // columns: one row block and one scale group each) and contracts it with the
 // signs in registers; dW never leaves them.  The contraction runs over the
 // tokens in steps of 64; both operands are token-major, so a step's dY and X
-// tiles are copied to LDS as they are (double-buffered) and both matrix
+// tiles are copied to LDS as they are, without passing registers where they are
+// aligned and whole (double-buffered), and both matrix
 // operands (8 consecutive tokens of one row or column per lane) are read with
 // the transposing LDS load: of 16 lanes, lane s supplies the address of 4
 // columns 4 (s & 3) .. of token s >> 2, and receives column s of the 4 tokens.
@@ -38,22 +39,26 @@ typedef __attribute__((ext_vector_type(4))) short i16x4;
 constexpr int kTile = 256;     // rows and columns of a tile
 constexpr int kSteps = 64;     // tokens per step
 constexpr int kThreads = 512;
-constexpr int kStride = 272;   // bf16 elements per LDS row (256 + 16)
-constexpr int kBuf = kSteps * kStride;
+// LDS image of a step's 64 tokens x 256 columns: pairs of tokens, each 1 KB of
+// 64-byte granules (32 columns) alternating between its two tokens and 128
+// bytes of padding, so that a granule of four consecutive tokens covers the 64
+// banks once and every operand's address is the lane's plus a constant.
+constexpr int kPair = 576;                    // bf16 elements per pair of tokens
+constexpr int kBuf = kSteps / 2 * kPair;
 constexpr size_t kLdsBytes = 4 * (size_t)kBuf * sizeof(uint16_t);
 static_assert(kLdsBytes >= 8 * MBOK_MAX_K * kRowBlock * 16, "the sign chunks fit the buffers");
 
-// 8 tokens of one column per lane: two transposing reads
+// 8 tokens of one column per lane: two transposing reads, of 4 tokens each
 __device__ __forceinline__ bf16x8 read_tr(const uint16_t* p) {
   typedef __attribute__((address_space(3))) i16x4 lds_i16x4;
   const i16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4*)p);
-  const i16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4*)(p + 4 * kStride));
+  const i16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4*)(p + 2 * kPair));
   return __builtin_bit_cast(bf16x8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
 }
 
 // Sum of v[0..15] over the 32 lanes of each half wavefront: the lane returns
 // the sum of v[r], r = its lane bits 4, 3, 2, 1 from high to low.
-__device__ __forceinline__ float sum_rows(float (&v)[16], int lane) {
+__device__ __forceinline__ float sum_rows(f32x16 v, int lane) {
   // bit 4 by swapping 16-lane rows: even rows keep v[0..7], odd rows v[8..15]
 #pragma unroll
   for (int r = 0; r < 8; ++r) {
@@ -66,8 +71,8 @@ __device__ __forceinline__ float sum_rows(float (&v)[16], int lane) {
     const bool up = (lane & (2 * h)) != 0;
 #pragma unroll
     for (int r = 0; r < h; ++r) {
-      const float give = up ? v[r] : v[r + h];
-      const float keep = up ? v[r + h] : v[r];
+      const float a = v[r], b = v[r + h];
+      const float give = up ? a : b, keep = up ? b : a;
       v[r] = keep + __shfl_xor(give, 2 * h);
     }
   }
@@ -78,7 +83,7 @@ template <int K>
 __global__ void __launch_bounds__(kThreads) scale_grad_kernel(
     const uint4* __restrict__ bits, const uint16_t* __restrict__ dY, int64_t lddy,
     const uint16_t* __restrict__ X, int64_t ldx, float* __restrict__ out, int T, int m, int n,
-    int RB, int slices, int accumulate) {
+    int RB, int slices, int accumulate, int aligned) {
   extern __shared__ __attribute__((aligned(16))) uint16_t smem[];
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -98,50 +103,63 @@ __global__ void __launch_bounds__(kThreads) scale_grad_kernel(
   const int full_end = min(s1, T / kSteps);  // steps of 64 live tokens
   const bool tail = s1 > full_end;
 
-  // copy role: piece u = token tid / 32 + 16 u of the step, 8 columns 8 (tid % 32) ..
-  const int ct = tid >> 5, cc = 8 * (tid & 31);
+  // copy role: piece u = token ct + 16 u of the step, 8 columns cc ..
+  const int ct = 2 * wave + ((lane >> 2) & 1);
+  const int cc = 8 * (4 * (lane >> 3) + (lane & 3));
   // columns past n read the last ones (their sums are never stored)
-  const uint16_t* xp = X + (int64_t)ct * ldx + min(j0 + cc, n - 8);
-  const int ia = i0 + cc;               // first row index of the dY piece
+  const int xc = min(j0 + cc, n - 8);
+  const int ia = i0 + cc;                   // first row index of the dY piece
   const int live = max(0, min(8, m - ia));  // of which inside m
-  const uint16_t* yp = dY + (int64_t)ct * lddy + min(ia, m - 1);
+  const int yc = min(ia, m - 1);
+  auto ybuf = [&](int b) { return smem + 2 * b * kBuf; };
+  auto xbuf = [&](int b) { return smem + (2 * b + 1) * kBuf; };
+  auto slot = [&](int u) { return (8 * u + wave) * kPair; };  // the wavefront's pair
 
   struct Regs {
-    u32x4 y[4], x[4];
+    u32x4 y[4];
   };
   Regs R0, R1;
-  auto load_dy = [&](const uint16_t* q, bool edge) {
-    if (!edge || live == 8) return u32x4(*reinterpret_cast<const u32x4_any*>(q));
+  auto load_dy = [&](const uint16_t* q) {
+    if (live == 8) return u32x4(*reinterpret_cast<const u32x4_any*>(q));
     uint32_t e[8];
 #pragma unroll
     for (int c = 0; c < 8; ++c) e[c] = c < live ? q[c] : 0u;
     return u32x4{e[0] | e[1] << 16, e[2] | e[3] << 16, e[4] | e[5] << 16, e[6] | e[7] << 16};
   };
-  auto load = [&](int s, Regs& R, bool edge) {
-    const int64_t t = (int64_t)s * kSteps;
+  auto load_y = [&](int s, Regs& R) {
 #pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      R.y[u] = load_dy(yp + (t + 16 * u) * lddy, edge);
-      R.x[u] = *reinterpret_cast<const u32x4*>(xp + (t + 16 * u) * ldx);
-    }
+    for (int u = 0; u < 4; ++u)
+      R.y[u] = load_dy(dY + ((int64_t)s * kSteps + ct + 16 * u) * lddy + yc);
+  };
+  auto store_y = [&](int b, const Regs& R, int u) {
+    *reinterpret_cast<u32x4*>(ybuf(b) + slot(u) + lane * 8) = R.y[u];
+  };
+  // a step of 64 live tokens straight to LDS, at 32-bit offsets from the step
+  auto copy_x = [&](int s, int b) {
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
+      copy_to_lds(X + ((int64_t)s * kSteps + 16 * u) * ldx, (uint32_t)(ct * ldx + xc) * 2u,
+                  xbuf(b) + slot(u));
+  };
+  auto copy_y = [&](int s, int b) {
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
+      copy_to_lds(dY + ((int64_t)s * kSteps + 16 * u) * lddy, (uint32_t)(ct * lddy + yc) * 2u,
+                  ybuf(b) + slot(u));
   };
   // the last, partial step: tokens past T are zero in both operands
-  auto load_tail = [&](int s, Regs& R) {
+  auto store_tail = [&](int s, int b) {
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
-      const int64_t t = (int64_t)s * kSteps + 16 * u;
-      R.y[u] = R.x[u] = u32x4{0u, 0u, 0u, 0u};
-      if (t + ct < T) {
-        R.y[u] = load_dy(yp + t * lddy, true);
-        R.x[u] = *reinterpret_cast<const u32x4*>(xp + t * ldx);
+      const int64_t t = (int64_t)s * kSteps + ct + 16 * u;
+      u32x4 y = u32x4{0u, 0u, 0u, 0u}, x = y;
+      if (t < T) {
+        y = load_dy(dY + t * lddy + yc);
+        x = *reinterpret_cast<const u32x4*>(X + t * ldx + xc);
       }
+      *reinterpret_cast<u32x4*>(ybuf(b) + slot(u) + lane * 8) = y;
+      *reinterpret_cast<u32x4*>(xbuf(b) + slot(u) + lane * 8) = x;
     }
-  };
-  auto ybuf = [&](int b) { return smem + 2 * b * kBuf; };
-  auto xbuf = [&](int b) { return smem + (2 * b + 1) * kBuf; };
-  auto store = [&](int b, const Regs& R, int u) {
-    *reinterpret_cast<u32x4*>(ybuf(b) + (ct + 16 * u) * kStride + cc) = R.y[u];
-    *reinterpret_cast<u32x4*>(xbuf(b) + (ct + 16 * u) * kStride + cc) = R.x[u];
   };
 
   f32x16 acc[2][4];
@@ -152,62 +170,102 @@ __global__ void __launch_bounds__(kThreads) scale_grad_kernel(
 #pragma unroll
       for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.f;
 
-  const int off = (8 * (lane >> 5) + ((lane & 15) >> 2)) * kStride + 16 * ((lane >> 4) & 1) +
-                  4 * (lane & 3);
-  auto mma = [&](int b, auto&& between) {
-    const uint16_t* ys = ybuf(b) + off + wi * 64;
-    const uint16_t* xs = xbuf(b) + off + wj * 128;
-    bf16x8 pa[2][2], pb[2][4];
-    auto frags = [&](int q) {
+  // operand of a 32-column block: tokens 16 q + 8 (lane / 32) + 4 h .., columns
+  // as read_tr's lanes take them
+  const int tl = (lane & 15) >> 2;  // token of the four
+  const int toff = (4 * (lane >> 5) + (tl >> 1)) * kPair + 32 * (tl & 1) +
+                   16 * ((lane >> 4) & 1) + 4 * (lane & 3);
+  bf16x8 pa[2][2], pb[2][4];
+  auto read_y = [&](int b, int q, int i) {
+    pa[q & 1][i] = read_tr(ybuf(b) + toff + wi * 128 + 8 * q * kPair + 64 * i);
+  };
+  auto read_x = [&](int b, int q, int j) {
+    pb[q & 1][j] = read_tr(xbuf(b) + toff + wj * 256 + 8 * q * kPair + 64 * j);
+  };
+  // products of sub-step q (16 tokens) one at a time, the operands of the next
+  // (nq, from buffer b) read between them; work(x) runs after product x
+  auto products = [&](int q, int b, int nq, auto&& work) {
 #pragma unroll
-      for (int i = 0; i < 2; ++i) pa[q & 1][i] = read_tr(ys + 16 * q * kStride + 32 * i);
-#pragma unroll
-      for (int j = 0; j < 4; ++j) pb[q & 1][j] = read_tr(xs + 16 * q * kStride + 32 * j);
-    };
-    frags(0);
-#pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      if (q < 3) frags(q + 1);
-#pragma unroll
-      for (int i = 0; i < 2; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-          acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(pa[q & 1][i], pb[q & 1][j],
-                                                              acc[i][j], 0, 0, 0);
-      between(q);
+    for (int x = 0; x < 8; ++x) {
+      const int i = x & 1, j = x >> 1;
+      acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(pa[q & 1][i], pb[q & 1][j], acc[i][j], 0,
+                                                          0, 0);
+      if (nq >= 0) {
+        if (x < 2) read_y(b, nq, x);
+        if (x < 4) read_x(b, nq, x);
+      }
+      work(x);
+      __builtin_amdgcn_sched_barrier(0);
     }
   };
+  auto first_operands = [&](int b) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) read_y(b, 0, i);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) read_x(b, 0, j);
+  };
 
-  auto walk = [&](auto edge_c) {
-    constexpr bool edge = decltype(edge_c)::value;
+  // Step s multiplies buffer s % 2.  The barrier stands before the last
+  // quarter of its products, whose operands are in registers by then: the next
+  // step's first operands and the copies of the step after it are in flight
+  // during that quarter.  DIRECT: dY goes straight to LDS too; otherwise
+  // (unaligned rows, a tile across the last row) by way of registers, loaded
+  // two steps before they are stored.
+  auto walk = [&](auto direct_c) {
+    constexpr bool DIRECT = decltype(direct_c)::value;
     const int S = full_end - s0;
     if (S <= 0) return;
     const int last = full_end - 1;
-    load(s0, R0, edge);
-    load(min(s0 + 1, last), R1, edge);
+    auto at = [&](int s) { return min(s0 + s, last); };  // the extra steps at the end are unused
+    copy_x(at(0), 0);
+    if constexpr (DIRECT) {
+      copy_y(at(0), 0);
+    } else {
+      load_y(at(0), R0);
+      load_y(at(1), R1);
 #pragma unroll
-    for (int u = 0; u < 4; ++u) store(0, R0, u);
-    __syncthreads();
-    for (int s = 0; s < S; s += 2) {
-      load(min(s0 + s + 2, last), R0, edge);
-      mma(0, [&](int q) { store(1, R1, q); });
-      __syncthreads();
-      if (s + 1 >= S) break;
-      load(min(s0 + s + 3, last), R1, edge);
-      mma(1, [&](int q) { store(0, R0, q); });
-      __syncthreads();
+      for (int u = 0; u < 4; ++u) store_y(0, R0, u);
     }
-  };
-  if (i0 + kTile <= m)
-    walk(std::false_type{});
-  else
-    walk(std::true_type{});
-  if (tail) {
-    load_tail(full_end, R0);
-#pragma unroll
-    for (int u = 0; u < 4; ++u) store(0, R0, u);
+    copies_done();
     __syncthreads();
-    mma(0, [](int) {});
+    copy_x(at(1), 1);
+    if constexpr (DIRECT) copy_y(at(1), 1);
+    else load_y(at(2), R0);
+    first_operands(0);
+    auto step = [&](int s, int b, Regs& R) {
+#pragma unroll
+      for (int q = 0; q < 3; ++q)
+        products(q, b, q + 1, [&](int x) {
+          if constexpr (!DIRECT) {
+            if (q == 1 && x >= 4) store_y(b ^ 1, R, x - 4);
+          }
+        });
+      copies_done();
+      __syncthreads();
+      copy_x(at(s + 2), b);
+      if constexpr (DIRECT) copy_y(at(s + 2), b);
+      else load_y(at(s + 3), R);
+      __builtin_amdgcn_sched_barrier(0);
+      products(3, b ^ 1, 0, [](int) {});
+    };
+    for (int s = 0; s < S; s += 2) {
+      step(s, 0, R1);
+      if (s + 1 >= S) break;
+      step(s + 1, 1, R0);
+    }
+    copies_done();
+  };
+  if (aligned && i0 + kTile <= m)
+    walk(std::true_type{});
+  else
+    walk(std::false_type{});
+  if (tail) {
+    __syncthreads();
+    store_tail(full_end, 0);
+    __syncthreads();
+    first_operands(0);
+#pragma unroll
+    for (int q = 0; q < 4; ++q) products(q, 0, q < 3 ? q + 1 : -1, [](int) {});
   }
 
   // the wavefront's row block and group: sign chunks to LDS (the buffers are
@@ -228,7 +286,7 @@ __global__ void __launch_bounds__(kThreads) scale_grad_kernel(
   for (int i = 0; i < 2; ++i) {
 #pragma unroll
     for (int k = 0; k < K; ++k) {
-      float v[16];
+      f32x16 v;
 #pragma unroll
       for (int r = 0; r < 16; ++r) {
         const int row = 32 * i + 8 * (r >> 2) + 4 * (lane >> 5) + (r & 3);
@@ -287,6 +345,10 @@ int launch_scale_grad(const mbok_desc* d, const void* packed, const void* dY, in
                       void* ws, hipStream_t stream) {
   const Geom geo = make_geom(d);
   const int slices = ws ? grad_slices(geo, T) : 1;
+  // straight copies of dY to LDS take 16-byte aligned rows
+  const int aligned = ((uintptr_t)dY & 15) == 0 && (lddy % 8) == 0;
+  // and 32-bit offsets over 16 rows: leading dimensions past that are refused
+  if (lddy >= (int64_t(1) << 26) || ldx >= (int64_t(1) << 26)) return MBOK_ERR_INVALID_ARG;
   const int64_t blocks = (int64_t)((geo.n + kTile - 1) / kTile) *
                          ((geo.m + kTile - 1) / kTile) * slices;
   float* out = slices > 1 ? reinterpret_cast<float*>(ws) : dalpha;
@@ -295,7 +357,7 @@ int launch_scale_grad(const mbok_desc* d, const void* packed, const void* dY, in
                        reinterpret_cast<const uint4*>(packed),
                        reinterpret_cast<const uint16_t*>(dY), lddy,
                        reinterpret_cast<const uint16_t*>(X), ldx, out, (int)T, geo.m, geo.n,
-                       geo.RB, slices, accumulate ? 1 : 0);
+                       geo.RB, slices, accumulate ? 1 : 0, aligned);
   };
   switch (geo.K) {
     case 1: go(scale_grad_kernel<1>); break;
