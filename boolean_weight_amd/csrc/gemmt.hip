@@ -36,7 +36,13 @@ typedef __attribute__((ext_vector_type(4))) __bf16 bf16x4;
 constexpr int kBN = 256;       // columns per workgroup tile
 constexpr int kThreads = 512;  // 8 wavefronts
 constexpr int kAStride = kRowBlock;  // bf16 elements per LDS row of dY
-constexpr int kWStride = kBN;        // and of W_hat
+// LDS image of W_hat's 64 x 256 tile: pairs of rows, each 1 KB of 64-byte
+// granules (32 columns) alternating between its two rows and 128 bytes of
+// padding, so that a granule of four consecutive rows covers the 64 banks once
+// and every operand's address is the lane's plus a constant.  The 16-byte
+// pieces of a granule are in the order piece ^ (row / 4 & 3): the 16 lanes (rows)
+// of a 16-byte write then meet 16 different bank groups.
+constexpr int kWPair = 576;  // bf16 elements per pair of rows
 
 // Token rows of a tile and how the 8 wavefronts share it: WT wavefronts along
 // the tokens, 8 / WT along the columns, each TI x TJ blocks of 32 x 32.
@@ -45,12 +51,12 @@ struct Tile {
   static constexpr int TI = TI_, TJ = TJ_, WT = WT_, WN = 8 / WT_;
   static constexpr int BT = 32 * TI * WT;
   static_assert(32 * TJ * WN == kBN, "256 columns");
-  static constexpr int kA = BT * kAStride, kW = kRowBlock * kWStride;  // elements
+  static constexpr int kA = BT * kAStride, kW = kRowBlock / 2 * kWPair;  // elements
   static constexpr size_t kLds = 2 * (size_t)(kA + kW) * sizeof(uint16_t);
 };
 
 // 8 rows (k0 .. k0 + 7) of one column per lane: two transposing reads, of rows
-// k0 .. k0 + 3 and k0 + 4 .. k0 + 7
+// k0 .. k0 + 3 and k0 + 4 .. k0 + 7 (p4)
 __device__ __forceinline__ bf16x8 read_tr(const uint16_t* p, const uint16_t* p4) {
   typedef __attribute__((address_space(3))) i16x4 lds_i16x4;
   const i16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4*)p);
@@ -164,20 +170,21 @@ __global__ void __launch_bounds__(kThreads) gemmt_kernel(
       for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.f;
 
   const int wt = wave / TL::WN, wn = wave % TL::WN;
-  // LDS positions.  A dY row is 8 pieces of 16 bytes, piece c of token r at
-  // position c ^ (r / 2 & 7); a W_hat row is 32 pieces, piece c of row r at c ^
-  // (4 (r & 3) + (r / 4 & 3)).  The 64 banks of LDS are 16 such positions, and
-  // the 16 lanes of a 16-byte access (32 of an 8-byte one) then meet each once.
-  // dY operand: token lane % 32, rows 16 q + 8 (lane / 32) ..; W_hat operand: see
-  // read_tr, rows 16 q + 8 (lane / 32) + 4 h ..
+  // A dY row in LDS is 8 pieces of 16 bytes, piece c of token r at position
+  // c ^ (r / 2 & 7): the 64 banks are 16 such positions, and the 16 lanes of a
+  // 16-byte read meet each once.
+  // dY operand: token lane % 32, rows 16 q + 8 (lane / 32) ..; W_hat operand: rows
+  // 16 q + 8 (lane / 32) + 4 h + (lane / 4 & 3), see read_tr
   const int arr = (wt * 32 * TI + (lane & 31)) * kAStride;
-  const int wrow = (8 * (lane >> 5) + ((lane & 15) >> 2)) * kWStride + 4 * (lane & 1);
-  const int wpiece = (2 * ((lane >> 4) & 1) + ((lane & 3) >> 1)) ^
-                     (4 * ((lane & 15) >> 2) + 2 * (lane >> 5));
   auto aoff = [&](int q) { return arr + 8 * ((2 * q + (lane >> 5)) ^ ((lane >> 1) & 7)); };
-  auto woff = [&](int j, int h) {
-    return wrow + 4 * h * kWStride + 8 * ((wn * 4 * TJ + 4 * j) ^ wpiece ^ h);
-  };
+  const int wl = (lane & 15) >> 2;  // row of the four
+  const int wpiece = (2 * ((lane >> 4) & 1) + ((lane & 3) >> 1)) ^ (2 * (lane >> 5));
+  const int wbase = (4 * (lane >> 5) + (wl >> 1)) * kWPair + 32 * (wl & 1) + 4 * (lane & 1) +
+                    wn * TJ * 64;
+  const int woff[2] = {wbase + 8 * wpiece, wbase + 2 * kWPair + 8 * (wpiece ^ 1)};
+  // where the unpacking thread's columns go: row `lane`, granule `wave`
+  const int wput = (lane >> 1) * kWPair + 32 * (lane & 1) + 64 * wave;
+  const int wkey = (lane >> 2) & 3;
 
   // One step's W_hat, from its signs and scales to LDS, in kChunks pieces of a
   // few vector instructions each (K = 4: in four): levels, selectors, then
@@ -187,8 +194,7 @@ __global__ void __launch_bounds__(kThreads) gemmt_kernel(
   uint32_t pairs[2], V[4], lo = 0, hi = 0, out[4];
   Levels L;
   auto w_piece = [&](int b, int q) {
-    const int piece = (wave * 4 + q) ^ (4 * (lane & 3) + ((lane >> 2) & 3));
-    *reinterpret_cast<u32x4*>(wbuf(b) + lane * kWStride + 8 * piece) =
+    *reinterpret_cast<u32x4*>(wbuf(b) + wput + 8 * (q ^ wkey)) =
         u32x4{out[0], out[1], out[2], out[3]};
   };
   auto form = [&](int b, const StepRegs& R, int c) {
@@ -234,8 +240,8 @@ __global__ void __launch_bounds__(kThreads) gemmt_kernel(
     pa[q & 1][i] = *reinterpret_cast<const bf16x8*>(abuf(b) + aoff(q) + i * 32 * kAStride);
   };
   auto read_w = [&](int b, int q, int j) {
-    pb[q & 1][j] = read_tr(wbuf(b) + woff(j, 0) + 16 * q * kWStride,
-                           wbuf(b) + woff(j, 1) + 16 * q * kWStride);
+    pb[q & 1][j] = read_tr(wbuf(b) + woff[0] + 8 * q * kWPair + 64 * j,
+                           wbuf(b) + woff[1] + 8 * q * kWPair + 64 * j);
   };
   // Products of sub-step q (16 rows), one at a time; after product x the
   // operands of sub-step q + 1 whose turn it is are read from buffer b (next
