@@ -21,7 +21,7 @@ CEILINGS_LIB = os.path.join(PKG, "libmbok_ceilings.so")
 CEILINGS_SOURCES = ["ceilings.hip"]
 
 SOURCES = ["mbok_api.cpp", "allocate.cpp", "quantize.hip", "refit.hip", "svid.hip", "pack.hip", "gemv.hip", "gemv_f4.hip", "gemvt.hip", "gemm.hip", "skinny.hip", "gated.hip",
-           "gated_f4.hip", "gemmt.hip", "scale_grad.hip", "distill.hip"]
+           "gated_f4.hip", "gated_mfma.hip", "gemmt.hip", "scale_grad.hip", "distill.hip"]
 ARCH = "gfx950"
 
 COMMON = [

@@ -1,0 +1,393 @@
+// The gated feed-forward block H = act(X Wg^T) (.) (X Wu^T) for many tokens on
+// the matrix cores (gfx950).
+//
+// "Highly Efficient and Effective LLMs with Multi-Boolean Architectures",
+// Paper-Notes reading note, 关键设计: W_hat = sum_k alpha_k (.) B_k with
+// group-wise scales.  Both projections are one stacked layer (mbok_gated.h), so
+// the block is one product with 256 tokens x 256 stacked rows (128 outputs) per
+// workgroup and an epilogue in registers.
+//
+// Bound: the matrix cores (4 T m n operations against a few bytes per weight),
+// here at ~2.1 GHz under this load.  8 wavefronts of 128 tokens x 64 rows (2 per
+// SIMD); the contraction runs in steps of 64 columns.  A step's activations
+// are copied from memory to LDS without passing registers, its weights are
+// formed from signs and scales, rounded to bf16 and stored, both
+// double-buffered in rows of 128 bytes.  What the design is about is keeping
+// the matrix cores fed: one matrix instruction takes 32 cycles, in which its
+// wavefront can issue a few vector instructions for free (measured: 4 to 5
+// beside every matrix instruction of both wavefronts cost 4%, 8 cost 37%), so
+// the weights' forming and the next operands' reads are laid between them a
+// few at a time, and the barrier of a step stands before the last quarter of
+// its products, whose operands are in registers by then.
+//
+// A wavefront's two 32-row blocks are 32 gate rows and the same 32 up rows: the
+// unpacking thread of stacked row 64 b + 16 u + 8 h + r writes its weights to
+// LDS row 64 b + 32 h + 8 u + r, so a lane holds both values of an output.  The
+// outputs go through LDS (free by then) to whole 16-byte stores.
+//
+// Tiles that would run as a partial last round of workgroups are cut along
+// the rows into halves, and what of those would be a partial round into
+// quarters (11008 x 4096, 2048 tokens: 688 tiles on 256 compute units are 2 +
+// 1/2 + 1/4 rounds instead of 3).
+#include <stdint.h>
+
+#include <type_traits>
+
+#include "mbok_device.h"
+#include "mbok_gated.h"
+#include "mbok_launch.h"
+#include "mbok_levels.h"
+
+namespace mbok {
+namespace {
+
+typedef __attribute__((ext_vector_type(4), aligned(2))) uint32_t u32x4_any;  // H rows start anywhere
+
+constexpr int kBT = 256;       // tokens of a tile
+constexpr int kBK = 64;        // columns per step
+constexpr int kThreads = 512;  // 8 wavefronts
+
+// BN stacked rows of a tile, shared by WT wavefronts along the tokens and 8 / WT
+// along the rows, each TI blocks of 32 tokens x 2 blocks of 32 rows.
+template <int BN_, int WT_>
+struct Part {
+  static constexpr int BN = BN_, WT = WT_, WN = 8 / WT_, TI = kBT / 32 / WT_;
+  static_assert(64 * WN == BN, "64 rows per wavefront");
+  static constexpr int TPR = kThreads / BN;  // threads per row in the unpacking
+  static constexpr int NP = 8 / TPR;         // 16-byte pieces each
+  static constexpr int kX = kBT * kBK, kW = BN * kBK;  // bf16 elements
+};
+constexpr size_t kLds = 2 * (size_t)(kBT + 256) * kBK * sizeof(uint16_t);
+constexpr int kHStride = 128 + 8;    // the output tile in LDS
+constexpr int kPreStride = 256 + 8;
+static_assert(kBT * kPreStride * 2 <= 160 * 1024, "the output tile fits LDS");
+constexpr size_t kLdsAll = kLds > kBT * kPreStride * 2 ? kLds : kBT * kPreStride * 2;
+
+template <typename AT, int K, typename P>
+__device__ __forceinline__ void gated_tile(const uint32_t* __restrict__ bits,
+                                           const AT* __restrict__ scales,
+                                           const uint16_t* __restrict__ X, int64_t ldx,
+                                           const GatedOut& out, int T, int m_pad, int G, int t0,
+                                           int n0, uint16_t* smem) {
+  constexpr int TI = P::TI, NP = P::NP;
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int S = 2 * G;  // steps
+  auto xbuf = [&](int b) { return smem + b * (P::kX + P::kW); };
+  auto wbuf = [&](int b) { return smem + b * (P::kX + P::kW) + P::kX; };
+
+  // A row of either tile is 8 pieces of 16 bytes, piece c of row r at position
+  // c ^ (r / 2 & 7): the 64 banks are 16 such positions, two rows.
+  // unpacking: pieces p0 .. p0 + NP - 1 of one row's 64 columns; rows past the
+  // packed layer read its last row (their sums are never stored)
+  const int trow = tid / P::TPR, p0 = (tid % P::TPR) * NP;
+  const int lrow = (trow & ~63) + 32 * ((trow >> 3) & 1) + 8 * ((trow >> 4) & 3) + (trow & 7);
+  const int word = p0 >> 2;  // 32-column word of the step
+  const int wput = lrow * kBK;
+  const int wkey = (lrow >> 1) & 7;
+  // the tile's first row block and, in 32-bit offsets from it, the thread's
+  // chunk of (row, group 0, kernel 0)
+  const int rb0 = min(n0, m_pad - kRowBlock) / kRowBlock;
+  const int row = min(n0 + trow, m_pad - 1);
+  const uint32_t chunk = (uint32_t)(row / kRowBlock - rb0) * (uint32_t)(G * K * kRowBlock) +
+                         (uint32_t)(row % kRowBlock);
+  const uint32_t woff = chunk * 16u + 4u * word, soff = chunk * (uint32_t)sizeof(AT);
+  const char* tile_w = reinterpret_cast<const char*>(bits) +
+                       (int64_t)rb0 * G * K * kRowBlock * 16;
+  const char* tile_s = reinterpret_cast<const char*>(scales) +
+                       (int64_t)rb0 * G * K * kRowBlock * (int64_t)sizeof(AT);
+  // activations: piece u of the step is token tid / 8 + 64 u, position tid % 8;
+  // tokens past T read the last one (never stored)
+  const int xrow = tid >> 3;
+  const int xpiece = (tid & 7) ^ ((xrow >> 1) & 7);
+  const uint16_t* tile_x = X + (int64_t)t0 * ldx;
+  uint32_t xoff[4];
+#pragma unroll
+  for (int u = 0; u < 4; ++u)
+    xoff[u] = (uint32_t)((int64_t)min(xrow + 64 * u, T - 1 - t0) * ldx * 2) + 16 * xpiece;
+  auto copy_x = [&](int s, int b) {
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
+      copy_to_lds(tile_x + s * kBK, xoff[u], xbuf(b) + (u * kThreads + wave * kWave) * 8);
+  };
+  struct Signs {
+    uint32_t w[K];
+    AT a[K];
+  };
+  Signs R0, R1;
+  auto load_w = [&](int s, Signs& R) {
+    const int g = s >> 1;
+    const char* wb = tile_w + (int64_t)g * (K * kRowBlock * 16) + 8 * (s & 1);
+    const char* sb = tile_s + (int64_t)g * (int)(K * kRowBlock * sizeof(AT));
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      R.w[k] = *reinterpret_cast<const uint32_t*>(wb + woff + k * kRowBlock * 16);
+      R.a[k] = *reinterpret_cast<const AT*>(sb + soff + k * kRowBlock * (int)sizeof(AT));
+    }
+  };
+
+  // one step's weights in kChunks pieces of a few instructions; the levels of
+  // a scale group serve its two steps
+  constexpr int kChunks = 24;
+  float af[K];
+  uint32_t pairs[2], V[4], lo = 0, hi = 0, o4[4];
+  Levels L;
+  auto put = [&](int b, int p) {
+    *reinterpret_cast<u32x4*>(wbuf(b) + wput + 8 * ((p0 + p) ^ wkey)) =
+        u32x4{o4[0], o4[1], o4[2], o4[3]};
+  };
+  auto form = [&](int b, const Signs& R, int c, bool levels) {
+    if (levels && c == 0) {
+#pragma unroll
+      for (int k = 0; k < K; ++k) af[k] = alpha_to_f32<AT>(R.a[k]);
+    }
+    if constexpr (K <= 3) {
+      if (levels && c < 2) pairs[c] = upper_pair<K>(af, c);
+      if (levels && c == 2) L = pack_levels<K>(pairs[0], pairs[1]);
+      if (c >= 3 && c < 6) word_selectors_part<K>(R.w, V, c - 3);
+      const int h = (c - 8) >> 1;  // quad of the thread's pieces
+      if (c >= 8 && h < 2 * NP) {
+        if ((c & 1) == 0) {
+          // the thread's pieces of its word: all, or the half or quarter p0 names
+          uint32_t sel = 0;
+          if (NP == 4) {
+            sel = quad_selector<K>(V, h >> 2, h & 3);
+          } else if (NP == 2) {
+            const uint32_t s0 = quad_selector<K>(V, 0, h), s1 = quad_selector<K>(V, 1, h);
+            sel = (p0 & 2) ? s1 : s0;
+          } else {
+            const uint32_t a0 = quad_selector<K>(V, 0, h), a1 = quad_selector<K>(V, 0, h + 2);
+            const uint32_t b0 = quad_selector<K>(V, 1, h), b1 = quad_selector<K>(V, 1, h + 2);
+            const uint32_t x0 = (p0 & 1) ? a1 : a0, x1 = (p0 & 1) ? b1 : b0;
+            sel = (p0 & 2) ? x1 : x0;
+          }
+          lo = quad_low(L, sel);
+          hi = quad_high(L, sel);
+        } else {
+          quad_pairs(lo, hi, o4 + 2 * (h & 1));
+          if (h & 1) put(b, h >> 1);
+        }
+      }
+    } else if (c >= 8 && (c & 3) == 0 && ((c - 8) >> 2) < NP) {
+      const int p = (c - 8) >> 2;
+      uint32_t o32[16];
+      unpack_word_k4<false>(R.w, af, o32);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        if (NP == 4) o4[e] = o32[4 * p + e];
+        else if (NP == 2) o4[e] = (p0 & 2) ? o32[8 + 4 * p + e] : o32[4 * p + e];
+        else {
+          const uint32_t x0 = (p0 & 1) ? o32[4 + e] : o32[e];
+          const uint32_t x1 = (p0 & 1) ? o32[12 + e] : o32[8 + e];
+          o4[e] = (p0 & 2) ? x1 : x0;
+        }
+      }
+      put(b, p);
+    }
+  };
+
+  f32x16 acc[TI][2];
+#pragma unroll
+  for (int i = 0; i < TI; ++i)
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.f;
+
+  const int wt = wave / P::WN, wn = wave % P::WN;
+  // operand of a 32-row block: row lane % 32, columns 16 q + 8 (lane / 32) ..
+  const int lbase = (lane & 31) * kBK;
+  auto opos = [&](int q) { return lbase + 8 * ((2 * q + (lane >> 5)) ^ ((lane >> 1) & 7)); };
+  bf16x8 pa[2][TI], pb[2][2];
+  auto read_x = [&](int b, int q, int i) {
+    pa[q & 1][i] = *reinterpret_cast<const bf16x8*>(xbuf(b) + opos(q) + (wt * TI + i) * 32 * kBK);
+  };
+  auto read_w = [&](int b, int q, int j) {
+    pb[q & 1][j] = *reinterpret_cast<const bf16x8*>(wbuf(b) + opos(q) + (wn * 2 + j) * 32 * kBK);
+  };
+  constexpr int NX = TI * 2;
+  // products of sub-step q one at a time; the operands of sub-step nq (buffer
+  // b) are read and work(x) runs after product x
+  auto products = [&](int q, int b, int nq, auto&& work) {
+#pragma unroll
+    for (int x = 0; x < NX; ++x) {
+      const int i = x % TI, j = x / TI;
+      acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(pa[q & 1][i], pb[q & 1][j], acc[i][j], 0,
+                                                          0, 0);
+      if (x < 2) read_w(b, nq, x);
+      if (x < TI) read_x(b, nq, x);
+      work(x);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+  };
+
+  auto at = [&](int s) { return min(s, S - 1); };  // the extra steps at the end are unused
+  copy_x(0, 0);
+  load_w(0, R0);
+  load_w(1, R1);
+#pragma unroll
+  for (int c = 0; c < kChunks; ++c) form(0, R0, c, true);
+  copies_done();
+  pin<K>(R1);
+  __syncthreads();
+  copy_x(1, 1);
+  load_w(at(2), R0);
+#pragma unroll
+  for (int j = 0; j < 2; ++j) read_w(0, 0, j);
+#pragma unroll
+  for (int i = 0; i < TI; ++i) read_x(0, 0, i);
+  // Step s: its products from buffer b = s % 2 while the weights of step s + 1
+  // are formed from R in the other; even steps of the contraction begin a
+  // scale group.
+  auto step = [&](int s, int b, Signs& R) {
+#pragma unroll
+    for (int q = 0; q < 3; ++q)
+      products(q, b, q + 1, [&](int x) {
+        const int y = q * NX + x;
+#pragma unroll
+        for (int c = 0; c < kChunks; ++c)
+          if (c * 3 * NX / kChunks == y) form(b ^ 1, R, c, b == 1);
+      });
+    copies_done();
+    __syncthreads();
+    copy_x(at(s + 2), b);
+    load_w(at(s + 3), R);
+    __builtin_amdgcn_sched_barrier(0);
+    products(3, b ^ 1, 0, [](int) {});
+  };
+  for (int s = 0; s < S; s += 2) {
+    step(s, 0, R1);
+    step(s + 1, 1, R0);
+  }
+  copies_done();
+
+  // ---- outputs.  C layout: lane l, register r -> token 8 (r / 4) + 4 (l / 32) +
+  // r % 4, row l % 32.  First H, then (training) the pre-activations.
+  __syncthreads();
+  const int o0 = n0 / 2;                     // first output of the tile
+  const int oc = wn * 32 + (lane & 31);      // the lane's output in the tile
+  const bool inside = o0 + oc < out.m;
+  const int tb = wt * 32 * TI + 4 * (lane >> 5);
+#pragma unroll
+  for (int i = 0; i < TI; ++i)
+#pragma unroll
+    for (int r = 0; r < 16; ++r) {
+      float unused;
+      const float h = activation<false>(out.act, acc[i][0][r], unused) * acc[i][1][r];
+      smem[(tb + 32 * i + 8 * (r >> 2) + (r & 3)) * kHStride + oc] = to_bf16(h);
+    }
+  __syncthreads();
+  constexpr int HP = P::BN / 16;  // 16-byte pieces of a row of H
+  for (int e = tid; e < kBT * HP; e += kThreads) {
+    const int t = e / HP, c = 8 * (e % HP);
+    if (t0 + t >= T || o0 + c >= out.m) continue;
+    const u32x4 v = *reinterpret_cast<const u32x4*>(smem + t * kHStride + c);
+    uint16_t* dst = out.H + (int64_t)(t0 + t) * out.ldh + o0 + c;
+    if (o0 + c + 8 <= out.m) {
+      *reinterpret_cast<u32x4_any*>(dst) = v;
+    } else {
+#pragma unroll
+      for (int q = 0; q < 8; ++q)
+        if (o0 + c + q < out.m)
+          dst[q] = (uint16_t)((q & 1) ? v[q >> 1] >> 16 : v[q >> 1] & 0xffffu);
+    }
+  }
+  if (!out.pre) return;
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < TI; ++i)
+#pragma unroll
+    for (int r = 0; r < 16; ++r) {
+      uint16_t* p = smem + (tb + 32 * i + 8 * (r >> 2) + (r & 3)) * kPreStride + 16 * (oc >> 3) +
+                    (oc & 7);
+      p[0] = inside ? to_bf16(acc[i][0][r]) : (uint16_t)0;
+      p[8] = inside ? to_bf16(acc[i][1][r]) : (uint16_t)0;
+    }
+  __syncthreads();
+  constexpr int PP = P::BN / 8;
+  const int m2 = 2 * ((out.m + 7) & ~7);
+  for (int e = tid; e < kBT * PP; e += kThreads) {
+    const int t = e / PP, c = 8 * (e % PP);
+    if (t0 + t < T && n0 + c < m2)
+      *reinterpret_cast<u32x4*>(out.pre + (int64_t)(t0 + t) * out.ldpre + n0 + c) =
+          *reinterpret_cast<const u32x4*>(smem + t * kPreStride + c);
+  }
+}
+
+// Workgroups 0 .. full - 1 take whole tiles, the next 2 (halves - full) halves of
+// tiles full .., then quarters of tiles halves ..
+template <typename AT, int K>
+__global__ void __launch_bounds__(kThreads) gated_mfma_kernel(
+    const uint32_t* __restrict__ bits, const AT* __restrict__ scales,
+    const uint16_t* __restrict__ X, int64_t ldx, GatedOut out, int T, int m_pad, int G, int ntx,
+    int nty, int full, int halves) {
+  extern __shared__ __attribute__((aligned(16))) uint16_t smem[];
+  const int b = blockIdx.x;
+  if (b < full) {
+    // XCD b % 8 takes consecutive positions of the tile order
+    const int p = (full & 7) == 0 ? (b & 7) * (full >> 3) + (b >> 3) : b;
+    const int tile = tile_at(p, ntx, nty);
+    gated_tile<AT, K, Part<256, 2>>(bits, scales, X, ldx, out, T, m_pad, G, (tile / ntx) * kBT,
+                                    (tile % ntx) * 256, smem);
+  } else if (b < full + 2 * (halves - full)) {
+    const int h = b - full;
+    const int tile = tile_at(full + (h >> 1), ntx, nty);
+    gated_tile<AT, K, Part<128, 4>>(bits, scales, X, ldx, out, T, m_pad, G, (tile / ntx) * kBT,
+                                    (tile % ntx) * 256 + 128 * (h & 1), smem);
+  } else {
+    const int h = b - full - 2 * (halves - full);
+    const int tile = tile_at(halves + (h >> 2), ntx, nty);
+    gated_tile<AT, K, Part<64, 8>>(bits, scales, X, ldx, out, T, m_pad, G, (tile / ntx) * kBT,
+                                   (tile % ntx) * 256 + 64 * (h & 3), smem);
+  }
+}
+
+constexpr int kUnits = 256;  // workgroups that run at once (one per compute unit)
+
+template <typename AT, int K>
+void launch_k(const Geom& geo, const void* packed, const uint16_t* X, int64_t T, int64_t ldx,
+              const GatedOut& out, hipStream_t stream) {
+  const uint32_t* bits = reinterpret_cast<const uint32_t*>(packed);
+  const AT* scales = reinterpret_cast<const AT*>(reinterpret_cast<const char*>(packed) +
+                                                 geo.bits_bytes);
+  const int ntx = (geo.m + 255) / 256, nty = (int)((T + kBT - 1) / kBT);
+  const int64_t tiles = (int64_t)ntx * nty;
+  // whole rounds of whole tiles; of the rest as many halves as fill rounds,
+  // the others as quarters
+  const int64_t full = tiles / kUnits * kUnits;
+  const int64_t halves = full + (2 * (tiles - full)) / kUnits * kUnits / 2;
+  const int64_t blocks = full + 2 * (halves - full) + 4 * (tiles - halves);
+  hipLaunchKernelGGL((gated_mfma_kernel<AT, K>), dim3((unsigned)blocks), dim3(kThreads), kLdsAll,
+                     stream, bits, scales, X, ldx, out, (int)T, geo.RB * kRowBlock, geo.G, ntx,
+                     nty, (int)full, (int)halves);
+}
+
+template <typename AT>
+void launch_t(const Geom& geo, const void* packed, const uint16_t* X, int64_t T, int64_t ldx,
+              const GatedOut& out, hipStream_t stream) {
+  switch (geo.K) {
+    case 1: launch_k<AT, 1>(geo, packed, X, T, ldx, out, stream); break;
+    case 2: launch_k<AT, 2>(geo, packed, X, T, ldx, out, stream); break;
+    case 3: launch_k<AT, 3>(geo, packed, X, T, ldx, out, stream); break;
+    default: launch_k<AT, 4>(geo, packed, X, T, ldx, out, stream); break;
+  }
+}
+
+}  // namespace
+
+// d: the stacked layer.  The kernel's offsets inside the layer's signs and
+// inside a tile's activations are 32 bits.
+int launch_gated_mfma(const mbok_desc* d, const void* packed, const void* X, int64_t T,
+                      int64_t ldx, const GatedOut& out, hipStream_t stream) {
+  const Geom geo = make_geom(d);
+  if (geo.bits_bytes / 4 >= (int64_t(1) << 32)) return MBOK_ERR_SHAPE;
+  if (ldx >= (int64_t(1) << 32) / (2 * kBT)) return MBOK_ERR_INVALID_ARG;
+  const uint16_t* x = reinterpret_cast<const uint16_t*>(X);
+  if (d->alpha_dtype == MBOK_F16)
+    launch_t<uint16_t>(geo, packed, x, T, ldx, out, stream);
+  else
+    launch_t<float>(geo, packed, x, T, ldx, out, stream);
+  return hipGetLastError() == hipSuccess ? MBOK_OK : MBOK_ERR_HIP;
+}
+
+}  // namespace mbok

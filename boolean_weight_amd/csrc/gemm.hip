@@ -268,20 +268,13 @@ constexpr int GEMM8_THREADS = 512;
 // The body of one workgroup: JB = 2 for a whole 256-row tile, 1 for one
 // 128-row half of a tile of the partial final round (a compile-time constant,
 // so the loop has no branches on it).
-//
-// Out is how the tile is stored.  With GatedOut the layer is the gated block's
-// stacked one, whose 16-row tiles hold 8 gate rows and the same 8 up rows:
-// the unpacking thread of stacked row 64 b + 16 u + 8 h + r writes its weights
-// to LDS row 64 b + 32 h + 8 u + r, so that a wavefront's two 32-row blocks are
-// 32 gate rows and the same 32 up rows, and a lane holds both values of an
-// output.
-template <typename AT, int K, int JB, bool LO, typename Out>
+template <typename AT, int K, int JB, bool LO>
 __device__ __forceinline__ void mfma8_tile(const uint32_t* __restrict__ bits,
                                            const AT* __restrict__ scales,
                                            const uint16_t* __restrict__ X, int64_t ldx,
-                                           const Out& out, int T, int m, int m_pad, int G,
-                                           int ntx, int tile, int half, uint16_t* smem) {
-  constexpr bool GATED = std::is_same<Out, GatedOut>::value;
+                                           float* __restrict__ Y, int64_t ldy, int T, int m,
+                                           int m_pad, int G, int ntx, int tile, int half,
+                                           uint16_t* smem) {
   // buffer b: activations at smem + 2b * TILE_ELEMS, weights right after
   const int tid = threadIdx.x;
   const int lane = tid & 63;
@@ -302,12 +295,9 @@ __device__ __forceinline__ void mfma8_tile(const uint32_t* __restrict__ bits,
   // n0 + tid/4, columns 16 (tid % 4) .., so that every wavefront unpacks)
   constexpr int TPR = JB == 2 ? 2 : 4;
   static_assert(GEMM8_THREADS / TPR == tile_rows, "one row per TPR threads");
-  const int trow = tid / TPR, upart = tid % TPR;
+  const int urow = tid / TPR, upart = tid % TPR;
   const int uword = JB == 2 ? upart : upart >> 1;  // 32-column word of the step
-  const int row = n0 + trow;
-  // LDS row of the thread's weights
-  const int urow = GATED ? (trow & ~63) + 32 * ((trow >> 3) & 1) + 8 * ((trow >> 4) & 3) + (trow & 7)
-                         : trow;
+  const int row = n0 + urow;
   const int rowc = row < m_pad ? row : m_pad - 1;
   const uint32_t row_chunk = (uint32_t)(rowc / kRowBlock) * (uint32_t)(G * K * kRowBlock) +
                              (uint32_t)(rowc % kRowBlock);
@@ -476,51 +466,17 @@ __device__ __forceinline__ void mfma8_tile(const uint32_t* __restrict__ bits,
 
   // C layout: lane l, register r -> token 8(r/4) + 4(l/32) + r%4, row l%32
 #pragma unroll
-  for (int i = 0; i < TI; ++i) {
-    const int tb = t0 + wt * 32 * TI + i * 32 + 4 * (lane >> 5);
-    if constexpr (GATED) {
-      const int orow = (n0 + wn * 32 * TJ) / 2 + lrow;  // the output of the lane's pair
-      if (orow >= m / 2) continue;
+  for (int i = 0; i < TI; ++i)
+#pragma unroll
+    for (int j = 0; j < TJ; ++j) {
+      const int n = n0 + wn * 32 * TJ + j * 32 + lrow;
+      if (n >= m) continue;
 #pragma unroll
       for (int r = 0; r < 16; ++r) {
-        const int t = tb + 8 * (r >> 2) + (r & 3);
-        if (t < T) out.put(t, orow, acc[i][0][r], acc[i][1][r]);
-      }
-    } else {
-#pragma unroll
-      for (int j = 0; j < TJ; ++j) {
-        const int n = n0 + wn * 32 * TJ + j * 32 + lrow;
-        if (n >= m) continue;
-#pragma unroll
-        for (int r = 0; r < 16; ++r) {
-          const int t = tb + 8 * (r >> 2) + (r & 3);
-          if (t < T) store_out<LO>(out.y + (int64_t)t * out.ldy + n, acc[i][j][r]);
-        }
+        const int t = t0 + wt * 32 * TI + i * 32 + 8 * (r >> 2) + 4 * (lane >> 5) + (r & 3);
+        if (t < T) store_out<LO>(Y + (int64_t)t * ldy + n, acc[i][j][r]);
       }
     }
-  }
-}
-
-template <typename AT, int K, bool LO, typename Out>
-__device__ __forceinline__ void mfma8_body(const uint32_t* __restrict__ bits,
-                                           const AT* __restrict__ scales,
-                                           const uint16_t* __restrict__ X, int64_t ldx,
-                                           const Out& out, int T, int m, int m_pad, int G,
-                                           int ntx, int nfull, int xcd_order) {
-  extern __shared__ __attribute__((aligned(16))) uint16_t smem[];
-  const int b = blockIdx.x;
-  const int nty = (T + BT - 1) / BT;
-  if (b < nfull) {
-    int p = b;
-    if (xcd_order && (nfull & 7) == 0) p = (b & 7) * (nfull >> 3) + (b >> 3);
-    const int tile = xcd_order ? tile_at(p, ntx, nty) : p;
-    mfma8_tile<AT, K, 2, LO>(bits, scales, X, ldx, out, T, m, m_pad, G, ntx, tile, 0, smem);
-  } else {
-    const int p = nfull + ((b - nfull) >> 1);
-    const int tile = xcd_order ? tile_at(p, ntx, nty) : p;
-    mfma8_tile<AT, K, 1, LO>(bits, scales, X, ldx, out, T, m, m_pad, G, ntx, tile,
-                             (b - nfull) & 1, smem);
-  }
 }
 
 template <typename AT, int K, bool LO>
@@ -528,17 +484,20 @@ __global__ void __launch_bounds__(GEMM8_THREADS) gemm_mfma8_kernel(
     const uint32_t* __restrict__ bits, const AT* __restrict__ scales,
     const uint16_t* __restrict__ X, int64_t ldx, float* __restrict__ Y, int64_t ldy, int T, int m,
     int m_pad, int G, int ntx, int nfull, int xcd_order) {
-  mfma8_body<AT, K, LO>(bits, scales, X, ldx, RowsOut{Y, ldy, m}, T, m, m_pad, G, ntx, nfull,
-                        xcd_order);
-}
-
-// the gated feed-forward block; m is the stacked layer's
-template <typename AT, int K>
-__global__ void __launch_bounds__(GEMM8_THREADS) gated_mfma8_kernel(
-    const uint32_t* __restrict__ bits, const AT* __restrict__ scales,
-    const uint16_t* __restrict__ X, int64_t ldx, GatedOut out, int T, int m, int m_pad, int G,
-    int ntx, int nfull, int xcd_order) {
-  mfma8_body<AT, K, false>(bits, scales, X, ldx, out, T, m, m_pad, G, ntx, nfull, xcd_order);
+  extern __shared__ __attribute__((aligned(16))) uint16_t smem[];
+  const int b = blockIdx.x;
+  const int nty = (T + BT - 1) / BT;
+  if (b < nfull) {
+    int p = b;
+    if (xcd_order && (nfull & 7) == 0) p = (b & 7) * (nfull >> 3) + (b >> 3);
+    const int tile = xcd_order ? tile_at(p, ntx, nty) : p;
+    mfma8_tile<AT, K, 2, LO>(bits, scales, X, ldx, Y, ldy, T, m, m_pad, G, ntx, tile, 0, smem);
+  } else {
+    const int p = nfull + ((b - nfull) >> 1);
+    const int tile = xcd_order ? tile_at(p, ntx, nty) : p;
+    mfma8_tile<AT, K, 1, LO>(bits, scales, X, ldx, Y, ldy, T, m, m_pad, G, ntx, tile,
+                         (b - nfull) & 1, smem);
+  }
 }
 
 // Compute units of the current device (queried once per device; host
@@ -566,8 +525,7 @@ int gemm_xcd_order() {
 
 template <typename AT, int K, bool LO>
 void launch_mfma8_k(const Geom& geo, const uint32_t* bits, const AT* scales, const uint16_t* Xb,
-                    int64_t T, int64_t ldx, float* Y, int64_t ldy, hipStream_t stream,
-                    const GatedOut* gated = nullptr) {
+                    int64_t T, int64_t ldx, float* Y, int64_t ldy, hipStream_t stream) {
   const size_t lds = 4 * TILE_ELEMS * sizeof(uint16_t);
   const int ntx = (geo.m + BN - 1) / BN;
   const int64_t ntiles = (int64_t)ntx * ((T + BT - 1) / BT);
@@ -575,14 +533,6 @@ void launch_mfma8_k(const Geom& geo, const uint32_t* bits, const AT* scales, con
   const int ncu = compute_units();
   const int64_t rem = ntiles % ncu;
   const int64_t nfull = ntiles - rem;
-  if constexpr (!LO) {
-    if (gated) {
-      hipLaunchKernelGGL((gated_mfma8_kernel<AT, K>), dim3((unsigned)(nfull + 2 * rem)),
-                         dim3(GEMM8_THREADS), lds, stream, bits, scales, Xb, ldx, *gated, (int)T,
-                         geo.m, geo.RB * kRowBlock, geo.G, ntx, (int)nfull, gemm_xcd_order());
-      return;
-    }
-  }
   hipLaunchKernelGGL((gemm_mfma8_kernel<AT, K, LO>), dim3((unsigned)(nfull + 2 * rem)),
                      dim3(GEMM8_THREADS), lds, stream, bits, scales, Xb, ldx, Y, ldy, (int)T,
                      geo.m, geo.RB * kRowBlock, geo.G, ntx, (int)nfull, gemm_xcd_order());
@@ -590,16 +540,16 @@ void launch_mfma8_k(const Geom& geo, const uint32_t* bits, const AT* scales, con
 
 template <typename AT, bool LO>
 void launch_mfma8(const Geom& geo, const void* packed, const void* X, int64_t T, int64_t ldx,
-                  float* Y, int64_t ldy, hipStream_t stream, const GatedOut* gated = nullptr) {
+                  float* Y, int64_t ldy, hipStream_t stream) {
   const uint32_t* bits = reinterpret_cast<const uint32_t*>(packed);
   const AT* scales = reinterpret_cast<const AT*>(reinterpret_cast<const char*>(packed) +
                                                  geo.bits_bytes);
   const uint16_t* Xb = reinterpret_cast<const uint16_t*>(X);
   switch (geo.K) {
-    case 1: launch_mfma8_k<AT, 1, LO>(geo, bits, scales, Xb, T, ldx, Y, ldy, stream, gated); break;
-    case 2: launch_mfma8_k<AT, 2, LO>(geo, bits, scales, Xb, T, ldx, Y, ldy, stream, gated); break;
-    case 3: launch_mfma8_k<AT, 3, LO>(geo, bits, scales, Xb, T, ldx, Y, ldy, stream, gated); break;
-    default: launch_mfma8_k<AT, 4, LO>(geo, bits, scales, Xb, T, ldx, Y, ldy, stream, gated); break;
+    case 1: launch_mfma8_k<AT, 1, LO>(geo, bits, scales, Xb, T, ldx, Y, ldy, stream); break;
+    case 2: launch_mfma8_k<AT, 2, LO>(geo, bits, scales, Xb, T, ldx, Y, ldy, stream); break;
+    case 3: launch_mfma8_k<AT, 3, LO>(geo, bits, scales, Xb, T, ldx, Y, ldy, stream); break;
+    default: launch_mfma8_k<AT, 4, LO>(geo, bits, scales, Xb, T, ldx, Y, ldy, stream); break;
   }
 }
 
@@ -720,30 +670,6 @@ int launch_gemm(const mbok_desc* d, const void* packed, const void* X, int64_t T
   if (d->alpha_dtype == MBOK_F16)
     return launch_mfma<uint16_t>(geo, packed, X, T, ldx, Y, ldy, passes, stream);
   return launch_mfma<float>(geo, packed, X, T, ldx, Y, ldy, passes, stream);
-}
-
-// T > 16 rows of the gated block (d: the stacked layer).  The kernel indexes
-// activations with 32-bit offsets, so very long inputs go in several launches
-// of whole token tiles.
-int launch_gated_mfma(const mbok_desc* d, const void* packed, const void* X, int64_t T,
-                      int64_t ldx, const GatedOut& out, hipStream_t stream) {
-  const Geom geo = make_geom(d);
-  if (geo.bits_bytes / 4 >= (int64_t(1) << 32)) return MBOK_ERR_SHAPE;
-  int64_t chunk = ((int64_t(1) << 32) - 1) / ldx / BT * BT;
-  if (chunk < BT) return MBOK_ERR_INVALID_ARG;
-  for (int64_t t = 0; t < T; t += chunk) {
-    const int64_t rows = T - t < chunk ? T - t : chunk;
-    const uint16_t* x = reinterpret_cast<const uint16_t*>(X) + t * ldx;
-    GatedOut o = out;
-    o.H += t * out.ldh;
-    if (o.pre) o.pre += t * out.ldpre;
-    if (d->alpha_dtype == MBOK_F16)
-      launch_mfma8<uint16_t, false>(geo, packed, x, rows, ldx, nullptr, 0, stream, &o);
-    else
-      launch_mfma8<float, false>(geo, packed, x, rows, ldx, nullptr, 0, stream, &o);
-    if (hipGetLastError() != hipSuccess) return MBOK_ERR_HIP;
-  }
-  return MBOK_OK;
 }
 
 }  // namespace mbok

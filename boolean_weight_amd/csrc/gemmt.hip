@@ -285,6 +285,7 @@ __global__ void __launch_bounds__(kThreads) gemmt_kernel(
     load_w(at(1), R1);
     form_all(0, R0);
     copies_done();
+    pin<K>(R1);
     __syncthreads();
     load_a(ALIGNED ? at(1) : at(2), 1, R0);
     load_w(at(2), R0);

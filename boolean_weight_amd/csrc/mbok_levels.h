@@ -30,7 +30,14 @@ __device__ __forceinline__ void copy_to_lds(const void* base, uint32_t off, cons
                : "s"(__builtin_amdgcn_readfirstlane(at)), "v"(off), "s"(base)
                : "memory");
 }
-__device__ __forceinline__ void copies_done() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
+// Waits for every load in flight.  The builtin, not assembly: the compiler then
+// knows that its own loads are done too (it otherwise waited for them again
+// after the next copies were issued, and so for those).
+__device__ __forceinline__ void copies_done() {
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_waitcnt(0x0f70);  // vmcnt(0); the other counters at their maximum
+  asm volatile("" ::: "memory");
+}
 
 __device__ __forceinline__ uint32_t bf16_pair(float a, float b) {
   const __bf16 ha = (__bf16)a, hb = (__bf16)b;  // nearest-even
@@ -99,7 +106,16 @@ __device__ __forceinline__ Levels make_levels(const float* a) {
 // nibble's other bits are other quads').  Two words are merged for two b at a
 // time.
 __device__ __forceinline__ uint32_t bit_select(uint32_t mask, uint32_t a, uint32_t b) {
-  return (a & mask) | (b & ~mask);  // one v_bfi_b32
+  uint32_t d;  // (a & mask) | (b & ~mask); the compiler takes it apart into three
+  asm("v_bfi_b32 %0, %1, %2, %3" : "=v"(d) : "s"(mask), "v"(a), "v"(b));
+  return d;
+}
+// Holds loaded signs and scales in registers at this point of the program, so
+// that their loads are not moved past a later barrier.
+template <int K, typename R>
+__device__ __forceinline__ void pin(R& r) {
+#pragma unroll
+  for (int k = 0; k < K; ++k) asm volatile("" : "+v"(r.w[k]), "+v"(r.a[k]));
 }
 // part 0, 1, 2 in turn (V holds what is between them)
 template <int K>
