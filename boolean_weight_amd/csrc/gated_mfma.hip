@@ -25,10 +25,11 @@
 // LDS row 64 b + 32 h + 8 u + r, so a lane holds both values of an output.  The
 // outputs go through LDS (free by then) to whole 16-byte stores.
 //
-// Tiles that would run as a partial last round of workgroups are cut along
-// the rows into halves, and what of those would be a partial round into
-// quarters (11008 x 4096, 2048 tokens: 688 tiles on 256 compute units are 2 +
-// 1/2 + 1/4 rounds instead of 3).
+// Few tokens or few rows take smaller tiles (see launch_k).  Cutting the last
+// partial round of whole tiles into halves and quarters was measured slower
+// than running it whole (11008 x 4096, 2048 tokens, 688 tiles on 256 compute
+// units: 346 against 328 us; a half copies the same activations for half the
+// products).
 #include <stdint.h>
 
 #include <type_traits>
@@ -43,25 +44,22 @@ namespace {
 
 typedef __attribute__((ext_vector_type(4), aligned(2))) uint32_t u32x4_any;  // H rows start anywhere
 
-constexpr int kBT = 256;       // tokens of a tile
-constexpr int kBK = 64;        // columns per step
-constexpr int kThreads = 512;  // 8 wavefronts
+constexpr int kBK = 64;  // columns per step
 
-// BN stacked rows of a tile, shared by WT wavefronts along the tokens and 8 / WT
-// along the rows, each TI blocks of 32 tokens x 2 blocks of 32 rows.
-template <int BN_, int WT_>
-struct Part {
-  static constexpr int BN = BN_, WT = WT_, WN = 8 / WT_, TI = kBT / 32 / WT_;
-  static_assert(64 * WN == BN, "64 rows per wavefront");
-  static constexpr int TPR = kThreads / BN;  // threads per row in the unpacking
-  static constexpr int NP = 8 / TPR;         // 16-byte pieces each
-  static constexpr int kX = kBT * kBK, kW = BN * kBK;  // bf16 elements
+// A workgroup's tile: WT wavefronts along the tokens and WN along the stacked
+// rows, each TI blocks of 32 tokens x 2 blocks of 32 rows.
+template <int WT_, int WN_, int TI_>
+struct Tile {
+  static constexpr int WT = WT_, WN = WN_, TI = TI_;
+  static constexpr int threads = 64 * WT * WN, BT = 32 * TI * WT, BN = 64 * WN;
+  static constexpr int NU = BT * 8 / threads;     // 16-byte pieces of activations each
+  static constexpr int kX = BT * kBK, kW = BN * kBK;  // bf16 elements
+  static constexpr int HS = BN / 2 + 8, PS = BN + 8;  // LDS rows of the outputs
+  static constexpr size_t lds =
+      2 * (size_t)(2 * (kX + kW) > BT * PS ? 2 * (kX + kW) : BT * PS);
+  static_assert(lds <= 160 * 1024 && NU * threads == BT * 8, "tile shape");
+  static_assert(threads == 2 * BN, "a thread unpacks one 32-column word of a row");
 };
-constexpr size_t kLds = 2 * (size_t)(kBT + 256) * kBK * sizeof(uint16_t);
-constexpr int kHStride = 128 + 8;    // the output tile in LDS
-constexpr int kPreStride = 256 + 8;
-static_assert(kBT * kPreStride * 2 <= 160 * 1024, "the output tile fits LDS");
-constexpr size_t kLdsAll = kLds > kBT * kPreStride * 2 ? kLds : kBT * kPreStride * 2;
 
 template <typename AT, int K, typename P>
 __device__ __forceinline__ void gated_tile(const uint32_t* __restrict__ bits,
@@ -69,7 +67,7 @@ __device__ __forceinline__ void gated_tile(const uint32_t* __restrict__ bits,
                                            const uint16_t* __restrict__ X, int64_t ldx,
                                            const GatedOut& out, int T, int m_pad, int G, int t0,
                                            int n0, uint16_t* smem) {
-  constexpr int TI = P::TI, NP = P::NP;
+  constexpr int TI = P::TI, NU = P::NU, kThreads = P::threads, kBT = P::BT;
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int S = 2 * G;  // steps
@@ -78,11 +76,10 @@ __device__ __forceinline__ void gated_tile(const uint32_t* __restrict__ bits,
 
   // A row of either tile is 8 pieces of 16 bytes, piece c of row r at position
   // c ^ (r / 2 & 7): the 64 banks are 16 such positions, two rows.
-  // unpacking: pieces p0 .. p0 + NP - 1 of one row's 64 columns; rows past the
-  // packed layer read its last row (their sums are never stored)
-  const int trow = tid / P::TPR, p0 = (tid % P::TPR) * NP;
+  // unpacking: one 32-column word of one row; rows past the packed layer read
+  // its last row (their sums are never stored)
+  const int trow = tid >> 1, word = tid & 1;
   const int lrow = (trow & ~63) + 32 * ((trow >> 3) & 1) + 8 * ((trow >> 4) & 3) + (trow & 7);
-  const int word = p0 >> 2;  // 32-column word of the step
   const int wput = lrow * kBK;
   const int wkey = (lrow >> 1) & 7;
   // the tile's first row block and, in 32-bit offsets from it, the thread's
@@ -96,18 +93,20 @@ __device__ __forceinline__ void gated_tile(const uint32_t* __restrict__ bits,
                        (int64_t)rb0 * G * K * kRowBlock * 16;
   const char* tile_s = reinterpret_cast<const char*>(scales) +
                        (int64_t)rb0 * G * K * kRowBlock * (int64_t)sizeof(AT);
-  // activations: piece u of the step is token tid / 8 + 64 u, position tid % 8;
+  // activations: piece u of the step is token tid / 8 + threads / 8 u, position
+  // tid % 8 (threads / 8 is a multiple of 16: the piece is the same for every u);
   // tokens past T read the last one (never stored)
   const int xrow = tid >> 3;
   const int xpiece = (tid & 7) ^ ((xrow >> 1) & 7);
   const uint16_t* tile_x = X + (int64_t)t0 * ldx;
-  uint32_t xoff[4];
+  uint32_t xoff[NU];
 #pragma unroll
-  for (int u = 0; u < 4; ++u)
-    xoff[u] = (uint32_t)((int64_t)min(xrow + 64 * u, T - 1 - t0) * ldx * 2) + 16 * xpiece;
+  for (int u = 0; u < NU; ++u)
+    xoff[u] = (uint32_t)((int64_t)min(xrow + kThreads / 8 * u, T - 1 - t0) * ldx * 2) +
+              16 * xpiece;
   auto copy_x = [&](int s, int b) {
 #pragma unroll
-    for (int u = 0; u < 4; ++u)
+    for (int u = 0; u < NU; ++u)
       copy_to_lds(tile_x + s * kBK, xoff[u], xbuf(b) + (u * kThreads + wave * kWave) * 8);
   };
   struct Signs {
@@ -133,7 +132,7 @@ __device__ __forceinline__ void gated_tile(const uint32_t* __restrict__ bits,
   uint32_t pairs[2], V[4], lo = 0, hi = 0, o4[4];
   Levels L;
   auto put = [&](int b, int p) {
-    *reinterpret_cast<u32x4*>(wbuf(b) + wput + 8 * ((p0 + p) ^ wkey)) =
+    *reinterpret_cast<u32x4*>(wbuf(b) + wput + 8 * ((4 * word + p) ^ wkey)) =
         u32x4{o4[0], o4[1], o4[2], o4[3]};
   };
   auto form = [&](int b, const Signs& R, int c, bool levels) {
@@ -145,22 +144,10 @@ __device__ __forceinline__ void gated_tile(const uint32_t* __restrict__ bits,
       if (levels && c < 2) pairs[c] = upper_pair<K>(af, c);
       if (levels && c == 2) L = pack_levels<K>(pairs[0], pairs[1]);
       if (c >= 3 && c < 6) word_selectors_part<K>(R.w, V, c - 3);
-      const int h = (c - 8) >> 1;  // quad of the thread's pieces
-      if (c >= 8 && h < 2 * NP) {
+      const int h = (c - 8) >> 1;  // quad of the word
+      if (c >= 8) {
         if ((c & 1) == 0) {
-          // the thread's pieces of its word: all, or the half or quarter p0 names
-          uint32_t sel = 0;
-          if (NP == 4) {
-            sel = quad_selector<K>(V, h >> 2, h & 3);
-          } else if (NP == 2) {
-            const uint32_t s0 = quad_selector<K>(V, 0, h), s1 = quad_selector<K>(V, 1, h);
-            sel = (p0 & 2) ? s1 : s0;
-          } else {
-            const uint32_t a0 = quad_selector<K>(V, 0, h), a1 = quad_selector<K>(V, 0, h + 2);
-            const uint32_t b0 = quad_selector<K>(V, 1, h), b1 = quad_selector<K>(V, 1, h + 2);
-            const uint32_t x0 = (p0 & 1) ? a1 : a0, x1 = (p0 & 1) ? b1 : b0;
-            sel = (p0 & 2) ? x1 : x0;
-          }
+          const uint32_t sel = quad_selector<K>(V, h >> 2, h & 3);
           lo = quad_low(L, sel);
           hi = quad_high(L, sel);
         } else {
@@ -168,20 +155,12 @@ __device__ __forceinline__ void gated_tile(const uint32_t* __restrict__ bits,
           if (h & 1) put(b, h >> 1);
         }
       }
-    } else if (c >= 8 && (c & 3) == 0 && ((c - 8) >> 2) < NP) {
+    } else if (c >= 8 && (c & 3) == 0) {
       const int p = (c - 8) >> 2;
       uint32_t o32[16];
       unpack_word_k4<false>(R.w, af, o32);
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        if (NP == 4) o4[e] = o32[4 * p + e];
-        else if (NP == 2) o4[e] = (p0 & 2) ? o32[8 + 4 * p + e] : o32[4 * p + e];
-        else {
-          const uint32_t x0 = (p0 & 1) ? o32[4 + e] : o32[e];
-          const uint32_t x1 = (p0 & 1) ? o32[12 + e] : o32[8 + e];
-          o4[e] = (p0 & 2) ? x1 : x0;
-        }
-      }
+      for (int e = 0; e < 4; ++e) o4[e] = o32[4 * p + e];
       put(b, p);
     }
   };
@@ -274,14 +253,14 @@ __device__ __forceinline__ void gated_tile(const uint32_t* __restrict__ bits,
     for (int r = 0; r < 16; ++r) {
       float unused;
       const float h = activation<false>(out.act, acc[i][0][r], unused) * acc[i][1][r];
-      smem[(tb + 32 * i + 8 * (r >> 2) + (r & 3)) * kHStride + oc] = to_bf16(h);
+      smem[(tb + 32 * i + 8 * (r >> 2) + (r & 3)) * P::HS + oc] = to_bf16(h);
     }
   __syncthreads();
   constexpr int HP = P::BN / 16;  // 16-byte pieces of a row of H
   for (int e = tid; e < kBT * HP; e += kThreads) {
     const int t = e / HP, c = 8 * (e % HP);
     if (t0 + t >= T || o0 + c >= out.m) continue;
-    const u32x4 v = *reinterpret_cast<const u32x4*>(smem + t * kHStride + c);
+    const u32x4 v = *reinterpret_cast<const u32x4*>(smem + t * P::HS + c);
     uint16_t* dst = out.H + (int64_t)(t0 + t) * out.ldh + o0 + c;
     if (o0 + c + 8 <= out.m) {
       *reinterpret_cast<u32x4_any*>(dst) = v;
@@ -298,7 +277,7 @@ __device__ __forceinline__ void gated_tile(const uint32_t* __restrict__ bits,
   for (int i = 0; i < TI; ++i)
 #pragma unroll
     for (int r = 0; r < 16; ++r) {
-      uint16_t* p = smem + (tb + 32 * i + 8 * (r >> 2) + (r & 3)) * kPreStride + 16 * (oc >> 3) +
+      uint16_t* p = smem + (tb + 32 * i + 8 * (r >> 2) + (r & 3)) * P::PS + 16 * (oc >> 3) +
                     (oc & 7);
       p[0] = inside ? to_bf16(acc[i][0][r]) : (uint16_t)0;
       p[8] = inside ? to_bf16(acc[i][1][r]) : (uint16_t)0;
@@ -310,39 +289,24 @@ __device__ __forceinline__ void gated_tile(const uint32_t* __restrict__ bits,
     const int t = e / PP, c = 8 * (e % PP);
     if (t0 + t < T && n0 + c < m2)
       *reinterpret_cast<u32x4*>(out.pre + (int64_t)(t0 + t) * out.ldpre + n0 + c) =
-          *reinterpret_cast<const u32x4*>(smem + t * kPreStride + c);
+          *reinterpret_cast<const u32x4*>(smem + t * P::PS + c);
   }
 }
 
-// Workgroups 0 .. full - 1 take whole tiles, the next 2 (halves - full) halves of
-// tiles full .., then quarters of tiles halves ..
-template <typename AT, int K>
-__global__ void __launch_bounds__(kThreads) gated_mfma_kernel(
+template <typename AT, int K, typename P>
+__global__ void __launch_bounds__(P::threads) gated_mfma_kernel(
     const uint32_t* __restrict__ bits, const AT* __restrict__ scales,
     const uint16_t* __restrict__ X, int64_t ldx, GatedOut out, int T, int m_pad, int G, int ntx,
-    int nty, int full, int halves) {
+    int nty) {
   extern __shared__ __attribute__((aligned(16))) uint16_t smem[];
-  const int b = blockIdx.x;
-  if (b < full) {
-    // XCD b % 8 takes consecutive positions of the tile order
-    const int p = (full & 7) == 0 ? (b & 7) * (full >> 3) + (b >> 3) : b;
-    const int tile = tile_at(p, ntx, nty);
-    gated_tile<AT, K, Part<256, 2>>(bits, scales, X, ldx, out, T, m_pad, G, (tile / ntx) * kBT,
-                                    (tile % ntx) * 256, smem);
-  } else if (b < full + 2 * (halves - full)) {
-    const int h = b - full;
-    const int tile = tile_at(full + (h >> 1), ntx, nty);
-    gated_tile<AT, K, Part<128, 4>>(bits, scales, X, ldx, out, T, m_pad, G, (tile / ntx) * kBT,
-                                    (tile % ntx) * 256 + 128 * (h & 1), smem);
-  } else {
-    const int h = b - full - 2 * (halves - full);
-    const int tile = tile_at(halves + (h >> 2), ntx, nty);
-    gated_tile<AT, K, Part<64, 8>>(bits, scales, X, ldx, out, T, m_pad, G, (tile / ntx) * kBT,
-                                   (tile % ntx) * 256 + 64 * (h & 3), smem);
-  }
+  const int b = blockIdx.x, blocks = ntx * nty;
+  // XCD b % 8 takes consecutive positions of the tile order (as far as 8 divides)
+  const int even = blocks & ~7;
+  const int p = b < even ? (b & 7) * (even >> 3) + (b >> 3) : b;
+  const int tile = tile_at(p, ntx, nty);
+  gated_tile<AT, K, P>(bits, scales, X, ldx, out, T, m_pad, G, (tile / ntx) * P::BT,
+                       (tile % ntx) * P::BN, smem);
 }
-
-constexpr int kUnits = 256;  // workgroups that run at once (one per compute unit)
 
 template <typename AT, int K>
 void launch_k(const Geom& geo, const void* packed, const uint16_t* X, int64_t T, int64_t ldx,
@@ -350,16 +314,20 @@ void launch_k(const Geom& geo, const void* packed, const uint16_t* X, int64_t T,
   const uint32_t* bits = reinterpret_cast<const uint32_t*>(packed);
   const AT* scales = reinterpret_cast<const AT*>(reinterpret_cast<const char*>(packed) +
                                                  geo.bits_bytes);
-  const int ntx = (geo.m + 255) / 256, nty = (int)((T + kBT - 1) / kBT);
-  const int64_t tiles = (int64_t)ntx * nty;
-  // whole rounds of whole tiles; of the rest as many halves as fill rounds,
-  // the others as quarters
-  const int64_t full = tiles / kUnits * kUnits;
-  const int64_t halves = full + (2 * (tiles - full)) / kUnits * kUnits / 2;
-  const int64_t blocks = full + 2 * (halves - full) + 4 * (tiles - halves);
-  hipLaunchKernelGGL((gated_mfma_kernel<AT, K>), dim3((unsigned)blocks), dim3(kThreads), kLdsAll,
-                     stream, bits, scales, X, ldx, out, (int)T, geo.RB * kRowBlock, geo.G, ntx,
-                     nty, (int)full, (int)halves);
+  auto tiles = [&](int bt, int bn) { return ((T + bt - 1) / bt) * ((geo.m + bn - 1) / bn); };
+  auto go = [&](auto tile) {
+    using P = decltype(tile);
+    const int ntx = (geo.m + P::BN - 1) / P::BN, nty = (int)((T + P::BT - 1) / P::BT);
+    hipLaunchKernelGGL((gated_mfma_kernel<AT, K, P>), dim3((unsigned)ntx * (unsigned)nty),
+                       dim3(P::threads), P::lds, stream, bits, scales, X, ldx, out, (int)T,
+                       geo.RB * kRowBlock, geo.G, ntx, nty);
+  };
+  // Whole tiles where they occupy more than half of the compute units; else
+  // 128 x 128 (two workgroups per compute unit) where those fill the part,
+  // else, and always for up to 64 tokens, 64 x 64 (five per compute unit).
+  if (T > 64 && tiles(256, 256) > 128) go(Tile<2, 4, 4>{});
+  else if (T > 64 && tiles(128, 128) >= 256) go(Tile<2, 2, 2>{});
+  else go(Tile<2, 1, 1>{});
 }
 
 template <typename AT>
@@ -381,7 +349,7 @@ int launch_gated_mfma(const mbok_desc* d, const void* packed, const void* X, int
                       int64_t ldx, const GatedOut& out, hipStream_t stream) {
   const Geom geo = make_geom(d);
   if (geo.bits_bytes / 4 >= (int64_t(1) << 32)) return MBOK_ERR_SHAPE;
-  if (ldx >= (int64_t(1) << 32) / (2 * kBT)) return MBOK_ERR_INVALID_ARG;
+  if (ldx >= (int64_t(1) << 32) / 512) return MBOK_ERR_INVALID_ARG;
   const uint16_t* x = reinterpret_cast<const uint16_t*>(X);
   if (d->alpha_dtype == MBOK_F16)
     launch_t<uint16_t>(geo, packed, x, T, ldx, out, stream);

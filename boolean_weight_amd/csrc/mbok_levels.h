@@ -25,9 +25,13 @@ typedef __attribute__((ext_vector_type(4))) uint32_t u32x4;
 __device__ __forceinline__ void copy_to_lds(const void* base, uint32_t off, const uint16_t* dst) {
   const uint32_t at =
       (uint32_t)(uintptr_t)(const __attribute__((address_space(3))) uint16_t*)dst;
+  const uint64_t from = (uint64_t)(uintptr_t)base;
+  const uint64_t sbase =
+      (uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)from) |
+      (uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)(from >> 32)) << 32;
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2"
                :
-               : "s"(__builtin_amdgcn_readfirstlane(at)), "v"(off), "s"(base)
+               : "s"(__builtin_amdgcn_readfirstlane(at)), "v"(off), "s"(sbase)
                : "memory");
 }
 // Waits for every load in flight.  The builtin, not assembly: the compiler then

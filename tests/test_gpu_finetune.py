@@ -219,7 +219,7 @@ def test_scale_grad_nonfinite_stays_in_its_scales():
 # the 8-row interleaving, the 64-row blocks and the 128-output tiles
 GATED = [(1, 1, 128), (1, 200, 1280), (2, 8, 256), (2, 73, 640), (3, 9, 128), (7, 100, 512),
          (16, 65, 384), (16, 4100, 256), (17, 31, 128), (64, 130, 256), (255, 64, 384),
-         (257, 129, 256), (300, 250, 1152)]
+         (257, 129, 256), (300, 250, 1152), (300, 8500, 128), (257, 5600, 128)]
 
 
 def gated_want(a, b, X, kind):
