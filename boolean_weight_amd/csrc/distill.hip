@@ -100,11 +100,6 @@ __device__ __forceinline__ double wave_sum(double v) {
   return v;
 }
 
-// NaN if either is: fmaxf drops NaN, and a row with a NaN logit has no answer.
-__device__ __forceinline__ float nan_max(float a, float b) {
-  return (a != a || b != b) ? __builtin_nanf("") : fmaxf(a, b);
-}
-
 __device__ __forceinline__ float teacher_logit(const void* l, int dtype, int64_t i) {
   if (dtype == MBOK_F32) return reinterpret_cast<const float*>(l)[i];
   if (dtype == MBOK_F16) return (float)reinterpret_cast<const _Float16*>(l)[i];
@@ -127,14 +122,29 @@ struct DistillRow {
   float tau, c_hi, c_lo;  // log2(e) / tau as an fp32 pair
 };
 
-// exp((x - m) / tau) for the sums: the rounding of the scaled argument is
-// carried to first order, so the sum keeps fp32's accuracy.
-__device__ __forceinline__ float exp_sum(float d, const DistillRow& r) {
+// exp(d / tau), d <= 0, carried to fp32 accuracy: the rounding of the scaled
+// argument to first order (for the few listed entries).
+__device__ __forceinline__ float exp_listed(float d, const DistillRow& r) {
   const float a = d * r.c_hi;
   const float lo = fmaf(d, r.c_hi, -a) + d * r.c_lo;
   const float e = __builtin_amdgcn_exp2f(a);
   return a < -126.f ? 0.f : fmaf(e * kLn2, lo, e);
 }
+
+// Sum of exp(d / tau) over a row: s the exponentials of the scaled arguments a,
+// m their moment sum e a, which corrects s for the rounding of the scale (the
+// roundings of the arguments themselves have either sign and average out).
+// A NaN d makes both NaN; -inf adds 0.
+struct ExpSum {
+  float s = 0.f, m = 0.f;
+  __device__ __forceinline__ void add(float e, float a) {
+    s += e;
+    m = fmaf(e, fmaxf(a, -150.f), m);
+  }
+  __device__ __forceinline__ double total(const DistillRow& r) const {
+    return (double)s + (double)m * ((double)kLn2 * (double)r.c_lo / (double)r.c_hi);
+  }
+};
 
 // The lists of one row in LDS: index (or -1), then p, then one bit per token.
 struct RowLds {
@@ -184,6 +194,30 @@ __device__ __forceinline__ void write_entries(const RowLds& s, const DistillRow&
     drow[v] = (OT)((q - p) * A);
   }
 }
+
+// The main pass's dz = exp((z - zmax) / tau) A.  For 16-bit gradients the factor
+// is folded into the exponent, exp2(z c + k): k's rounding (2^-24 of |k| < 2^8)
+// is far below theirs.
+template <typename OT>
+struct GradScale {
+  static constexpr bool kFold = sizeof(OT) == 2;
+  float A, zmax, c, k;
+  uint32_t sign;
+  __device__ __forceinline__ GradScale(float A_, float zmax_, const DistillRow& r)
+      : A(A_), zmax(zmax_), c(r.c_hi) {
+    if (kFold) {
+      sign = __float_as_uint(A) & 0x80000000u;
+      // A = 0 (or a row without an answer) goes through the exponent as well:
+      // log2 0 = -inf gives 0, NaN stays NaN
+      k = __builtin_amdgcn_logf(fabsf(A)) - zmax * c;
+    }
+  }
+  __device__ __forceinline__ float operator()(float z) const {
+    if (kFold)
+      return __uint_as_float(__float_as_uint(__builtin_amdgcn_exp2f(fmaf(z, c, k))) ^ sign);
+    return __builtin_amdgcn_exp2f((z - zmax) * c) * A;
+  }
+};
 
 template <typename ZT, typename OT, int NV, bool GRAD>
 __global__ void __launch_bounds__(kMaxThreads) distill_kernel(
@@ -251,19 +285,17 @@ __global__ void __launch_bounds__(kMaxThreads) distill_kernel(
     zl[j] = v < 0 ? 0.f : to_f32(row[v]);
   }
 
-  // largest logit
+  // largest logit (a NaN is dropped here: it makes the sum below NaN)
   float mx = -INFINITY;
   each([&](int, const Vec<ZT>& x) {
 #pragma unroll
-    for (int e = 0; e < N; ++e) mx = nan_max(mx, to_f32(x.v[e]));
+    for (int e = 0; e < N; ++e) mx = fmaxf(mx, to_f32(x.v[e]));
   });
-  const bool bad = mx != mx;
   mx = wave_max(mx);
   if (lane == 0) red_f[wave] = mx;
-  const bool nan_row = __syncthreads_or(bad) != 0;  // also: lists and cleared bits are in LDS
+  __syncthreads();  // also: lists and cleared bits are in LDS
   mx = red_f[0];
   for (int i = 1; i < nw; ++i) mx = fmaxf(mx, red_f[i]);
-  if (nan_row) mx = __builtin_nanf("");
 
   bool twice = false;
   for (int j = tid; j < r.top; j += nt)
@@ -272,20 +304,30 @@ __global__ void __launch_bounds__(kMaxThreads) distill_kernel(
   __syncthreads();
 
   // sums of exponentials: all, and (with t_lse) the unlisted ones
-  float sa = 0.f, sr = 0.f;
+  ExpSum sa, sr;
   const bool rest = t_lse != nullptr;
-  each([&](int v, const Vec<ZT>& x) {
-    uint32_t m = 0;
-    if (rest) m = s.bits[(v * N) >> 5] >> ((v * N) & 31);
+  auto scaled = [&](ZT z) { return (to_f32(z) - mx) * r.c_hi; };
+  if (rest) {
+    each([&](int v, const Vec<ZT>& x) {
+      const uint32_t m = s.bits[(v * N) >> 5] >> ((v * N) & 31);
 #pragma unroll
-    for (int e = 0; e < N; ++e) {
-      const float ex = exp_sum(to_f32(x.v[e]) - mx, r);
-      sa += ex;
-      if (rest) sr += (m >> e) & 1u ? 0.f : ex;
-    }
-  });
+      for (int e = 0; e < N; ++e) {
+        const float a = scaled(x.v[e]), ex = __builtin_amdgcn_exp2f(a);
+        sa.add(ex, a);
+        sr.add((m >> e) & 1u ? 0.f : ex, a);
+      }
+    });
+  } else {
+    each([&](int, const Vec<ZT>& x) {
+#pragma unroll
+      for (int e = 0; e < N; ++e) {
+        const float a = scaled(x.v[e]);
+        sa.add(__builtin_amdgcn_exp2f(a), a);
+      }
+    });
+  }
   {
-    const double da = wave_sum((double)sa), dr = rest ? wave_sum((double)sr) : 0.0;
+    const double da = wave_sum(sa.total(r)), dr = rest ? wave_sum(sr.total(r)) : 0.0;
     if (lane == 0) {
       red_d[2 * wave] = da;
       red_d[2 * wave + 1] = dr;
@@ -317,7 +359,7 @@ __global__ void __launch_bounds__(kMaxThreads) distill_kernel(
       Nsum = 0.0;
       if (tm > -INFINITY)
         for (int j = lane; j < r.top; j += kWave)
-          Nsum += (double)exp_sum(s.p[j] - tm, r);
+          Nsum += (double)exp_listed(s.p[j] - tm, r);
       Nsum = wave_sum(Nsum);
       log_n = log(Nsum);
       shift = (double)tm;
@@ -335,7 +377,7 @@ __global__ void __launch_bounds__(kMaxThreads) distill_kernel(
           p = exp(log_p);
         } else {
           log_p = ((double)l - shift) * inv_tau - log_n;
-          p = (double)exp_sum(l - st.tmax, r) / Nsum;
+          p = (double)exp_listed(l - st.tmax, r) / Nsum;
         }
         if (s.idx[j] < 0) p = 0.0;
         s.p[j] = (float)p;
@@ -370,11 +412,11 @@ __global__ void __launch_bounds__(kMaxThreads) distill_kernel(
   const float A = w * r.tau;
   const float Aq = st.inv_n > 0.f ? A * st.inv_s : 0.f;
   const float Au = Aq * st.unlist;
+  const GradScale<OT> scale(Au, mx, r);
   each([&](int v, const Vec<ZT>& x) {
     float d[N];
 #pragma unroll
-    for (int e = 0; e < N; ++e)
-      d[e] = __builtin_amdgcn_exp2f((to_f32(x.v[e]) - mx) * r.c_hi) * Au;
+    for (int e = 0; e < N; ++e) d[e] = scale(to_f32(x.v[e]));
     store_vec<OT, N>(drow, v, r.V, d);
   });
   __syncthreads();
@@ -417,7 +459,7 @@ __global__ void __launch_bounds__(kMaxThreads) distill_backward_kernel(
     if (v >= 0) {
       const float l = teacher_logit(t_logits, t_dtype, t * ldt + j);
       p = t_lse ? (float)exp((double)l / (double)r.tau - (double)t_lse[t])
-                : exp_sum(l - st.tmax, r) * st.inv_n;
+                : exp_listed(l - st.tmax, r) * st.inv_n;
       if (!(st.inv_n > 0.f)) p = 0.f;
       zl[j] = to_f32(row[v]);
       twice |= mark_entry(s.bits, v);
@@ -429,12 +471,12 @@ __global__ void __launch_bounds__(kMaxThreads) distill_backward_kernel(
   const float A = w * r.tau * dl;
   const float Aq = st.inv_n > 0.f ? A * st.inv_s : 0.f;
   const float Au = Aq * st.unlist;
+  const GradScale<OT> scale(Au, st.zmax, r);
   for (int v = tid; v < nvec; v += nt) {
     const Vec<ZT> x = load_vec(row, v, r.V);
     float d[N];
 #pragma unroll
-    for (int e = 0; e < N; ++e)
-      d[e] = __builtin_amdgcn_exp2f((to_f32(x.v[e]) - st.zmax) * r.c_hi) * Au;
+    for (int e = 0; e < N; ++e) d[e] = scale(to_f32(x.v[e]));
     store_vec<OT, N>(drow, v, r.V, d);
   }
   __syncthreads();
@@ -458,8 +500,10 @@ int launch_rows(const mbok_distill_desc* d, const DistillArgs& a, float* loss, f
   const int nvec = (d->vocab + Vec<ZT>::N - 1) / Vec<ZT>::N;
   const size_t lds = row_lds_bytes(d);
   const DistillRow r = row_of(d);
+  // 8 vectors per thread; with few rows, where latency counts, 2
+  const int want = a.T < 512 ? 2 : 8;
   int threads = 256;
-  while (threads < kMaxThreads && threads * 8 < nvec) threads *= 2;
+  while (threads < kMaxThreads && threads * want < nvec) threads *= 2;
   const int per = (nvec + threads - 1) / threads;
   auto go = [&](auto kernel) {
     hipLaunchKernelGGL(kernel, dim3((unsigned)a.T), dim3(threads), lds, stream,

@@ -11,12 +11,10 @@
 #include "mbok_device.h"
 #include "mbok_gated.h"
 #include "mbok_launch.h"
+#include "mbok_levels.h"
 
 namespace mbok {
 namespace {
-
-typedef __attribute__((ext_vector_type(4))) uint32_t u32x4;
-typedef __attribute__((ext_vector_type(4), aligned(2))) uint32_t u32x4_any;  // dH rows start anywhere
 
 __device__ __forceinline__ float lane_value(const u32x4& v, int e) {
   return bf16_bits_to_f32((e & 1) ? v[e >> 1] >> 16 : v[e >> 1] & 0xffffu);
@@ -35,15 +33,7 @@ __global__ void __launch_bounds__(256) gated_backward_kernel(
   const u32x4 gv = p[0], uv = p[1];
   const uint16_t* h = dH + t * lddh + 8 * tile;
   const int live = min(8, m - 8 * tile);
-  u32x4 sv;
-  if (live == 8) {
-    sv = *reinterpret_cast<const u32x4_any*>(h);
-  } else {
-    uint32_t e[8];
-#pragma unroll
-    for (int c = 0; c < 8; ++c) e[c] = c < live ? h[c] : 0u;
-    sv = u32x4{e[0] | e[1] << 16, e[2] | e[3] << 16, e[4] | e[5] << 16, e[6] | e[7] << 16};
-  }
+  const u32x4 sv = load_piece(h, live, m >= 8);  // dH rows start anywhere
   uint32_t dg[8], du[8];
 #pragma unroll
   for (int c = 0; c < 8; ++c) {

@@ -152,13 +152,9 @@ __global__ void __launch_bounds__(kThreads) gemmt_kernel(
     if (!a_live) return;
     const int i0 = rb * kRowBlock + 8 * apart;
 #pragma unroll
-    for (int u = 0; u < NA; ++u) {
-      uint32_t e[8];
-#pragma unroll
-      for (int q = 0; q < 8; ++q) e[q] = i0 + q < m ? dy_at(u, rb)[q] : 0u;
+    for (int u = 0; u < NA; ++u)
       *reinterpret_cast<u32x4*>(abuf(b) + (u * kThreads + tid) * 8) =
-          u32x4{e[0] | e[1] << 16, e[2] | e[3] << 16, e[4] | e[5] << 16, e[6] | e[7] << 16};
-    }
+          load_piece(dy_at(u, rb), max(0, min(8, m - i0)), m >= 8);
   };
 
   f32x16 acc[TI][TJ];
@@ -356,42 +352,48 @@ __global__ void __launch_bounds__(kThreads) gemmt_kernel(
     }
 }
 
-// dX = sum of the slices' partial sums in order, rounded once; 8 columns per thread
+// dX = sum of the slices' partial sums in order, rounded once; 4 columns per thread
 __global__ void __launch_bounds__(256) gemmt_reduce_kernel(const float* __restrict__ part,
                                                            uint16_t* __restrict__ dX,
                                                            int64_t lddx, int T, int n,
                                                            int slices) {
-  const int64_t e = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 8;
+  const int64_t e = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4;
   const int64_t total = (int64_t)T * n;
   if (e >= total) return;
-  float s[8];
+  float s[4] = {0.f, 0.f, 0.f, 0.f};
+  for (int k = 0; k < slices; k += 8) {  // eight loads at a time, added in order
+    float4 v[8];
 #pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    const float4 v = *reinterpret_cast<const float4*>(part + e + 4 * h);
-    s[4 * h] = v.x, s[4 * h + 1] = v.y, s[4 * h + 2] = v.z, s[4 * h + 3] = v.w;
+    for (int u = 0; u < 8; ++u)
+      v[u] = k + u < slices ? *reinterpret_cast<const float4*>(part + (k + u) * total + e)
+                            : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int u = 0; u < 8; ++u) s[0] += v[u].x, s[1] += v[u].y, s[2] += v[u].z, s[3] += v[u].w;
   }
-  for (int k = 1; k < slices; ++k)
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const float4 v = *reinterpret_cast<const float4*>(part + k * total + e + 4 * h);
-      s[4 * h] += v.x, s[4 * h + 1] += v.y, s[4 * h + 2] += v.z, s[4 * h + 3] += v.w;
-    }
   const int64_t t = e / n, j = e - t * n;
-  *reinterpret_cast<u32x4*>(dX + t * lddx + j) =
-      u32x4{bf16_pair(s[0], s[1]), bf16_pair(s[2], s[3]), bf16_pair(s[4], s[5]),
-            bf16_pair(s[6], s[7])};
+  *reinterpret_cast<uint2*>(dX + t * lddx + j) =
+      make_uint2(bf16_pair(s[0], s[1]), bf16_pair(s[2], s[3]));
 }
 
 constexpr int kUnits = 256;  // workgroups that fill the part (one per compute unit)
 
-int tile_tokens(int64_t T) { return T <= 32 ? 32 : T <= 64 ? 64 : T <= 128 ? 128 : 256; }
+// Tokens per tile: as many as there are, up to 256, but fewer where tiles and
+// slices of at least four steps would leave most compute units idle.
+int tile_tokens(const Geom& geo, int64_t T) {
+  const int64_t cols = (geo.n + kBN - 1) / kBN, most = geo.RB < 8 ? 1 : geo.RB / 4;
+  int bt = T <= 32 ? 32 : T <= 64 ? 64 : T <= 128 ? 128 : 256;
+  while (bt > 32 && cols * ((T + bt - 1) / bt) * most < 96) bt /= 2;
+  return bt;
+}
 
-// Slices of the row blocks: as many as keep the workgroups within one round
+// Slices of the row blocks: as many as keep the workgroups within one round,
+// of two steps at least
 int gemmt_slices(const Geom& geo, int64_t T) {
-  const int bt = tile_tokens(T);
+  const int bt = tile_tokens(geo, T);
   const int64_t tiles = ((geo.n + kBN - 1) / kBN) * ((T + bt - 1) / bt);
   int64_t s = kUnits / tiles;
-  if (s > geo.RB / 2) s = geo.RB / 2;  // two steps each at least
+  if (s > geo.RB / 2) s = geo.RB / 2;
+  if (s > 32) s = 32;  // what the joining kernel adds per output
   return s < 1 ? 1 : (int)s;
 }
 
@@ -416,7 +418,7 @@ int launch_k(const Geom& geo, const void* packed, const uint16_t* dY, int64_t T,
     else launch(gemmt_kernel<AT, K, TL, P, false>);
   };
   auto by_tile = [&](auto partial) {
-    switch (tile_tokens(T)) {
+    switch (tile_tokens(geo, T)) {
       case 32: go(Tile<1, 1, 1>{}, partial); break;
       case 64: go(Tile<2, 1, 1>{}, partial); break;
       case 128: go(Tile<4, 1, 1>{}, partial); break;
@@ -425,7 +427,7 @@ int launch_k(const Geom& geo, const void* packed, const uint16_t* dY, int64_t T,
   };
   if (slices > 1) {
     by_tile(std::true_type{});
-    const int64_t threads = T * geo.n / 8;
+    const int64_t threads = T * geo.n / 4;
     hipLaunchKernelGGL(gemmt_reduce_kernel, dim3((unsigned)((threads + 255) / 256)), dim3(256), 0,
                        stream, part, dX, lddx, (int)T, geo.n, slices);
   } else {

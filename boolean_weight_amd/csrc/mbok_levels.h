@@ -14,6 +14,32 @@ typedef __attribute__((ext_vector_type(16))) float f32x16;
 // struct member went through scratch memory)
 typedef __attribute__((ext_vector_type(4))) uint32_t u32x4;
 
+// 8 bf16 values at p (any 2-byte alignment) of which the first `live` lie inside
+// the row and the others are returned as 0 without being read.  back: at least
+// 8 values of the row end where the live ones do, so one load of those, shifted,
+// serves a partial piece.
+typedef __attribute__((ext_vector_type(4), aligned(2))) uint32_t u32x4_unaligned;
+__device__ __forceinline__ u32x4 load_piece(const uint16_t* p, int live, bool back) {
+  if (live == 8) return u32x4(*reinterpret_cast<const u32x4_unaligned*>(p));
+  u32x4 r = u32x4{0u, 0u, 0u, 0u};
+  if (live <= 0) return r;
+  if (back) {
+    const u32x4 v = *reinterpret_cast<const u32x4_unaligned*>(p + live - 8);
+    const int drop = 8 - live;  // values before p: 1 .. 7
+    const bool d4 = drop & 4, d2 = drop & 2, d1 = drop & 1;
+    uint32_t w[5] = {d4 ? v[2] : v[0], d4 ? v[3] : v[1], d4 ? 0u : v[2], d4 ? 0u : v[3], 0u};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[i] = d2 ? (i < 3 ? w[i + 1] : 0u) : w[i];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) r[i] = d1 ? (w[i] >> 16 | (i < 3 ? w[i + 1] << 16 : 0u)) : w[i];
+    return r;
+  }
+  uint32_t e[8];
+#pragma unroll
+  for (int c = 0; c < 8; ++c) e[c] = c < live ? p[c] : 0u;
+  return u32x4{e[0] | e[1] << 16, e[2] | e[3] << 16, e[4] | e[5] << 16, e[6] | e[7] << 16};
+}
+
 // Copies 16 bytes per lane from memory to LDS without passing registers: lane l
 // of the wavefront writes dst + 16 l (dst is the wavefront's).  The copy is in
 // flight until copies_done(); a barrier after that shows it to the workgroup.

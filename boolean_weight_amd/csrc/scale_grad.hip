@@ -33,7 +33,6 @@
 namespace mbok {
 namespace {
 
-typedef __attribute__((ext_vector_type(4), aligned(2))) uint32_t u32x4_any;  // dY rows start anywhere
 typedef __attribute__((ext_vector_type(4))) short i16x4;
 
 constexpr int kTile = 256;     // rows and columns of a tile
@@ -119,13 +118,7 @@ __global__ void __launch_bounds__(kThreads) scale_grad_kernel(
     u32x4 y[4];
   };
   Regs R0, R1;
-  auto load_dy = [&](const uint16_t* q) {
-    if (live == 8) return u32x4(*reinterpret_cast<const u32x4_any*>(q));
-    uint32_t e[8];
-#pragma unroll
-    for (int c = 0; c < 8; ++c) e[c] = c < live ? q[c] : 0u;
-    return u32x4{e[0] | e[1] << 16, e[2] | e[3] << 16, e[4] | e[5] << 16, e[6] | e[7] << 16};
-  };
+  auto load_dy = [&](const uint16_t* q) { return load_piece(q, live, m >= 8); };
   auto load_y = [&](int s, Regs& R) {
 #pragma unroll
     for (int u = 0; u < 4; ++u)
@@ -317,8 +310,14 @@ __global__ void __launch_bounds__(256) scale_grad_reduce_kernel(const float* __r
                                                                 int accumulate) {
   const int64_t e = (int64_t)blockIdx.x * 256 + threadIdx.x;
   if (e >= count) return;
-  float s = part[e];
-  for (int k = 1; k < slices; ++k) s += part[k * count + e];
+  float s = 0.f;
+  for (int k = 0; k < slices; k += 8) {  // eight loads at a time, added in order
+    float v[8];
+#pragma unroll
+    for (int u = 0; u < 8; ++u) v[u] = k + u < slices ? part[(int64_t)(k + u) * count + e] : 0.f;
+#pragma unroll
+    for (int u = 0; u < 8; ++u) s += v[u];
+  }
   out[e] = accumulate ? out[e] + s : s;
 }
 
@@ -328,7 +327,8 @@ int grad_slices(const Geom& geo, int64_t T) {
   const int64_t tiles = (int64_t)((geo.n + kTile - 1) / kTile) * ((geo.m + kTile - 1) / kTile);
   int64_t s = kUnits / tiles;
   const int64_t steps = (T + kSteps - 1) / kSteps;
-  if (s > steps / 4) s = steps / 4;  // four steps each at least
+  if (s > steps / 2) s = steps / 2;  // two steps each at least
+  if (s > 32) s = 32;                // what the joining kernel adds per scale
   return s < 1 ? 1 : (int)s;
 }
 
