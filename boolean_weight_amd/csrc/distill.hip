@@ -131,6 +131,15 @@ __device__ __forceinline__ float exp_listed(float d, const DistillRow& r) {
   return a < -126.f ? 0.f : fmaf(e * kLn2, lo, e);
 }
 
+// exp(x) to about 1 ulp of fp32 for a float64 x: the argument's low part to
+// first order.
+__device__ __forceinline__ float exp_fine(double x) {
+  const double a = x * 1.4426950408889634074;
+  const float hi = (float)a;
+  const float e = __builtin_amdgcn_exp2f(hi);
+  return hi < -126.f ? 0.f : fmaf(e * kLn2, (float)(a - (double)hi), e);
+}
+
 // Sum of exp(d / tau) over a row: s the exponentials of the scaled arguments a,
 // m their moment sum e a, which corrects s for the rounding of the scale (the
 // roundings of the arguments themselves have either sign and average out).
@@ -374,7 +383,7 @@ __global__ void __launch_bounds__(kMaxThreads) distill_kernel(
         double log_p = 0.0;
         if (rest) {
           log_p = (double)l * inv_tau - log_n;
-          p = exp(log_p);
+          p = (double)exp_fine(log_p);
         } else {
           log_p = ((double)l - shift) * inv_tau - log_n;
           p = (double)exp_listed(l - st.tmax, r) / Nsum;
@@ -458,7 +467,7 @@ __global__ void __launch_bounds__(kMaxThreads) distill_backward_kernel(
     float p = 0.f;
     if (v >= 0) {
       const float l = teacher_logit(t_logits, t_dtype, t * ldt + j);
-      p = t_lse ? (float)exp((double)l / (double)r.tau - (double)t_lse[t])
+      p = t_lse ? exp_fine((double)l * (1.0 / (double)r.tau) - (double)t_lse[t])
                 : exp_listed(l - st.tmax, r) * st.inv_n;
       if (!(st.inv_n > 0.f)) p = 0.f;
       zl[j] = to_f32(row[v]);

@@ -642,15 +642,24 @@ TokenKernel token_kernel(const mbok_desc* d, int64_t T) {
   return kTokSkinny;
 }
 
-// the gated block's kernel by the same rule (d: the stacked layer); its
-// one-token form is always the matrix-core decode kernel
+// The gated block's kernel (d: the stacked layer) by the same rule, except that
+// its one-token form is always the matrix-core decode kernel, and that 7 and 8
+// tokens, the rest of the octet one product holds, stay on the per-group form
+// where the layer has at least 2^27 sign bits (measured, us, per-group form
+// against bf16 +-1: two 11008x4096, K = 3 13.9 / 20.0 at 8 tokens; two
+// 13824x5120, K = 3 19.5 / 34.4; two 4096x4096, K = 2 8.8 / 7.7; its two-octet
+// form for 16 tokens 21.9 / 21.8).
 int launch_gated_stacked(const mbok_desc* d, const void* packed, const void* X, int64_t T,
                          int64_t ldx, const GatedOut& out, hipStream_t stream) {
   if (T > skinny_max_tokens()) return launch_gated_mfma(d, packed, X, T, ldx, out, stream);
   if (T == 1) return launch_gated_f4(d, packed, X, T, ldx, out, stream);
-  if ((T - 1) * ldx + d->n <= INT32_MAX && token_kernel(d, T) != kTokSkinny &&
-      T <= gated_f4_max_tokens())
-    return launch_gated_f4(d, packed, X, T, ldx, out, stream);
+  if ((T - 1) * ldx + d->n <= INT32_MAX && T <= gated_f4_max_tokens()) {
+    const char* v = getenv("MBOK_SKINNY_VARIANT");
+    const bool octet = T > 6 && !(v && *v) &&
+                       (int64_t)d->K * d->m * d->n >= (int64_t(1) << 27);
+    if (octet || token_kernel(d, T) != kTokSkinny)
+      return launch_gated_f4(d, packed, X, T, ldx, out, stream);
+  }
   return launch_gated_skinny(d, packed, X, T, ldx, out, stream);
 }
 
