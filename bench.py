@@ -156,12 +156,18 @@ def code_text(src: str) -> str:
     return re.sub(r"\s+", " ", "".join(out)).strip()
 
 
+# headers that hold the bodies of a source's kernels
+KERNEL_HEADERS = {"gemv_f4.hip": ["f4_body.h"], "gemm.hip": ["mbok_levels.h"]}
+
+
 def source_digest(T, m=None, n=None, K=None):
     """Digest of the code (comments and layout aside) of the kernel source one
-    call runs and of the shared device header."""
+    call runs, of the headers with its kernels' bodies and of the shared
+    device header."""
     import hashlib
     h = hashlib.sha256()
-    for f in (kernel_family(T, m, n, K)[0], "mbok_device.h"):
+    source = kernel_family(T, m, n, K)[0]
+    for f in [source, *KERNEL_HEADERS.get(source, []), "mbok_device.h"]:
         with open(os.path.join(CSRC, f), encoding="utf-8") as fh:
             h.update(code_text(fh.read()).encode())
     return h.hexdigest()[:16]

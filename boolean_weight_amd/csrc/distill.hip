@@ -204,27 +204,33 @@ __device__ __forceinline__ void write_entries(const RowLds& s, const DistillRow&
   }
 }
 
-// The main pass's dz = exp((z - zmax) / tau) A.  For 16-bit gradients the factor
-// is folded into the exponent, exp2(z c + k): k's rounding (2^-24 of |k| < 2^8)
-// is far below theirs.
+// The main pass's dz = exp((z - zmax) / tau) A of a vector.  For 16-bit gradients
+// the factor is folded into the exponent, exp2(z c + k), where the largest
+// logit is small enough for k's rounding (2^-24 of |k|) to stay far below
+// theirs; it takes two instructions fewer.
 template <typename OT>
 struct GradScale {
-  static constexpr bool kFold = sizeof(OT) == 2;
   float A, zmax, c, k;
   uint32_t sign;
+  bool fold;  // the same for the whole row
   __device__ __forceinline__ GradScale(float A_, float zmax_, const DistillRow& r)
-      : A(A_), zmax(zmax_), c(r.c_hi) {
-    if (kFold) {
-      sign = __float_as_uint(A) & 0x80000000u;
-      // A = 0 (or a row without an answer) goes through the exponent as well:
-      // log2 0 = -inf gives 0, NaN stays NaN
-      k = __builtin_amdgcn_logf(fabsf(A)) - zmax * c;
-    }
+      : A(A_), zmax(zmax_), c(r.c_hi), k(0.f), sign(__float_as_uint(A_) & 0x80000000u) {
+    const float shift = zmax * c;
+    fold = sizeof(OT) == 2 && fabsf(shift) < 256.f;
+    // A = 0 goes through the exponent as well (log2 0 = -inf gives 0), NaN stays
+    if (fold) k = __builtin_amdgcn_logf(fabsf(A)) - shift;
   }
-  __device__ __forceinline__ float operator()(float z) const {
-    if (kFold)
-      return __uint_as_float(__float_as_uint(__builtin_amdgcn_exp2f(fmaf(z, c, k))) ^ sign);
-    return __builtin_amdgcn_exp2f((z - zmax) * c) * A;
+  template <typename ZT, int N>
+  __device__ __forceinline__ void operator()(const Vec<ZT>& x, float (&d)[N]) const {
+    if (fold) {
+#pragma unroll
+      for (int e = 0; e < N; ++e)
+        d[e] = __uint_as_float(
+            __float_as_uint(__builtin_amdgcn_exp2f(fmaf(to_f32(x.v[e]), c, k))) ^ sign);
+    } else {
+#pragma unroll
+      for (int e = 0; e < N; ++e) d[e] = __builtin_amdgcn_exp2f((to_f32(x.v[e]) - zmax) * c) * A;
+    }
   }
 };
 
@@ -424,8 +430,7 @@ __global__ void __launch_bounds__(kMaxThreads) distill_kernel(
   const GradScale<OT> scale(Au, mx, r);
   each([&](int v, const Vec<ZT>& x) {
     float d[N];
-#pragma unroll
-    for (int e = 0; e < N; ++e) d[e] = scale(to_f32(x.v[e]));
+    scale(x, d);
     store_vec<OT, N>(drow, v, r.V, d);
   });
   __syncthreads();
@@ -484,8 +489,7 @@ __global__ void __launch_bounds__(kMaxThreads) distill_backward_kernel(
   for (int v = tid; v < nvec; v += nt) {
     const Vec<ZT> x = load_vec(row, v, r.V);
     float d[N];
-#pragma unroll
-    for (int e = 0; e < N; ++e) d[e] = scale(to_f32(x.v[e]));
+    scale(x, d);
     store_vec<OT, N>(drow, v, r.V, d);
   }
   __syncthreads();

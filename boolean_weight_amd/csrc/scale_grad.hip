@@ -119,10 +119,13 @@ __global__ void __launch_bounds__(kThreads) scale_grad_kernel(
   };
   Regs R0, R1;
   auto load_dy = [&](const uint16_t* q) { return load_piece(q, live, m >= 8); };
-  auto load_y = [&](int s, Regs& R) {
+  auto load_y = [&](int s, Regs& R, auto edge) {
 #pragma unroll
-    for (int u = 0; u < 4; ++u)
-      R.y[u] = load_dy(dY + ((int64_t)s * kSteps + ct + 16 * u) * lddy + yc);
+    for (int u = 0; u < 4; ++u) {
+      const uint16_t* q = dY + ((int64_t)s * kSteps + ct + 16 * u) * lddy + yc;
+      if constexpr (decltype(edge)::value) R.y[u] = load_dy(q);
+      else R.y[u] = u32x4(*reinterpret_cast<const u32x4_unaligned*>(q));
+    }
   };
   auto store_y = [&](int b, const Regs& R, int u) {
     *reinterpret_cast<u32x4*>(ybuf(b) + slot(u) + lane * 8) = R.y[u];
@@ -204,7 +207,7 @@ __global__ void __launch_bounds__(kThreads) scale_grad_kernel(
   // during that quarter.  DIRECT: dY goes straight to LDS too; otherwise
   // (unaligned rows, a tile across the last row) by way of registers, loaded
   // two steps before they are stored.
-  auto walk = [&](auto direct_c) {
+  auto walk = [&](auto direct_c, auto edge) {
     constexpr bool DIRECT = decltype(direct_c)::value;
     const int S = full_end - s0;
     if (S <= 0) return;
@@ -214,8 +217,8 @@ __global__ void __launch_bounds__(kThreads) scale_grad_kernel(
     if constexpr (DIRECT) {
       copy_y(at(0), 0);
     } else {
-      load_y(at(0), R0);
-      load_y(at(1), R1);
+      load_y(at(0), R0, edge);
+      load_y(at(1), R1, edge);
 #pragma unroll
       for (int u = 0; u < 4; ++u) store_y(0, R0, u);
     }
@@ -223,7 +226,7 @@ __global__ void __launch_bounds__(kThreads) scale_grad_kernel(
     __syncthreads();
     copy_x(at(1), 1);
     if constexpr (DIRECT) copy_y(at(1), 1);
-    else load_y(at(2), R0);
+    else load_y(at(2), R0, edge);
     first_operands(0);
     auto step = [&](int s, int b, Regs& R) {
 #pragma unroll
@@ -237,7 +240,7 @@ __global__ void __launch_bounds__(kThreads) scale_grad_kernel(
       __syncthreads();
       copy_x(at(s + 2), b);
       if constexpr (DIRECT) copy_y(at(s + 2), b);
-      else load_y(at(s + 3), R);
+      else load_y(at(s + 3), R, edge);
       __builtin_amdgcn_sched_barrier(0);
       products(3, b ^ 1, 0, [](int) {});
     };
@@ -248,10 +251,12 @@ __global__ void __launch_bounds__(kThreads) scale_grad_kernel(
     }
     copies_done();
   };
-  if (aligned && i0 + kTile <= m)
-    walk(std::true_type{});
+  if (i0 + kTile > m)
+    walk(std::false_type{}, std::true_type{});
+  else if (aligned)
+    walk(std::true_type{}, std::false_type{});
   else
-    walk(std::false_type{});
+    walk(std::false_type{}, std::false_type{});
   if (tail) {
     __syncthreads();
     store_tail(full_end, 0);

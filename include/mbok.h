@@ -512,7 +512,8 @@ int mbok_gemm_precise(const mbok_desc* d, const void* packed, const void* X,
  * activations, and what the layer below takes as its dY).  Row sums run in a
  * fixed order: results are bit-reproducible for a given workspace choice.
  *  packed    device, MBOK_LAYOUT_L64 buffer of this descriptor.
- *  dY        device bf16 [T, lddy], lddy >= m, 2-byte aligned.
+ *  dY        device bf16 [T, lddy], lddy >= m, 2-byte aligned (16-byte
+ *            aligned rows, lddy % 8 == 0, run faster).
  *  T         1 .. MBOK_MAX_T.
  *  dX        device bf16 [T, lddx], lddx >= n, lddx % 8 == 0; overwritten.
  *            Must not overlap dY.
@@ -543,8 +544,10 @@ size_t mbok_gemmt_workspace_bytes(const mbok_desc* d, int64_t T);
  * bf16 products, fp32 sums), contracted with the signs in fp32 and never
  * stored.
  *  packed     device, the layer's buffer (its signs are read, not its scales).
- *  dY         device bf16 [T, lddy], lddy >= m, 2-byte aligned.
+ *  dY         device bf16 [T, lddy], lddy >= m, 2-byte aligned (16-byte
+ *             aligned rows, lddy % 8 == 0, run faster).
  *  X          device bf16 [T, ldx], ldx >= n, ldx % 8 == 0, 16-byte aligned.
+ *             Leading dimensions below 2^26.
  *  T          1 .. MBOK_MAX_T.
  *  dalpha     device fp32 [K][m][n/128] (the order of mbok_pack's alpha).
  *  accumulate 0 overwrites dalpha; otherwise the result is added to it
@@ -617,10 +620,12 @@ int mbok_gated_pack(const mbok_desc* d, const int8_t* signs_gate, const void* al
  *          each rounded once to bf16, in the stacked order (padding columns
  *          are written as 0), for mbok_gated_backward.  16-byte aligned,
  *          ldpre % 8 == 0.
+ * Weights: exact per scale (see mbok_gemm) for T <= 16, levels rounded to bf16
+ * for larger T.  H and pre must not overlap X or each other.
  * For T <= 16 a non-finite activation of a token makes its H (and pre) NaN on
  * the matrix-core paths; larger T follow IEEE arithmetic.
- * Errors: INVALID_ARG (NULL, act, leading dimensions), SHAPE (T; a stacked
- * layer of 2^32 or more sign words for T > 16), DTYPE (x_dtype other than
+ * Errors: INVALID_ARG (NULL, act, leading dimensions; ldx >= 2^23 for T > 16),
+ * SHAPE (T; a stacked layer of 2^32 or more sign words for T > 16), DTYPE (x_dtype other than
  * MBOK_BF16), ALIGN, HIP, mbok_gated_stack's.
  */
 int mbok_gated(const mbok_desc* d, const void* packed, const void* X, int32_t x_dtype,

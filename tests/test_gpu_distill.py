@@ -203,6 +203,43 @@ def test_distill_masked_vocabulary_and_bad_rows():
         assert torch.isnan(dZ[[3, 4, 5, 6]]).all()
 
 
+@pytest.mark.parametrize("shift", [-3000.0, 300.0, 3.0e4])
+def test_distill_large_logits(shift):
+    """Logits far from zero: only differences count (as far as the type keeps
+    them: the reference takes the rounded logits)."""
+    for z in ("f32", "f16", "bf16"):
+        say(f"distill shift {shift} {z}")
+        Z, l, idx, teacher = inputs(3, 900, 12, "f32", 19)
+        Z = (Z + shift).to(TYPES[z])
+        lse = torch.logsumexp(teacher, -1)
+        for t_lse in (None, lse):
+            check(*run(Z, l, idx, 1.0, t_lse), Z, l, idx, 1.0, t_lse)
+            check(*run(Z, l, idx, 1.0, t_lse, mode="pair"), Z, l, idx, 1.0, t_lse)
+
+
+def test_distill_largest_values():
+    """The type's largest finite logits: the row's mass is on them."""
+    say("distill largest values")
+    for z in ("f32", "bf16", "f16"):
+        big = torch.finfo(TYPES[z]).max
+        Z = torch.zeros(2, 100, dtype=TYPES[z])
+        Z[0, 7], Z[1, 3], Z[1, 50] = big, big, big
+        l, idx = torch.zeros(2, 2), torch.tensor([[7, 9], [3, 50]], dtype=torch.int32)
+        loss, dZ = run(Z, l, idx, 1.0)
+        want = torch.zeros(2, 100)
+        want[0, 7], want[0, 9] = 0.5, -0.5
+        assert torch.equal(dZ.cpu().float(), want)
+
+
+def test_distill_longest_list_of_the_largest_vocabulary():
+    say("distill largest")
+    V, top = bw.MBOK_MAX_VOCAB, bw.MBOK_MAX_TOP
+    Z, l, idx, teacher = inputs(1, V, top, "bf16", 3)
+    idx[0, 5] = idx[0, 900]
+    lse = torch.logsumexp(teacher, -1)
+    check(*run(Z, l, idx, 1.0, lse), Z, l, idx, 1.0, lse)
+
+
 def test_distill_strides_and_neighbours():
     """Rows at odd elements inside wider buffers: nothing outside is written."""
     say("distill strides")

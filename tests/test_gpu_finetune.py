@@ -279,6 +279,22 @@ def test_gated_few_token_forms(variant, monkeypatch):
         assert ((H - h).abs() <= (U + 2.0 ** -14) * h.abs() + 2.0 ** -100).all()
 
 
+def test_gated_octet_rule(monkeypatch):
+    """7 and 8 tokens of a large layer take the per-group form: its bits."""
+    m, n, K = 6000, 4096, 3
+    a, b = gauss_layer(m, n, K, "f16", 3), gauss_layer(m, n, K, "f16", 4)
+    d, packed = gated_layer(a, b, "f16")
+    for T in (7, 8):
+        say(f"gated octet T={T}")
+        X = wide(gauss(T, n, T), n)
+        H = [torch.empty(T, m, dtype=BF, device=DEV) for _ in range(2)]
+        monkeypatch.delenv("MBOK_SKINNY_VARIANT", raising=False)
+        bw.mbok_gated(d, packed, X, H[0])
+        monkeypatch.setenv("MBOK_SKINNY_VARIANT", "f4g")
+        bw.mbok_gated(d, packed, X, H[1])
+        assert torch.equal(*H)
+
+
 @pytest.mark.parametrize("T", [1, 2, 4, 16, 100, 600])
 def test_gated_gaussian(T):
     """|H - ref| <= the activation's slope (at most 1.13) times g's error times
