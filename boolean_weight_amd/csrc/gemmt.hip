@@ -64,11 +64,12 @@ __device__ __forceinline__ bf16x8 read_tr(const uint16_t* p, const uint16_t* p4)
   return __builtin_bit_cast(bf16x8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
 }
 
-template <typename AT, int K, typename TL, bool PART, bool ALIGNED>
+// SLICED: every tile is (full = 0), which leaves the other epilogue out.
+template <typename AT, int K, typename TL, bool ALIGNED, bool SLICED>
 __global__ void __launch_bounds__(kThreads) gemmt_kernel(
     const uint32_t* __restrict__ bits, const AT* __restrict__ scales,
     const uint16_t* __restrict__ dY, int64_t lddy, uint16_t* __restrict__ dX, int64_t lddx,
-    float* __restrict__ part, int T, int m, int n, int RB, int slices) {
+    float* __restrict__ part, int T, int m, int n, int RB, int full, int rest, int slices) {
   constexpr int TI = TL::TI, TJ = TL::TJ, BT = TL::BT;
   constexpr int NA = (BT * 8 + kThreads - 1) / kThreads;  // 16-byte pieces of dY per thread
   extern __shared__ __attribute__((aligned(16))) uint16_t smem[];
@@ -76,16 +77,24 @@ __global__ void __launch_bounds__(kThreads) gemmt_kernel(
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int G = n / kGroup;
   const int ntx = (n + kBN - 1) / kBN, nty = (T + BT - 1) / BT;
-  const int ntiles = ntx * nty;
-  // workgroup -> (slice, tile): consecutive positions on one XCD
-  int p = blockIdx.x;
-  const int nb = ntiles * slices;
-  if ((nb & 7) == 0) p = (p & 7) * (nb >> 3) + (p >> 3);
-  const int slice = p / ntiles;
-  const int tile = tile_at(p - slice * ntiles, ntx, nty);
+  // workgroup -> tile and slice: the first `full` workgroups a whole tile each,
+  // the others slices of the last `rest` tiles, slice by slice (unit u of them
+  // has its own partial sums); consecutive positions on one XCD in either part
+  int p = blockIdx.x, unit = -1, slice = 0;
+  if (!SLICED && p < full) {
+    if ((full & 7) == 0) p = (p & 7) * (full >> 3) + (p >> 3);
+  } else {
+    unit = p - full;
+    const int nu = rest * slices;
+    if ((nu & 7) == 0) unit = (unit & 7) * (nu >> 3) + (unit >> 3);
+    slice = unit / rest;
+    p = full + unit - slice * rest;
+  }
+  const int parts = SLICED || unit >= 0 ? slices : 1;
+  const int tile = tile_at(p, ntx, nty);
   const int t0 = (tile / ntx) * BT, j0 = (tile % ntx) * kBN;
-  const int rb0 = (int)((int64_t)RB * slice / slices);
-  const int rb1 = (int)((int64_t)RB * (slice + 1) / slices);
+  const int rb0 = (int)((uint32_t)RB * slice / parts);  // RB < 2^26, 32 slices at most
+  const int rb1 = (int)((uint32_t)RB * (slice + 1) / parts);
   // steps over whole row blocks; a partial last block is the tail
   const int full_end = min(rb1, m / kRowBlock);
   const int S = full_end - rb0;  // may be 0 or less
@@ -332,46 +341,69 @@ __global__ void __launch_bounds__(kThreads) gemmt_kernel(
   }
 
   // C layout: lane l, register r -> token 8 (r / 4) + 4 (l / 32) + r % 4, column l % 32
+  const int tb = wt * TI * 32 + 4 * (lane >> 5), cb = wn * TJ * 32 + (lane & 31);
+  if (SLICED || unit >= 0) {
+    float* dst = part + (int64_t)unit * (min(T, BT) * kBN);
+#pragma unroll
+    for (int i = 0; i < TI; ++i)
+#pragma unroll
+      for (int j = 0; j < TJ; ++j)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) {
+          const int t = tb + 32 * i + 8 * (r >> 2) + (r & 3);
+          if (t0 + t < T) dst[t * kBN + cb + 32 * j] = acc[i][j][r];
+        }
+    return;
+  }
+  // rounded and, through LDS (free by now), to whole 16-byte stores
+  constexpr int OS = kBN + 8;
+  static_assert((size_t)BT * OS * 2 <= TL::kLds, "the output tile fits the buffers");
+  __syncthreads();
 #pragma unroll
   for (int i = 0; i < TI; ++i)
 #pragma unroll
-    for (int j = 0; j < TJ; ++j) {
-      const int col = j0 + (wn * TJ + j) * 32 + (lane & 31);
-      if (col >= n) continue;
+    for (int j = 0; j < TJ; ++j)
 #pragma unroll
-      for (int r = 0; r < 16; ++r) {
-        const int t = t0 + (wt * TI + i) * 32 + 8 * (r >> 2) + 4 * (lane >> 5) + (r & 3);
-        if (t >= T) continue;
-        if (PART) {
-          part[((int64_t)slice * T + t) * n + col] = acc[i][j][r];
-        } else {
-          dX[(int64_t)t * lddx + col] =
-              __builtin_bit_cast(uint16_t, (__bf16)acc[i][j][r]);
-        }
-      }
-    }
+      for (int r = 0; r < 16; ++r)
+        smem[(tb + 32 * i + 8 * (r >> 2) + (r & 3)) * OS + cb + 32 * j] =
+            __builtin_bit_cast(uint16_t, (__bf16)acc[i][j][r]);
+  __syncthreads();
+  for (int e = tid; e < BT * (kBN / 8); e += kThreads) {
+    const int t = e / (kBN / 8), c = 8 * (e % (kBN / 8));
+    if (t0 + t < T && j0 + c < n)
+      *reinterpret_cast<u32x4*>(dX + (int64_t)(t0 + t) * lddx + j0 + c) =
+          *reinterpret_cast<const u32x4*>(smem + t * OS + c);
+  }
 }
 
-// dX = sum of the slices' partial sums in order, rounded once; 4 columns per thread
+// The tiles that were sliced: the slices' partial sums added in order and rounded
+// once; 4 columns per thread.
 __global__ void __launch_bounds__(256) gemmt_reduce_kernel(const float* __restrict__ part,
                                                            uint16_t* __restrict__ dX,
-                                                           int64_t lddx, int T, int n,
-                                                           int slices) {
-  const int64_t e = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4;
-  const int64_t total = (int64_t)T * n;
-  if (e >= total) return;
+                                                           int64_t lddx, int T, int n, int bt,
+                                                           int full, int rest, int slices) {
+  // a block takes 4 rows of one tile; all offsets are below kUnits tiles' worth
+  const int idx = blockIdx.y, rows = min(T, bt), stride = rest * rows * kBN;
+  const int row = blockIdx.x * 4 + (threadIdx.x >> 6), col = (threadIdx.x & 63) * 4;
+  if (row >= rows) return;
+  const float* src = part + (idx * rows + row) * kBN + col;
   float s[4] = {0.f, 0.f, 0.f, 0.f};
-  for (int k = 0; k < slices; k += 8) {  // eight loads at a time, added in order
+  for (int k = 0; k < slices; k += 8) {  // eight loads at a time
     float4 v[8];
 #pragma unroll
     for (int u = 0; u < 8; ++u)
-      v[u] = k + u < slices ? *reinterpret_cast<const float4*>(part + (k + u) * total + e)
+      v[u] = k + u < slices ? *reinterpret_cast<const float4*>(src + (k + u) * stride)
                             : make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
     for (int u = 0; u < 8; ++u) s[0] += v[u].x, s[1] += v[u].y, s[2] += v[u].z, s[3] += v[u].w;
   }
-  const int64_t t = e / n, j = e - t * n;
-  *reinterpret_cast<uint2*>(dX + t * lddx + j) =
+  // where it goes: after the loads, which the divisions would hold up (2.5 -> 2.1 us);
+  // what a tile has outside T x n was not written, and is not stored
+  const int ntx = (n + kBN - 1) / kBN, nty = (T + bt - 1) / bt;
+  const int tile = tile_at(full + idx, ntx, nty);
+  const int t = (tile / ntx) * bt + row, j = (tile % ntx) * kBN + col;
+  if (t >= T || j >= n) return;
+  *reinterpret_cast<uint2*>(dX + (int64_t)t * lddx + j) =
       make_uint2(bf16_pair(s[0], s[1]), bf16_pair(s[2], s[3]));
 }
 
@@ -386,85 +418,98 @@ int tile_tokens(const Geom& geo, int64_t T) {
   return bt;
 }
 
-// Slices of the row blocks: as many as keep the workgroups within one round,
-// of two steps at least
-int gemmt_slices(const Geom& geo, int64_t T) {
-  const int bt = tile_tokens(geo, T);
-  const int64_t tiles = ((geo.n + kBN - 1) / kBN) * ((T + bt - 1) / bt);
-  int64_t s = kUnits / tiles;
-  if (s > geo.RB / 2) s = geo.RB / 2;
-  if (s > 32) s = 32;  // what the joining kernel adds per output
-  return s < 1 ? 1 : (int)s;
+// Whole rounds of whole tiles; the row blocks of the tiles that are left in
+// as many slices as keep them within one more round, of two steps at least.
+// (4096 x 11008, 2048 tokens: 344 tiles, 256 whole and 88 in two slices.)
+struct Split {
+  int bt, full, rest, slices;
+};
+Split gemmt_split(const Geom& geo, int64_t T, bool workspace) {
+  Split s;
+  s.bt = tile_tokens(geo, T);
+  const int64_t tiles = ((geo.n + kBN - 1) / kBN) * ((T + s.bt - 1) / s.bt);
+  s.full = (int)tiles;
+  s.rest = 0;
+  s.slices = 1;
+  if (!workspace || tiles % kUnits == 0) return s;
+  const int64_t rest = tiles % kUnits;
+  int64_t k = kUnits / rest;
+  if (k > geo.RB / 2) k = geo.RB / 2;
+  if (k > 32) k = 32;  // what the joining kernel adds per output
+  if (k > 1) {
+    s.full = (int)(tiles - rest);
+    s.rest = (int)rest;
+    s.slices = (int)k;
+  }
+  return s;
 }
 
 template <typename AT, int K>
 int launch_k(const Geom& geo, const void* packed, const uint16_t* dY, int64_t T, int64_t lddy,
-             uint16_t* dX, int64_t lddx, float* part, int slices, hipStream_t stream) {
+             uint16_t* dX, int64_t lddx, float* part, const Split& s, hipStream_t stream) {
   // straight copies to LDS take 16-byte aligned rows at 32-bit offsets
   const bool aligned =
       ((uintptr_t)dY & 15) == 0 && (lddy % 8) == 0 && lddy < (int64_t(1) << 32) / 512;
   const uint32_t* bits = reinterpret_cast<const uint32_t*>(packed);
   const AT* scales = reinterpret_cast<const AT*>(reinterpret_cast<const char*>(packed) +
                                                  geo.bits_bytes);
-  auto go = [&](auto tl, auto partial) {
+  auto go = [&](auto tl) {
     using TL = decltype(tl);
-    constexpr bool P = decltype(partial)::value;
-    const int64_t blocks = (int64_t)((geo.n + kBN - 1) / kBN) * ((T + TL::BT - 1) / TL::BT) * slices;
     auto launch = [&](auto kernel) {
-      hipLaunchKernelGGL(kernel, dim3((unsigned)blocks), dim3(kThreads), TL::kLds, stream, bits,
-                         scales, dY, lddy, dX, lddx, part, (int)T, geo.m, geo.n, geo.RB, slices);
+      hipLaunchKernelGGL(kernel, dim3((unsigned)(s.full + s.rest * s.slices)), dim3(kThreads),
+                         TL::kLds, stream, bits, scales, dY, lddy, dX, lddx, part, (int)T, geo.m,
+                         geo.n, geo.RB, s.full, s.rest, s.slices);
     };
-    if (aligned) launch(gemmt_kernel<AT, K, TL, P, true>);
-    else launch(gemmt_kernel<AT, K, TL, P, false>);
-  };
-  auto by_tile = [&](auto partial) {
-    switch (tile_tokens(geo, T)) {
-      case 32: go(Tile<1, 1, 1>{}, partial); break;
-      case 64: go(Tile<2, 1, 1>{}, partial); break;
-      case 128: go(Tile<4, 1, 1>{}, partial); break;
-      default: go(Tile<4, 2, 2>{}, partial); break;
+    if (s.full == 0) {
+      if (aligned) launch(gemmt_kernel<AT, K, TL, true, true>);
+      else launch(gemmt_kernel<AT, K, TL, false, true>);
+    } else {
+      if (aligned) launch(gemmt_kernel<AT, K, TL, true, false>);
+      else launch(gemmt_kernel<AT, K, TL, false, false>);
     }
   };
-  if (slices > 1) {
-    by_tile(std::true_type{});
-    const int64_t threads = T * geo.n / 4;
-    hipLaunchKernelGGL(gemmt_reduce_kernel, dim3((unsigned)((threads + 255) / 256)), dim3(256), 0,
-                       stream, part, dX, lddx, (int)T, geo.n, slices);
-  } else {
-    by_tile(std::false_type{});
+  switch (s.bt) {
+    case 32: go(Tile<1, 1, 1>{}); break;
+    case 64: go(Tile<2, 1, 1>{}); break;
+    case 128: go(Tile<4, 1, 1>{}); break;
+    default: go(Tile<4, 2, 2>{}); break;
+  }
+  if (s.slices > 1) {
+    const int rows = T < s.bt ? (int)T : s.bt;
+    hipLaunchKernelGGL(gemmt_reduce_kernel, dim3((rows + 3) / 4, s.rest), dim3(256), 0, stream,
+                       part, dX, lddx, (int)T, geo.n, s.bt, s.full, s.rest, s.slices);
   }
   return hipGetLastError() == hipSuccess ? MBOK_OK : MBOK_ERR_HIP;
 }
 
 template <typename AT>
 int launch_t(const Geom& geo, const void* packed, const void* dY, int64_t T, int64_t lddy,
-             void* dX, int64_t lddx, float* part, int slices, hipStream_t stream) {
+             void* dX, int64_t lddx, float* part, const Split& s, hipStream_t stream) {
   const uint16_t* g = reinterpret_cast<const uint16_t*>(dY);
   uint16_t* o = reinterpret_cast<uint16_t*>(dX);
   switch (geo.K) {
-    case 1: return launch_k<AT, 1>(geo, packed, g, T, lddy, o, lddx, part, slices, stream);
-    case 2: return launch_k<AT, 2>(geo, packed, g, T, lddy, o, lddx, part, slices, stream);
-    case 3: return launch_k<AT, 3>(geo, packed, g, T, lddy, o, lddx, part, slices, stream);
-    default: return launch_k<AT, 4>(geo, packed, g, T, lddy, o, lddx, part, slices, stream);
+    case 1: return launch_k<AT, 1>(geo, packed, g, T, lddy, o, lddx, part, s, stream);
+    case 2: return launch_k<AT, 2>(geo, packed, g, T, lddy, o, lddx, part, s, stream);
+    case 3: return launch_k<AT, 3>(geo, packed, g, T, lddy, o, lddx, part, s, stream);
+    default: return launch_k<AT, 4>(geo, packed, g, T, lddy, o, lddx, part, s, stream);
   }
 }
 
 }  // namespace
 
 size_t gemmt_workspace_bytes(const mbok_desc* d, int64_t T) {
-  const Geom geo = make_geom(d);
-  const int s = gemmt_slices(geo, T);
-  return s > 1 ? (size_t)s * (size_t)T * (size_t)geo.n * sizeof(float) : 0;
+  const Split s = gemmt_split(make_geom(d), T, true);
+  return s.slices > 1 ? (size_t)s.rest * s.slices * (T < s.bt ? T : s.bt) * kBN * sizeof(float) : 0;
 }
 
 int launch_gemmt(const mbok_desc* d, const void* packed, const void* dY, int64_t T, int64_t lddy,
                  void* dX, int64_t lddx, void* ws, hipStream_t stream) {
   const Geom geo = make_geom(d);
-  const int slices = ws ? gemmt_slices(geo, T) : 1;
+  const Split s = gemmt_split(geo, T, ws != nullptr);
   float* part = reinterpret_cast<float*>(ws);
   if (d->alpha_dtype == MBOK_F16)
-    return launch_t<uint16_t>(geo, packed, dY, T, lddy, dX, lddx, part, slices, stream);
-  return launch_t<float>(geo, packed, dY, T, lddy, dX, lddx, part, slices, stream);
+    return launch_t<uint16_t>(geo, packed, dY, T, lddy, dX, lddx, part, s, stream);
+  return launch_t<float>(geo, packed, dY, T, lddy, dX, lddx, part, s, stream);
 }
 
 }  // namespace mbok

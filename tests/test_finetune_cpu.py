@@ -251,9 +251,11 @@ def test_workspace_bytes(lib):
         assert fn(ctypes.byref(BAD_DESC), 4) == 0
         assert fn(ctypes.byref(d), 0) == 0
         assert fn(ctypes.byref(d), bw.MBOK_MAX_T + 1) == 0
-    # few tokens: several slices of [T, n] sums
-    need = bw.mbok_gemmt_workspace_bytes(d, 16)
-    assert need > 0 and need % (16 * 4096 * 4) == 0
+    # few tokens: several slices of every 256-column tile's sums; many: of the
+    # tiles past whole rounds; whole rounds: none
+    assert bw.mbok_gemmt_workspace_bytes(d, 16) == 16 * 16 * (16 * 256 * 4)
+    assert bw.mbok_gemmt_workspace_bytes(d, 4096 + 256) == 16 * 16 * (256 * 256 * 4)
+    assert bw.mbok_gemmt_workspace_bytes(d, 4096) == 0
 
 
 def test_binding_refuses_host_tensors():

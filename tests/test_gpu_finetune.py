@@ -85,7 +85,8 @@ def gated_layer(a, b, dt):
 
 GEMMT = [(1, 1, 128), (2, 7, 128), (5, 63, 256), (16, 64, 384), (32, 65, 512), (33, 130, 640),
          (64, 200, 256), (65, 1000, 128), (128, 129, 1152), (129, 64, 256), (257, 300, 768),
-         (300, 128, 384), (40, 4096, 256), (513, 70, 11008)]
+         (300, 128, 384), (40, 4096, 256), (513, 70, 11008), (2049, 520, 7680),
+         (1025, 300, 13312)]
 
 
 @pytest.mark.parametrize("T,m,n", GEMMT)
