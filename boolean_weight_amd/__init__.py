@@ -46,7 +46,7 @@ MBOK_MAX_SVID_ITERS = 1000
 MBOK_ACT_SILU, MBOK_ACT_GELU = 0, 1
 MBOK_MAX_TOP = 1024
 MBOK_MAX_VOCAB = 1 << 19
-MBOK_MAX_DISTILL_ROWS = 1 << 24
+MBOK_MAX_DISTILL_ROWS = 1 << 23
 MBOK_DISTILL_STATS = 8
 
 _HERE = os.path.dirname(os.path.abspath(__file__))

@@ -507,6 +507,15 @@ size_t row_lds_bytes(const mbok_distill_desc* d) {
   return ((size_t)d->top * 3 + ((size_t)d->vocab + 31) / 32) * 4;
 }
 
+// Threads of a row's workgroup for `want` vectors each; a launch has fewer than
+// 2^32 threads (256 for each of MBOK_MAX_DISTILL_ROWS rows are 2^31).
+int row_threads(int64_t T, int nvec, int want) {
+  int threads = 256;
+  while (threads < kMaxThreads && threads * want < nvec && T * threads * 2 <= UINT32_MAX)
+    threads *= 2;
+  return threads;
+}
+
 template <typename ZT, typename OT>
 int launch_rows(const mbok_distill_desc* d, const DistillArgs& a, float* loss, float* stats,
                 hipStream_t stream) {
@@ -514,9 +523,7 @@ int launch_rows(const mbok_distill_desc* d, const DistillArgs& a, float* loss, f
   const size_t lds = row_lds_bytes(d);
   const DistillRow r = row_of(d);
   // 8 vectors per thread; with few rows, where latency counts, 2
-  const int want = a.T < 512 ? 2 : 8;
-  int threads = 256;
-  while (threads < kMaxThreads && threads * want < nvec) threads *= 2;
+  const int threads = row_threads(a.T, nvec, a.T < 512 ? 2 : 8);
   const int per = (nvec + threads - 1) / threads;
   auto go = [&](auto kernel) {
     hipLaunchKernelGGL(kernel, dim3((unsigned)a.T), dim3(threads), lds, stream,
@@ -541,8 +548,7 @@ template <typename ZT, typename OT>
 int launch_rows_backward(const mbok_distill_desc* d, const DistillArgs& a, const float* stats,
                          const float* dloss, hipStream_t stream) {
   const int nvec = (d->vocab + Vec<ZT>::N - 1) / Vec<ZT>::N;
-  int threads = 256;
-  while (threads < kMaxThreads && threads * 4 < nvec) threads *= 2;
+  const int threads = row_threads(a.T, nvec, 4);
   hipLaunchKernelGGL((distill_backward_kernel<ZT, OT>), dim3((unsigned)a.T), dim3(threads),
                      row_lds_bytes(d), stream, reinterpret_cast<const ZT*>(a.Z), a.ldz,
                      a.t_logits, a.t_dtype, a.t_index, a.ldt, a.t_lse, a.weight, row_of(d),

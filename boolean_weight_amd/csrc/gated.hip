@@ -63,7 +63,7 @@ int launch_gated_backward(const mbok_desc* d, const void* packed, const void* pr
                           int64_t lddpre, void* dX, int64_t lddx, void* ws, hipStream_t stream) {
   const int64_t items = T * ((d->m + 7) / 8);
   const int64_t blocks = (items + 255) / 256;
-  if (blocks > 0x7fffffff) return MBOK_ERR_SHAPE;
+  if (blocks > UINT32_MAX / 256) return MBOK_ERR_SHAPE;  // a launch has 2^32 threads at most
   hipLaunchKernelGGL(gated_backward_kernel, dim3((unsigned)blocks), dim3(256), 0, stream,
                      reinterpret_cast<const uint16_t*>(pre), ldpre,
                      reinterpret_cast<const uint16_t*>(dH), lddh,

@@ -625,8 +625,8 @@ int mbok_gated_pack(const mbok_desc* d, const int8_t* signs_gate, const void* al
  * For T <= 16 a non-finite activation of a token makes its H (and pre) NaN on
  * the matrix-core paths; larger T follow IEEE arithmetic.
  * Errors: INVALID_ARG (NULL, act, leading dimensions; ldx >= 2^23 for T > 16),
- * SHAPE (T; a stacked layer of 2^32 or more sign words for T > 16), DTYPE (x_dtype other than
- * MBOK_BF16), ALIGN, HIP, mbok_gated_stack's.
+ * SHAPE (T; a stacked layer of 2^32 or more sign words for T > 16), DTYPE
+ * (x_dtype other than MBOK_BF16), ALIGN, HIP, mbok_gated_stack's.
  */
 int mbok_gated(const mbok_desc* d, const void* packed, const void* X, int32_t x_dtype,
                int64_t T, int64_t ldx, int32_t act, void* H, int64_t ldh, void* pre,
@@ -645,8 +645,8 @@ int mbok_gated(const mbok_desc* d, const void* packed, const void* X, int32_t x_
  *  dX    device bf16 [T, lddx] or NULL (then only dpre is computed).
  *  workspace  device, mbok_gemmt_workspace_bytes(stacked, T) bytes or NULL,
  *        as for mbok_gemmt.
- * Errors: INVALID_ARG (NULL, act, leading dimensions), SHAPE (T), ALIGN
- * (packed, pre, dpre, dX 16 bytes, ldpre, lddpre, lddx % 8, dH 2 bytes,
+ * Errors: INVALID_ARG (NULL, act, leading dimensions), SHAPE (T; T ceil(m / 8)
+ * of 2^32 or more), ALIGN (packed, pre, dpre, dX 16 bytes, ldpre, lddpre, lddx % 8, dH 2 bytes,
  * workspace 256 bytes), HIP, mbok_gated_stack's.
  */
 int mbok_gated_backward(const mbok_desc* d, const void* packed, const void* pre,
@@ -658,7 +658,7 @@ int mbok_gated_backward(const mbok_desc* d, const void* packed, const void* pre,
  * mbok_distill, its most rows, and floats of statistics per row. */
 #define MBOK_MAX_TOP 1024
 #define MBOK_MAX_VOCAB (1 << 19)
-#define MBOK_MAX_DISTILL_ROWS (1 << 24)
+#define MBOK_MAX_DISTILL_ROWS (1 << 23)
 #define MBOK_DISTILL_STATS 8
 
 /* Shape of one distillation loss.  Fill it with mbok_distill_desc_init. */

@@ -170,6 +170,14 @@ def test_gated_backward_refuses(lib, change, err):
     assert call(lib.mbok_gated_backward, base, **change) == err
 
 
+def test_gated_backward_refuses_more_than_a_launch(lib):
+    m = 1 << 19
+    d = bw.mbok_desc_init(m, 512, 1, bw.MBOK_F16)
+    base, _d = gated_backward_args()
+    assert call(lib.mbok_gated_backward, base, d=ctypes.byref(d), T=bw.MBOK_MAX_T, lddh=m,
+                ldpre=2 * m, lddpre=2 * m) == -2
+
+
 @pytest.mark.parametrize("change,err", [
     (dict(d=None), -1), (dict(sg=None), -1), (dict(ag=None), -1), (dict(su=None), -1),
     (dict(au=None), -1), (dict(packed=None), -1), (dict(sg=P + 8), -4), (dict(ag=P + 8), -4),

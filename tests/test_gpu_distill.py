@@ -339,3 +339,28 @@ def test_distill_many_rows_graph_and_streams():
     torch.cuda.synchronize()
     for o in outs:
         assert torch.equal(o[0], want[0]) and torch.equal(o[1], want[1])
+
+
+def test_distill_most_rows():
+    """The most rows a call takes, of 8 tokens each: every row against the same
+    formulas in float64."""
+    T, V = bw.MBOK_MAX_DISTILL_ROWS, 8
+    say(f"distill T={T} V={V}")
+    gen = torch.Generator(device=DEV).manual_seed(5)
+    Z = torch.randn(T, V, generator=gen, device=DEV, dtype=torch.float32)
+    l = torch.zeros(T, 1, device=DEV)
+    idx = torch.randint(0, V, (T, 1), generator=gen, device=DEV, dtype=torch.int32)
+    d = bw.mbok_distill_desc_init(V, 1, 1.0)
+    loss = torch.full((T,), -5.0, device=DEV)
+    stats = torch.empty(T, bw.MBOK_DISTILL_STATS, device=DEV)
+    dZ, dZ2 = torch.empty_like(Z), torch.empty_like(Z)
+    bw.mbok_distill(d, Z, l, idx, loss, stats=stats, dZ=dZ)
+    bw.mbok_distill_backward(d, Z, l, idx, stats, torch.ones(T, device=DEV), dZ2)
+    logq = torch.log_softmax(Z.to(F64), -1)
+    want = -logq.gather(1, idx.long())[:, 0]
+    # |log q| < 16: 2^-16 and 2^-20 of it, as above
+    assert ((loss.to(F64) - want).abs() <= 2.0 ** -15).all()
+    grad = logq.exp()
+    grad.scatter_add_(1, idx.long(), torch.full((T, 1), -1.0, dtype=F64, device=DEV))
+    for g in (dZ, dZ2):
+        assert ((g.to(F64) - grad).abs() <= 2.0 ** -15).all()
