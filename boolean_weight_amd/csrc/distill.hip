@@ -12,7 +12,9 @@
 // Bound: the row of logits, read once and (gradient) written once.  One
 // workgroup takes one row and keeps it in registers as loaded (NV 16-byte
 // vectors per thread), so the maximum, the sum of exponentials and the
-// gradient cost one read.  Rows of more than 16 vectors for each of 1024
+// gradient cost one read (2048 rows of 32000 bf16 logits with the gradient:
+// 76 us, 3.4 TB/s read and written, against 53 us for a copy; what is left are
+// ~15 vector instructions per two logits).  Rows of more than 16 vectors for each of 1024
 // threads (131072 16-bit logits) are read again for each pass.  Rows start
 // at any element: the 16-byte accesses need no alignment on this part, and
 // the last, partial vector of a row goes element by element.

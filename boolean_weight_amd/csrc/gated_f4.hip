@@ -4,7 +4,9 @@
 // hold 8 gate rows and the same 8 up rows, with the activation and the
 // product applied where a tile's wavefront sums are added.  The two
 // projections, the activation and the product are one kernel and the fp32
-// pre-activations never leave it.
+// pre-activations never leave it.  Bound as there by the read of the signs (two
+// 11008 x 4096, K = 3: 8.6 us for one token, 38 MB; 13.9 us for 8 tokens,
+// where the bf16 +-1 kernel takes 20.6).
 #include "f4_body.h"
 #include "mbok_gated.h"
 

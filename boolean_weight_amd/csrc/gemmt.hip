@@ -16,6 +16,13 @@
 // LDS load ds_read_b64_tr_b16: of 16 lanes, lane s supplies the address of 4
 // columns 4 (s & 3) .. of row s >> 2, and receives column s of the 4 rows.
 //
+// Bound: the matrix cores (2 T m n operations; 4096 x 11008, K = 3, 2048
+// tokens: 172 us, 1072 TFLOP/s, matrix cores 63% busy), for few tokens the
+// steps of a slice, one LDS round trip each (5120 x 5120, 16 tokens: 12.7 us
+// against 1.8 us of reading).  256 columns because a weight is then formed once
+// per 256 tokens; the tokens of a tile by tile_tokens, the slices by
+// gemmt_split.
+//
 // Rows past m have zero weights, and dY is read inside its m columns only: a
 // partial last row block is a step of its own with element-wise loads.
 #include <stdint.h>

@@ -16,6 +16,11 @@
 // the transposing LDS load: of 16 lanes, lane s supplies the address of 4
 // columns 4 (s & 3) .. of token s >> 2, and receives column s of the 4 tokens.
 //
+// Bound: the matrix cores (2 T m n operations; 4096 x 11008, K = 3, 2048
+// tokens: 168 us, 1099 TFLOP/s, matrix cores 63% busy; dY rows that are not
+// 16-byte aligned pass registers: 4001 x 4096 117 us against 70).  A tile of
+// 256 x 256 reads each operand once per 256 columns or rows of the other.
+//
 // Contraction with the signs: lane l holds column l % 32 of each of the
 // group's four 32-column words for 32 rows, so per (row, word, kernel) one
 // shift brings the column's bit to the sign position and flips the sum's sign;
