@@ -13,8 +13,8 @@
 // workgroup takes one row and keeps it in registers as loaded (NV 16-byte
 // vectors per thread), so the maximum, the sum of exponentials and the
 // gradient cost one read (2048 rows of 32000 bf16 logits with the gradient:
-// 76 us, 3.4 TB/s read and written, against 53 us for a copy; what is left are
-// ~15 vector instructions per two logits).  Rows of more than 16 vectors for each of 1024
+// 74 us, 3.5 TB/s read and written, against 53 us for a copy; what is left are
+// ~12 vector instructions per logit).  Rows of more than 16 vectors for each of 1024
 // threads (131072 16-bit logits) are read again for each pass.  Rows start
 // at any element: the 16-byte accesses need no alignment on this part, and
 // the last, partial vector of a row goes element by element.
@@ -141,21 +141,6 @@ __device__ __forceinline__ float exp_fine(double x) {
   const float e = __builtin_amdgcn_exp2f(hi);
   return hi < -126.f ? 0.f : fmaf(e * kLn2, (float)(a - (double)hi), e);
 }
-
-// Sum of exp(d / tau) over a row: s the exponentials of the scaled arguments a,
-// m their moment sum e a, which corrects s for the rounding of the scale (the
-// roundings of the arguments themselves have either sign and average out).
-// A NaN d makes both NaN; -inf adds 0.
-struct ExpSum {
-  float s = 0.f, m = 0.f;
-  __device__ __forceinline__ void add(float e, float a) {
-    s += e;
-    m = fmaf(e, fmaxf(a, -150.f), m);
-  }
-  __device__ __forceinline__ double total(const DistillRow& r) const {
-    return (double)s + (double)m * ((double)kLn2 * (double)r.c_lo / (double)r.c_hi);
-  }
-};
 
 // The lists of one row in LDS: index (or -1), then p, then one bit per token.
 struct RowLds {
@@ -320,31 +305,46 @@ __global__ void __launch_bounds__(kMaxThreads) distill_kernel(
   if (twice) twice_any = 1;
   __syncthreads();
 
-  // sums of exponentials: all, and (with t_lse) the unlisted ones
-  ExpSum sa, sr;
+  // Sums of exponentials: all, and (with t_lse) the unlisted ones.  The scaled
+  // argument (z - max) c is one fma, z c - k with k = max c rounded, where k is
+  // small (2^klo then corrects the sums for that rounding, |klo| <= 2^-17: to
+  // first order), else subtracted first.  That c is log2(e) / tau rounded
+  // moves log sum by at most 2^-25 E_q[(max - z) / tau] <= 2^-25 log V, since
+  // that mean is the entropy of q less log sum.  (Carrying it exactly cost
+  // two instructions per logit, the subtraction one: 2048 x 32000 bf16 with
+  // gradient 76.5 -> 74.1 us.)
+  float sa = 0.f, sr = 0.f;
   const bool rest = t_lse != nullptr;
-  auto scaled = [&](ZT z) { return (to_f32(z) - mx) * r.c_hi; };
-  if (rest) {
-    each([&](int v, const Vec<ZT>& x) {
-      const uint32_t m = s.bits[(v * N) >> 5] >> ((v * N) & 31);
+  const float k = mx * r.c_hi;
+  const bool near = fabsf(k) < 256.f;
+  auto sum = [&](auto near_c) {
+    auto ex = [&](ZT z) {
+      return __builtin_amdgcn_exp2f(decltype(near_c)::value ? fmaf(to_f32(z), r.c_hi, -k)
+                                                            : (to_f32(z) - mx) * r.c_hi);
+    };
+    if (rest) {
+      each([&](int v, const Vec<ZT>& x) {
+        const uint32_t m = s.bits[(v * N) >> 5] >> ((v * N) & 31);
 #pragma unroll
-      for (int e = 0; e < N; ++e) {
-        const float a = scaled(x.v[e]), ex = __builtin_amdgcn_exp2f(a);
-        sa.add(ex, a);
-        sr.add((m >> e) & 1u ? 0.f : ex, a);
-      }
-    });
-  } else {
-    each([&](int, const Vec<ZT>& x) {
+        for (int e = 0; e < N; ++e) {
+          const float y = ex(x.v[e]);
+          sa += y;
+          sr += (m >> e) & 1u ? 0.f : y;
+        }
+      });
+    } else {
+      each([&](int, const Vec<ZT>& x) {
 #pragma unroll
-      for (int e = 0; e < N; ++e) {
-        const float a = scaled(x.v[e]);
-        sa.add(__builtin_amdgcn_exp2f(a), a);
-      }
-    });
-  }
+        for (int e = 0; e < N; ++e) sa += ex(x.v[e]);
+      });
+    }
+  };
+  if (near) sum(std::true_type{});
+  else sum(std::false_type{});
   {
-    const double da = wave_sum(sa.total(r)), dr = rest ? wave_sum(sr.total(r)) : 0.0;
+    const double fix =
+        near ? 1.0 - (double)kLn2 * ((double)mx * (double)r.c_hi - (double)k) : 1.0;
+    const double da = wave_sum((double)sa) * fix, dr = rest ? wave_sum((double)sr) * fix : 0.0;
     if (lane == 0) {
       red_d[2 * wave] = da;
       red_d[2 * wave + 1] = dr;

@@ -4,7 +4,7 @@ mbok_distill_backward) against the float64 reference, through the C ABI.
 Tolerances, derived (eps = 2^-24, the fp32 half step):
   loss   The exponentials of a row are summed in fp32 per thread (at most 128
          terms before float64) and each carries the hardware exponential's 1
-         ulp = 2 eps and its argument's correction: log S is off by at most
+         ulp = 2 eps; log2(e) / tau in fp32 moves log S by at most eps / 2 log V: log S is off by at most
          ~ 130 eps in the worst case, the listed p by ~ 8 eps relative.  So
          |loss - ref| <= w tau^2 (2^-16 + 2^-20 (|kl| + spread)), where spread
          bounds |log p - log q| over the listed entries with p > 0.
