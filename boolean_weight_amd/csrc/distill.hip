@@ -5,9 +5,11 @@
 // distillation from the full-precision model.  Per row, with q = softmax(z /
 // tau) over the vocabulary and the teacher's listed (index v_j, logit l_j):
 //     loss = w tau^2 [ sum_j p_j (log p_j - log q_{v_j}) + p_r log(p_r / q_r) ]
-//     dz_v = w tau [ q_v (1 - [v not listed] p_r / q_r) - sum_{j: v_j = v} p_j ]
-// where p is the softmax of the listed l / tau (then p_r = 0), or with t_lse
-// exp(l / tau - t_lse) and p_r = 1 - sum p the mass of what is not listed.
+//     dz_v = w tau [ q_v (s - [v not listed] p_r / q_r) - sum_{j: v_j = v} p_j ]
+// where p is the softmax of the listed l / tau (then p_r = 0 and s = 1), or
+// with t_lse exp(l / tau - t_lse) and p_r = 1 - sum p the mass of what is not
+// listed; s = sum p + p_r is 1 as well unless p_r is cut off at 0 (an index
+// listed twice, a t_lse that is too small) or its class drops out.
 //
 // Bound: the row of logits, read once and (gradient) written once.  One
 // workgroup takes one row and keeps it in registers as loaded (NV 16-byte
@@ -112,10 +114,11 @@ __device__ __forceinline__ float teacher_logit(const void* l, int dtype, int64_t
 struct RowStats {
   float zmax;    // largest logit
   float inv_s;   // 1 / sum exp((z - zmax) / tau)
-  float unlist;  // factor of q_v for unlisted v: 1 - p_r / q_r
+  float unlist;  // factor of q_v for unlisted v: mass - p_r / q_r
   float tmax;    // largest listed teacher logit (no t_lse)
   float inv_n;   // 1 / sum exp((l - tmax) / tau); 0: no teacher weight
-  float pad[3];
+  float mass;    // s, the sum of the teacher's masses: the factor of q_v for listed v
+  float pad[2];
 };
 static_assert(sizeof(RowStats) == MBOK_DISTILL_STATS * sizeof(float), "stats row");
 
@@ -187,7 +190,7 @@ __device__ __forceinline__ void write_entries(const RowLds& s, const DistillRow&
       p = s.p[j];
     }
     const float q = __builtin_amdgcn_exp2f((zl[j] - st.zmax) * r.c_hi) * st.inv_s;
-    drow[v] = (OT)((q - p) * A);
+    drow[v] = (OT)(fmaf(q, st.mass, -p) * A);
   }
 }
 
@@ -408,14 +411,17 @@ __global__ void __launch_bounds__(kMaxThreads) distill_kernel(
       for (int j = lane; j < r.top; j += kWave) s.p[j] = 0.f;
       if (S != S) kl = S;
     }
-    st.unlist = 1.f;
+    double mass = rest ? psum : 1.0, ratio = 0.0;
     if (rest && R > 0.0) {
       const double pr = fmax(0.0, 1.0 - psum), qr = R / S;
       if (pr > 0.0) {
         kl += pr * log(pr / qr);
-        st.unlist = (float)(1.0 - pr / qr);
+        mass += pr;
+        ratio = pr / qr;
       }
     }
+    st.mass = (float)mass;
+    st.unlist = (float)(mass - ratio);
     if (lane == 0) {
       loss[t] = (float)((double)w * (double)r.tau * (double)r.tau * kl);
       sh = st;

@@ -683,9 +683,12 @@ int mbok_distill_desc_init(mbok_distill_desc* d, int32_t vocab, int32_t top,
  *   t_lse given: p_j = exp(l_j / tau - t_lse) (the teacher's own
  *                probabilities); what is not listed is one more class of
  *                mass p_r = max(0, 1 - sum_j p_j), q_r = sum of the other q_v:
- *                loss += w tau^2 p_r log(p_r / q_r), and for unlisted v
- *                dz_v = w tau q_v (1 - p_r / q_r)
+ *                loss += w tau^2 p_r log(p_r / q_r)
  *                (no such class when every token is listed or q_r is 0)
+ *                dz_v = w tau (s q_v - sum_{j: v_j = v} p_j), for unlisted v
+ *                w tau q_v (s - p_r / q_r), with s = sum_j p_j plus the p_r
+ *                that was used: 1, more where an index is listed twice or
+ *                t_lse is too small for p_r to make up, less without the class
  * An entry whose index is negative or >= V is not there (rows with fewer
  * entries); an index listed twice counts twice.  A row whose listed entries
  * carry no teacher weight (none there, or all l = -inf) has, without t_lse,

@@ -1,0 +1,148 @@
+"""The distillation loss and gradient where the teacher's masses do not add to
+1, are not numbers, or lie where the student has next to nothing, against the
+float64 definition, in one pass and as two calls.
+
+Tolerances, with eps = 2^-24 (the fp32 half step):
+  loss  log S and the logarithms of the listed entries are off by at most 2^-17
+        (a row's exponentials are summed in fp32, at most 128 terms each),
+        every p by 2^-22 relative, and the teacher's rest, 1 less a sum, by
+        2^-22 absolute; so by w tau^2 mass (2^-16 + 2^-20 spread), spread being
+        the largest |log p - log q| and mass the sum of the teacher's masses.
+  dZ    2^-16 of the magnitudes a value is the difference of (the reference's
+        `size`), then one rounding: eps_t / 2 relative, or half the smallest
+        step (fp16 2^-25; below the smallest normal value fp32 and bf16
+        results may be flushed).
+"""
+import math
+
+import pytest
+import torch
+
+import boolean_weight_amd as bw
+import distill_ref as ref
+from gpu_util import DEV, say
+
+pytestmark = pytest.mark.gpu
+
+F64 = torch.float64
+TYPES = {"f32": torch.float32, "f16": torch.float16, "bf16": torch.bfloat16}
+MODES = ("step", "pair")
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _gpu():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    bw.load_library()
+    yield
+    torch.cuda.synchronize()
+
+
+def dev(x):
+    return None if x is None else x.to(DEV)
+
+
+def run(Z, l, idx, tau, lse=None, w=None, mode="step", dloss=None, grad=None):
+    T, V = Z.shape
+    d = bw.mbok_distill_desc_init(V, l.shape[1], tau)
+    args = [dev(Z), dev(l), dev(idx.to(torch.int32))]
+    kw = dict(t_lse=dev(lse), weight=dev(w))
+    loss = torch.full((T,), -5.0, device=DEV)
+    dZ = torch.full((T, V), -7.0, dtype=grad or Z.dtype, device=DEV)
+    if mode == "step":
+        bw.mbok_distill(d, *args, loss, dZ=dZ, **kw)
+    else:
+        stats = torch.full((T, bw.MBOK_DISTILL_STATS), math.nan, device=DEV)
+        bw.mbok_distill(d, *args, loss, stats=stats, **kw)
+        dl = torch.ones(T, device=DEV) if dloss is None else dev(dloss)
+        bw.mbok_distill_backward(d, *args, stats, dl, dZ, **kw)
+    return loss.cpu(), dZ.cpu()
+
+
+def check(Z, l, idx, tau, lse=None, w=None, grad=None, modes=MODES):
+    T = Z.shape[0]
+    for mode in modes:
+        dloss = torch.linspace(0.5, 2.0, T) if mode == "pair" else None
+        loss, dZ = run(Z, l, idx, tau, lse, w, mode, dloss, grad)
+        want, grads, size = ref.distill(Z, l, idx, tau, lse, w, dloss)
+        assert torch.equal(torch.isnan(loss), torch.isnan(want)), (mode, loss, want)
+        wt = torch.ones(T, dtype=F64) if w is None else w.to(F64).abs()
+        for t in range(T):
+            if math.isnan(float(want[t])) or float(wt[t]) == 0.0:
+                continue
+            row = ref.masses(Z.shape[1], l[t], idx[t], tau, None if lse is None else lse[t])
+            if row is None:
+                assert float(loss[t]) == 0.0
+                continue
+            x = Z[t].to(F64) / tau
+            spread = float((x.max() - x[x > -math.inf].min())) + math.log(Z.shape[1]) + \
+                float(row[2][row[1] > 0].abs().max() if bool((row[1] > 0).any()) else 0.0)
+            mass = max(1.0, float(row[1].sum()))
+            tol = float(wt[t]) * tau * tau * mass * (2.0 ** -16 + 2.0 ** -20 * spread)
+            assert abs(float(loss[t]) - float(want[t])) <= tol, (mode, t, loss[t], want[t], tol)
+        assert torch.equal(torch.isnan(dZ), torch.isnan(grads)), mode
+        info = torch.finfo(dZ.dtype)
+        least = 2.0 ** -25 if dZ.dtype == torch.float16 else info.smallest_normal
+        tol = 2.0 ** -16 * size + info.eps / 2 * grads.abs() + least
+        off = (dZ.to(F64) - grads).abs()
+        ok = (off <= tol) | torch.isnan(grads)
+        assert ok.all(), (mode, (off - tol).nan_to_num(-1.0).max(), off.nan_to_num(0).max())
+
+
+def inputs(T, V, top, seed, z="f32", scale=2.5):
+    gen = torch.Generator().manual_seed(seed)
+    teacher = torch.randn(T, V, generator=gen) * scale
+    Z = (teacher + torch.randn(T, V, generator=gen)).to(TYPES[z])
+    l, idx = teacher.topk(top, -1)
+    return Z, l.contiguous(), idx, teacher
+
+
+@pytest.mark.parametrize("z,grad", [("f32", "f32"), ("bf16", "bf16"), ("f16", "bf16")])
+@pytest.mark.parametrize("V,top", [(17, 8), (1000, 20), (33001, 64)])
+def test_masses_that_do_not_add_to_one(z, grad, V, top):
+    """A likely index listed twice and three times (more than 1), a log-sum that
+    is too small (more than 1) and too large (a larger rest)."""
+    say(f"distill masses V={V} top={top} {z}->{grad}")
+    Z, l, idx, teacher = inputs(5, V, top, 3 * V, z)
+    for t, j in ((0, 1), (1, 1), (1, 2), (4, top - 1)):
+        idx[t, j], l[t, j] = idx[t, 0], l[t, 0]
+    for tau in (1.0, 2.0):
+        lse = torch.logsumexp(teacher / tau, -1) + torch.tensor([0.0, 0.0, -0.5, 0.5, -0.1])
+        check(Z, l, idx, tau, lse, grad=TYPES[grad])
+        check(Z, l, idx, tau, grad=TYPES[grad])
+
+
+def test_everything_unlisted_masked():
+    """Nothing is left for the teacher's rest: q_r is 0 and its class drops out,
+    so the row's masses add to less than 1 (and to nothing in the last row)."""
+    for z in ("f32", "bf16"):
+        say(f"distill unlisted masked {z}")
+        Z, l, idx, teacher = inputs(4, 300, 6, 21, z)
+        for t in range(4):
+            free = torch.ones(300, dtype=torch.bool)
+            free[idx[t]] = False
+            Z[t, free] = -math.inf
+        lse = torch.logsumexp(teacher, -1)
+        l[3, :] = -math.inf
+        w = torch.tensor([1.0, 0.25, 3.0, 1.0])
+        check(Z, l, idx, 1.0, lse, w)
+
+
+def test_differences_with_a_repeated_token():
+    """dZ against central differences of the call's own loss, masses above 1.
+    With h = 2^-5 the third derivative (below 2) leaves h^2 / 6 2 < 4e-4, and
+    the fp32 loss (below 8, off by 2^-18) adds 2^-18 / h = 2^-13."""
+    say("distill differences")
+    V, h = 40, 2.0 ** -5
+    Z, l, idx, teacher = inputs(1, V, 5, 9, scale=1.0)
+    idx[0, 1], l[0, 1] = idx[0, 0], l[0, 0]
+    lse = torch.logsumexp(teacher, -1) - 1.0
+    many = Z.repeat(2 * V, 1)
+    for v in range(V):
+        many[2 * v, v] += h
+        many[2 * v + 1, v] -= h
+    loss, _ = run(many, l.repeat(2 * V, 1), idx.repeat(2 * V, 1), 1.0, lse.repeat(2 * V))
+    diff = (loss.to(F64).view(V, 2) @ torch.tensor([1.0, -1.0], dtype=F64)) / (2 * h)
+    for mode in MODES:
+        dZ = run(Z, l, idx, 1.0, lse, mode=mode)[1][0].to(F64)
+        assert (diff - dZ).abs().max() < 6e-4
