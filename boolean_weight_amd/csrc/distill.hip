@@ -116,7 +116,7 @@ struct RowStats {
   float inv_s;   // 1 / sum exp((z - zmax) / tau)
   float unlist;  // factor of q_v for unlisted v: mass - p_r / q_r
   float tmax;    // largest listed teacher logit (no t_lse)
-  float inv_n;   // 1 / sum exp((l - tmax) / tau); 0: no teacher weight
+  float inv_n;   // 1 / sum exp((l - tmax) / tau); 0: no teacher weight, NaN: no number
   float mass;    // s, the sum of the teacher's masses: the factor of q_v for listed v
   float pad[2];
 };
@@ -376,18 +376,22 @@ __global__ void __launch_bounds__(kMaxThreads) distill_kernel(
       for (int j = lane; j < r.top; j += kWave) tm = fmaxf(tm, s.p[j]);
       tm = wave_max(tm);
       st.tmax = tm;
+      // a NaN was dropped from the maximum: it makes the sum NaN, beside
+      // entries of -inf too; so does a maximum of +inf
       Nsum = 0.0;
-      if (tm > -INFINITY)
-        for (int j = lane; j < r.top; j += kWave)
-          Nsum += (double)exp_listed(s.p[j] - tm, r);
+      for (int j = lane; j < r.top; j += kWave) {
+        const float l = s.p[j];
+        if (tm > -INFINITY) Nsum += (double)exp_listed(l - tm, r);
+        else if (l != l) Nsum = l;
+      }
       Nsum = wave_sum(Nsum);
       log_n = log(Nsum);
       shift = (double)tm;
-      st.inv_n = Nsum > 0.0 ? (float)(1.0 / Nsum) : 0.f;
+      st.inv_n = Nsum != 0.0 ? (float)(1.0 / Nsum) : 0.f;
     }
     const double log_s = log(S);
     double kl = 0.0, psum = 0.0;
-    if (st.inv_n > 0.f || rest) {
+    if (st.inv_n != 0.f) {
       for (int j = lane; j < r.top; j += kWave) {
         const float l = s.p[j];
         double p;
@@ -411,7 +415,7 @@ __global__ void __launch_bounds__(kMaxThreads) distill_kernel(
       for (int j = lane; j < r.top; j += kWave) s.p[j] = 0.f;
       if (S != S) kl = S;
     }
-    double mass = rest ? psum : 1.0, ratio = 0.0;
+    double mass = rest ? psum : Nsum == Nsum ? 1.0 : Nsum, ratio = 0.0;
     if (rest && R > 0.0) {
       const double pr = fmax(0.0, 1.0 - psum), qr = R / S;
       if (pr > 0.0) {
@@ -433,7 +437,7 @@ __global__ void __launch_bounds__(kMaxThreads) distill_kernel(
 
   const RowStats st = sh;
   const float A = w * r.tau;
-  const float Aq = st.inv_n > 0.f ? A * st.inv_s : 0.f;
+  const float Aq = st.inv_n != 0.f ? A * st.inv_s : 0.f;
   const float Au = Aq * st.unlist;
   const GradScale<OT> scale(Au, mx, r);
   each([&](int v, const Vec<ZT>& x) {
@@ -442,7 +446,7 @@ __global__ void __launch_bounds__(kMaxThreads) distill_kernel(
     store_vec<OT, N>(drow, v, r.V, d);
   });
   __syncthreads();
-  if (st.inv_n > 0.f)
+  if (st.inv_n != 0.f)
     write_entries<ZT, OT>(s, r, zl, drow, st, A, twice_any != 0);
 }
 
@@ -482,7 +486,7 @@ __global__ void __launch_bounds__(kMaxThreads) distill_backward_kernel(
       const float l = teacher_logit(t_logits, t_dtype, t * ldt + j);
       p = t_lse ? exp_fine((double)l * (1.0 / (double)r.tau) - (double)t_lse[t])
                 : exp_listed(l - st.tmax, r) * st.inv_n;
-      if (!(st.inv_n > 0.f)) p = 0.f;
+      if (st.inv_n == 0.f) p = 0.f;
       zl[j] = to_f32(row[v]);
       twice |= mark_entry(s.bits, v);
     }
@@ -491,7 +495,7 @@ __global__ void __launch_bounds__(kMaxThreads) distill_backward_kernel(
   if (twice) twice_any = 1;
   __syncthreads();
   const float A = w * r.tau * dl;
-  const float Aq = st.inv_n > 0.f ? A * st.inv_s : 0.f;
+  const float Aq = st.inv_n != 0.f ? A * st.inv_s : 0.f;
   const float Au = Aq * st.unlist;
   const GradScale<OT> scale(Au, st.zmax, r);
   for (int v = tid; v < nvec; v += nt) {
@@ -501,7 +505,7 @@ __global__ void __launch_bounds__(kMaxThreads) distill_backward_kernel(
     store_vec<OT, N>(drow, v, r.V, d);
   }
   __syncthreads();
-  if (st.inv_n > 0.f)
+  if (st.inv_n != 0.f)
     write_entries<ZT, OT>(s, r, zl, drow, st, A, twice_any != 0);
 }
 

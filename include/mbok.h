@@ -694,7 +694,8 @@ int mbok_distill_desc_init(mbok_distill_desc* d, int32_t vocab, int32_t top,
  * carry no teacher weight (none there, or all l = -inf) has, without t_lse,
  * loss 0 and gradient 0.  A row of weight 0 is not read: loss 0, gradient 0.
  * A p_j of 0 contributes nothing; q_{v_j} = 0 with p_j > 0 gives +inf; NaN
- * logits, +inf logits and rows of only -inf give NaN.
+ * or +inf among a row's logits or its listed teacher logits, and rows of only
+ * -inf, give NaN (the loss and the row's gradient).
  * Row maxima, sums and logarithms are at least fp32 (the sums of a row and
  * the loss in float64 at the end).
  *  Z        device [T, ldz] of z_dtype (MBOK_F32, MBOK_F16, MBOK_BF16).

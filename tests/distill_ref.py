@@ -15,7 +15,7 @@ def masses(V, l, idx, tau, lse):
     at = [j for j, v in enumerate(idx.tolist()) if 0 <= v < V]
     v, x = idx[at].long(), l[at].to(F64) / tau
     if lse is not None:
-        logp = x - float(lse)
+        logp = torch.where(x < math.inf, x, NAN) - float(lse)
         return v, logp.exp(), logp
     if not len(at) or bool((x == -math.inf).all()):
         return None
@@ -68,5 +68,5 @@ def distill(Z, l, idx, tau, lse=None, weight=None, dloss=None):
     for t in (w == 0).nonzero()[:, 0]:
         loss[t] = 0.0
     for t in (g == 0).nonzero()[:, 0]:
-        dZ[t] = 0.0
+        dZ[t] = size[t] = 0.0
     return loss, dZ, size.abs()

@@ -59,3 +59,14 @@ def test_gradient_with_everything_unlisted_masked():
     assert torch.allclose(diff[0, idx[0]], dZ[0, idx[0]], rtol=0, atol=1e-6)
     assert not dZ[0, free].any()
     assert abs(float(dZ.sum())) < 1e-12  # q and the masses cancel over the row
+
+
+def test_teacher_logits_that_are_no_numbers():
+    Z = torch.zeros(1, 4, dtype=F64)
+    idx = torch.tensor([[0, 2]])
+    for lse in (None, torch.tensor([1.0])):
+        for bad in ((math.nan, 0.0), (math.inf, 0.0), (math.inf, math.inf), (-math.inf, math.nan)):
+            loss, dZ, _ = ref.distill(Z, torch.tensor([bad]), idx, 1.0, lse)
+            assert torch.isnan(loss).all() and torch.isnan(dZ).all()
+    loss, dZ, _ = ref.distill(Z, torch.tensor([[-math.inf, -math.inf]]), idx, 1.0)
+    assert float(loss) == 0.0 and not dZ.any()

@@ -146,3 +146,34 @@ def test_differences_with_a_repeated_token():
     for mode in MODES:
         dZ = run(Z, l, idx, 1.0, lse, mode=mode)[1][0].to(F64)
         assert (diff - dZ).abs().max() < 6e-4
+
+
+@pytest.mark.parametrize("rest", [False, True])
+def test_teacher_logits_that_are_no_numbers(rest):
+    """NaN or +inf among the listed teacher logits (an overflowed fp16 row): loss
+    and gradient of the row are NaN, beside entries of -inf too, and of that row
+    only; not where the entry is not there or the row has no weight."""
+    for z, td in (("f32", "f32"), ("bf16", "f16"), ("f16", "bf16")):
+        say(f"distill teacher non-finite {z} teacher {td} rest={rest}")
+        Z, l, idx, teacher = inputs(9, 300, 6, 22, z)
+        l = l.to(TYPES[td])
+        l[0, 3] = math.nan
+        l[1, 0] = math.inf
+        l[2, 2] = l[2, 4] = math.inf
+        l[3, :] = -math.inf
+        l[3, 5] = math.nan
+        l[4, :] = math.nan
+        l[5, 1] = math.nan
+        idx[5, 1] = -1
+        l[6, :] = math.nan
+        idx[6, :] = 300
+        l[7, 0] = math.nan
+        lse = torch.logsumexp(teacher, -1) if rest else None
+        w = torch.tensor([1.0] * 7 + [0.0, 2.0])
+        check(Z, l, idx, 1.0, lse, w)
+        loss, dZ = run(Z, l, idx, 1.0, lse, w)
+        assert torch.isnan(loss).tolist() == [True] * 5 + [False] * 4
+        assert torch.isnan(dZ[:5]).all() and not torch.isnan(dZ[5:]).any()
+        if not rest:
+            assert float(loss[6]) == 0.0 and not dZ[6].any()
+        assert float(loss[7]) == 0.0 and not dZ[7].any()
