@@ -9,7 +9,12 @@
 // where p is the softmax of the listed l / tau (then p_r = 0 and s = 1), or
 // with t_lse exp(l / tau - t_lse) and p_r = 1 - sum p the mass of what is not
 // listed; s = sum p + p_r is 1 as well unless p_r is cut off at 0 (an index
-// listed twice, a t_lse that is too small) or its class drops out.
+// listed twice, a t_lse that is too small) or its class drops out.  What is
+// not listed may lie far below the largest logit, so its sum R is taken
+// relative to its own largest logit zu: log q_r keeps its digits at any
+// distance, and the factor of exp((z_v - zu) / tau),
+//     s exp((zu - zmax) / tau) / S - p_r / R,
+// stays below s + p_r where p_r / q_r overflows.
 //
 // Bound: the row of logits, read once and (gradient) written once.  One
 // workgroup takes one row and keeps it in registers as loaded (NV 16-byte
@@ -113,11 +118,11 @@ __device__ __forceinline__ float teacher_logit(const void* l, int dtype, int64_t
 // Statistics of a row, as stats holds them
 struct RowStats {
   float zmax;    // largest logit
-  float inv_s;   // 1 / sum exp((z - zmax) / tau)
-  float unlist;  // factor of q_v for unlisted v: mass - p_r / q_r
+  float listed;  // s / S: s q_v = exp((z_v - zmax) / tau) listed for listed v
   float tmax;    // largest listed teacher logit (no t_lse)
   float inv_n;   // 1 / sum exp((l - tmax) / tau); 0: no teacher weight, NaN: no number
-  float mass;    // s, the sum of the teacher's masses: the factor of q_v for listed v
+  // dz_v = w tau exp((z_v - zu) / tau) unlisted for the others
+  float zu, unlisted;
   float pad[2];
 };
 static_assert(sizeof(RowStats) == MBOK_DISTILL_STATS * sizeof(float), "stats row");
@@ -174,7 +179,7 @@ __device__ __forceinline__ bool mark_entry(uint32_t* bits, int v) {
 }
 
 // The gradient of the listed entries, after the main pass of the same
-// workgroup and a barrier: base scale A = w tau; q = exp((z - zmax) c) inv_s.
+// workgroup and a barrier: base scale A = w tau.
 template <typename ZT, typename OT>
 __device__ __forceinline__ void write_entries(const RowLds& s, const DistillRow& r,
                                               const float* zl, OT* drow, const RowStats& st,
@@ -189,23 +194,23 @@ __device__ __forceinline__ void write_entries(const RowLds& s, const DistillRow&
     } else {
       p = s.p[j];
     }
-    const float q = __builtin_amdgcn_exp2f((zl[j] - st.zmax) * r.c_hi) * st.inv_s;
-    drow[v] = (OT)(fmaf(q, st.mass, -p) * A);
+    const float e = __builtin_amdgcn_exp2f((zl[j] - st.zmax) * r.c_hi);
+    drow[v] = (OT)(fmaf(e, st.listed, -p) * A);
   }
 }
 
-// The main pass's dz = exp((z - zmax) / tau) A of a vector.  For 16-bit gradients
-// the factor is folded into the exponent, exp2(z c + k), where the largest
-// logit is small enough for k's rounding (2^-24 of |k|) to stay far below
-// theirs; it takes two instructions fewer.
+// The main pass's dz = exp((z - zu) / tau) A of a vector.  For 16-bit gradients
+// the factor is folded into the exponent, exp2(z c + k), where zu is small
+// enough for k's rounding (2^-24 of |k|) to stay far below theirs; it takes
+// two instructions fewer.
 template <typename OT>
 struct GradScale {
-  float A, zmax, c, k;
+  float A, zu, c, k;
   uint32_t sign;
   bool fold;  // the same for the whole row
-  __device__ __forceinline__ GradScale(float A_, float zmax_, const DistillRow& r)
-      : A(A_), zmax(zmax_), c(r.c_hi), k(0.f), sign(__float_as_uint(A_) & 0x80000000u) {
-    const float shift = zmax * c;
+  __device__ __forceinline__ GradScale(float A_, float zu_, const DistillRow& r)
+      : A(A_), zu(zu_), c(r.c_hi), k(0.f), sign(__float_as_uint(A_) & 0x80000000u) {
+    const float shift = zu * c;
     fold = sizeof(OT) == 2 && fabsf(shift) < 256.f;
     // A = 0 goes through the exponent as well (log2 0 = -inf gives 0), NaN stays
     if (fold) k = __builtin_amdgcn_logf(fabsf(A)) - shift;
@@ -219,7 +224,7 @@ struct GradScale {
             __float_as_uint(__builtin_amdgcn_exp2f(fmaf(to_f32(x.v[e]), c, k))) ^ sign);
     } else {
 #pragma unroll
-      for (int e = 0; e < N; ++e) d[e] = __builtin_amdgcn_exp2f((to_f32(x.v[e]) - zmax) * c) * A;
+      for (int e = 0; e < N; ++e) d[e] = __builtin_amdgcn_exp2f((to_f32(x.v[e]) - zu) * c) * A;
     }
   }
 };
@@ -232,7 +237,7 @@ __global__ void __launch_bounds__(kMaxThreads) distill_kernel(
     RowStats* __restrict__ stats, OT* dZ, int64_t lddz) {
   constexpr int N = Vec<ZT>::N;
   extern __shared__ __attribute__((aligned(16))) uint32_t smem[];
-  __shared__ float red_f[kMaxThreads / kWave];
+  __shared__ float red_f[2 * kMaxThreads / kWave];
   __shared__ double red_d[2 * kMaxThreads / kWave];
   __shared__ RowStats sh;
   __shared__ int twice_any;
@@ -290,55 +295,84 @@ __global__ void __launch_bounds__(kMaxThreads) distill_kernel(
     zl[j] = v < 0 ? 0.f : to_f32(row[v]);
   }
 
-  // largest logit (a NaN is dropped here: it makes the sum below NaN)
-  float mx = -INFINITY;
-  each([&](int, const Vec<ZT>& x) {
-#pragma unroll
-    for (int e = 0; e < N; ++e) mx = fmaxf(mx, to_f32(x.v[e]));
-  });
-  mx = wave_max(mx);
-  if (lane == 0) red_f[wave] = mx;
-  __syncthreads();  // also: lists and cleared bits are in LDS
-  mx = red_f[0];
-  for (int i = 1; i < nw; ++i) mx = fmaxf(mx, red_f[i]);
-
   bool twice = false;
-  for (int j = tid; j < r.top; j += nt)
-    if (s.idx[j] >= 0) twice |= mark_entry(s.bits, s.idx[j]);
-  if (twice) twice_any = 1;
-  __syncthreads();
+  auto mark = [&] {
+    for (int j = tid; j < r.top; j += nt)
+      if (s.idx[j] >= 0) twice |= mark_entry(s.bits, s.idx[j]);
+    if (twice) twice_any = 1;
+  };
+  auto listed_at = [&](int v) { return s.bits[(v * N) >> 5] >> ((v * N) & 31); };
+  // largest logit mx (a NaN is dropped here: it makes the sums below NaN), and
+  // zu, from which the main passes count: the largest one, or, with t_lse, the
+  // largest of what is not listed (0 if that is -inf)
+  const bool rest = t_lse != nullptr;
+  float mx = -INFINITY, zu = -INFINITY;
+  if (rest) {
+    __syncthreads();  // lists and cleared bits are in LDS
+    mark();
+    __syncthreads();
+    each([&](int v, const Vec<ZT>& x) {
+      const uint32_t m = listed_at(v);
+#pragma unroll
+      for (int e = 0; e < N; ++e) zu = fmaxf(zu, (m >> e) & 1u ? -INFINITY : to_f32(x.v[e]));
+    });
+    for (int j = tid; j < r.top; j += nt)
+      if (s.idx[j] >= 0) mx = fmaxf(mx, zl[j]);
+    zu = wave_max(zu);
+    mx = wave_max(mx);
+    if (lane == 0) red_f[2 * wave] = zu, red_f[2 * wave + 1] = mx;
+    __syncthreads();
+    for (int i = 0; i < nw; ++i) {
+      zu = fmaxf(zu, red_f[2 * i]);
+      mx = fmaxf(mx, red_f[2 * i + 1]);
+    }
+    mx = fmaxf(mx, zu);
+    if (!(zu > -INFINITY)) zu = 0.f;
+  } else {
+    each([&](int, const Vec<ZT>& x) {
+#pragma unroll
+      for (int e = 0; e < N; ++e) mx = fmaxf(mx, to_f32(x.v[e]));
+    });
+    mx = wave_max(mx);
+    if (lane == 0) red_f[wave] = mx;
+    __syncthreads();  // also: lists and cleared bits are in LDS
+    mx = red_f[0];
+    for (int i = 1; i < nw; ++i) mx = fmaxf(mx, red_f[i]);
+    zu = mx;
+    mark();
+    __syncthreads();
+  }
 
-  // Sums of exponentials: all, and (with t_lse) the unlisted ones.  The scaled
-  // argument (z - max) c is one fma, z c - k with k = max c rounded, where k is
-  // small (2^klo then corrects the sums for that rounding, |klo| <= 2^-17: to
-  // first order), else subtracted first.  That c is log2(e) / tau rounded
-  // moves log sum by at most 2^-25 E_q[(max - z) / tau] <= 2^-25 log V, since
+  // Sums of exponentials: all, or (with t_lse) the unlisted ones and apart from
+  // them the listed ones, each index once.  The scaled argument (z - zu) c is
+  // one fma, z c - k with k = zu c rounded, where k is small (2^klo then
+  // corrects the sum for that rounding, |klo| <= 2^-17: to first order), else
+  // subtracted first.  That c is log2(e) / tau rounded (2^-24 relative at most)
+  // moves log sum by at most 2^-24 E_q[(max - z) / tau] <= 2^-24 log V, since
   // that mean is the entropy of q less log sum.  (Carrying it exactly cost
   // two instructions per logit, the subtraction one: 2048 x 32000 bf16 with
   // gradient 76.5 -> 74.1 us.)
-  float sa = 0.f, sr = 0.f;
-  const bool rest = t_lse != nullptr;
-  const float k = mx * r.c_hi;
+  float sum_z = 0.f;
+  const float k = zu * r.c_hi;
   const bool near = fabsf(k) < 256.f;
   auto sum = [&](auto near_c) {
     auto ex = [&](ZT z) {
       return __builtin_amdgcn_exp2f(decltype(near_c)::value ? fmaf(to_f32(z), r.c_hi, -k)
-                                                            : (to_f32(z) - mx) * r.c_hi);
+                                                            : (to_f32(z) - zu) * r.c_hi);
     };
     if (rest) {
       each([&](int v, const Vec<ZT>& x) {
-        const uint32_t m = s.bits[(v * N) >> 5] >> ((v * N) & 31);
+        const uint32_t m = listed_at(v);
 #pragma unroll
         for (int e = 0; e < N; ++e) {
           const float y = ex(x.v[e]);
-          sa += y;
-          sr += (m >> e) & 1u ? 0.f : y;
+          sum_z += (m >> e) & 1u ? 0.f : y;
         }
       });
     } else {
       each([&](int, const Vec<ZT>& x) {
 #pragma unroll
-        for (int e = 0; e < N; ++e) sa += ex(x.v[e]);
+        for (int e = 0; e < N; ++e) sum_z += ex(x.v[e]);
       });
     }
   };
@@ -346,26 +380,42 @@ __global__ void __launch_bounds__(kMaxThreads) distill_kernel(
   else sum(std::false_type{});
   {
     const double fix =
-        near ? 1.0 - (double)kLn2 * ((double)mx * (double)r.c_hi - (double)k) : 1.0;
-    const double da = wave_sum((double)sa) * fix, dr = rest ? wave_sum((double)sr) * fix : 0.0;
+        near ? 1.0 - (double)kLn2 * ((double)zu * (double)r.c_hi - (double)k) : 1.0;
+    const double dz = wave_sum((double)sum_z) * fix;
+    double dl = 0.0;
+    if (rest) {
+      const double inv_tau = 1.0 / (double)r.tau;
+      for (int j = tid; j < r.top; j += nt) {
+        const int v = s.idx[j];
+        bool first = v >= 0;
+        if (twice_any)
+          for (int i = 0; i < j; ++i) first &= s.idx[i] != v;
+        if (first) dl += (double)exp_fine(((double)zl[j] - (double)mx) * inv_tau);
+      }
+      dl = wave_sum(dl);
+    }
     if (lane == 0) {
-      red_d[2 * wave] = da;
-      red_d[2 * wave + 1] = dr;
+      red_d[2 * wave] = dz;
+      red_d[2 * wave + 1] = dl;
     }
   }
   __syncthreads();
 
   // the first wavefront: teacher, loss, statistics
   if (wave == 0) {
-    double S = 0.0, R = 0.0;
+    // R: the sum of the main pass, relative to zu; S: the whole row's, to zmax
+    double S = 0.0, R = 0.0, up = 1.0;
     for (int i = 0; i < nw; ++i) {
-      S += red_d[2 * i];
-      R += red_d[2 * i + 1];
+      R += red_d[2 * i];
+      S += red_d[2 * i + 1];
     }
     const double inv_tau = 1.0 / (double)r.tau;
+    if (rest) up = R != 0.0 ? exp(((double)zu - (double)mx) * inv_tau) : 0.0;
+    S += R * up;
+    if (!(mx > -INFINITY)) S = __builtin_nan("");  // only -inf
     RowStats st = {};
     st.zmax = mx;
-    st.inv_s = (float)(1.0 / S);
+    st.zu = zu;
     double log_n, shift, Nsum = 1.0;  // log p_j = (l_j - shift) / tau - log_n
     if (rest) {
       shift = 0.0;
@@ -413,19 +463,18 @@ __global__ void __launch_bounds__(kMaxThreads) distill_kernel(
       psum = wave_sum(psum);
     } else {
       for (int j = lane; j < r.top; j += kWave) s.p[j] = 0.f;
-      if (S != S) kl = S;
     }
-    double mass = rest ? psum : Nsum == Nsum ? 1.0 : Nsum, ratio = 0.0;
-    if (rest && R > 0.0) {
-      const double pr = fmax(0.0, 1.0 - psum), qr = R / S;
-      if (pr > 0.0) {
-        kl += pr * log(pr / qr);
-        mass += pr;
-        ratio = pr / qr;
-      }
+    if (S != S) kl = S;
+    double mass = rest ? psum : Nsum == Nsum ? 1.0 : Nsum, take = 0.0;
+    const double pr = rest ? fmax(0.0, 1.0 - psum) : 0.0;
+    if (pr > 0.0 && R > 0.0) {
+      kl += pr * (log(pr) - (((double)zu - (double)mx) * inv_tau + log(R) - log_s));
+      mass += pr;
+      take = pr / R;
     }
-    st.mass = (float)mass;
-    st.unlist = (float)(mass - ratio);
+    if (st.inv_n == 0.f) mass = 0.0;
+    st.listed = (float)(mass / S);
+    st.unlisted = (float)(mass * up / S - take);
     if (lane == 0) {
       loss[t] = (float)((double)w * (double)r.tau * (double)r.tau * kl);
       sh = st;
@@ -437,9 +486,7 @@ __global__ void __launch_bounds__(kMaxThreads) distill_kernel(
 
   const RowStats st = sh;
   const float A = w * r.tau;
-  const float Aq = st.inv_n != 0.f ? A * st.inv_s : 0.f;
-  const float Au = Aq * st.unlist;
-  const GradScale<OT> scale(Au, mx, r);
+  const GradScale<OT> scale(A * st.unlisted, zu, r);
   each([&](int v, const Vec<ZT>& x) {
     float d[N];
     scale(x, d);
@@ -495,9 +542,7 @@ __global__ void __launch_bounds__(kMaxThreads) distill_backward_kernel(
   if (twice) twice_any = 1;
   __syncthreads();
   const float A = w * r.tau * dl;
-  const float Aq = st.inv_n != 0.f ? A * st.inv_s : 0.f;
-  const float Au = Aq * st.unlist;
-  const GradScale<OT> scale(Au, st.zmax, r);
+  const GradScale<OT> scale(A * st.unlisted, st.zu, r);
   for (int v = tid; v < nvec; v += nt) {
     const Vec<ZT> x = load_vec(row, v, r.V);
     float d[N];

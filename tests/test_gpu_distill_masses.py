@@ -177,3 +177,42 @@ def test_teacher_logits_that_are_no_numbers(rest):
         if not rest:
             assert float(loss[6]) == 0.0 and not dZ[6].any()
         assert float(loss[7]) == 0.0 and not dZ[7].any()
+
+
+@pytest.mark.parametrize("gap", [60.0, 85.0, 87.0, 88.0, 90.0, 200.0, 1000.0])
+def test_rest_far_below_the_listed(gap):
+    """Everything unlisted lies `gap` tau below the listed tokens, where its
+    exponentials relative to the largest logit leave fp32: the teacher's rest
+    keeps its term, and its gradient stays w tau p_r at most."""
+    for z, grad, V, top in (("f32", "f32", 1000, 12), ("bf16", "bf16", 1000, 12),
+                            ("f32", "bf16", 33001, 64), ("bf16", "bf16", 140003, 7)):
+        for tau, w in ((1.0, 1.0), (0.5, 65536.0), (4.0, 65536.0)):
+            say(f"distill gap={gap} V={V} {z}->{grad} tau={tau} w={w}")
+            T = 3
+            Z, l, idx, _ = inputs(T, V, top, 17, "f32", scale=1.0)
+            idx[2, 1], l[2, 1] = idx[2, 0], l[2, 0]
+            up = torch.zeros(T, V).scatter_(1, idx, gap * tau)
+            Z = (Z + up).to(TYPES[z])
+            lse = torch.logsumexp(l / tau, -1) - math.log(0.9)
+            check(Z, l, idx, tau, lse, torch.full((T,), w), TYPES[grad])
+
+
+def test_rest_far_below_with_bad_values():
+    """NaN and +inf among the listed, among the unlisted far below, and rows of
+    only -inf with and without listed entries."""
+    say("distill gap bad values")
+    T, V = 8, 700
+    Z, l, idx, _ = inputs(T, V, 9, 18)
+    Z.scatter_add_(1, idx, torch.full((T, 9), 150.0))
+    free = [v for v in range(V) if all(v not in idx[t].tolist() for t in range(T))][5]
+    Z[0, free] = math.nan
+    Z[1, free] = math.inf
+    Z[2, int(idx[2, 4])] = math.nan
+    Z[3, int(idx[3, 4])] = math.inf
+    Z[4, :] = -math.inf
+    Z[5, :] = -math.inf
+    idx[5, :] = -1
+    Z[6, free] = -math.inf
+    idx[7, :] = -1
+    lse = torch.logsumexp(l, -1) + 0.2
+    check(Z, l, idx, 1.0, lse)
