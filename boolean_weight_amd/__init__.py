@@ -316,6 +316,19 @@ def mbok_gemv_workspace_bytes(d: mbok_desc) -> int:
 _WORKSPACES: dict = {}
 
 
+def _torch_stream(device: torch.device, stream) -> torch.cuda.Stream:
+    """The torch stream of a call's `stream` argument (a handle of 0 is the
+    default stream; an ExternalStream of it would be one of torch's own)."""
+    if stream is None:
+        return torch.cuda.current_stream(device)
+    if isinstance(stream, torch.cuda.Stream):
+        return stream
+    handle = int(stream)
+    if handle == 0:
+        return torch.cuda.default_stream(device)
+    return torch.cuda.ExternalStream(handle, device=device)
+
+
 def workspace_for(nbytes: int, device=None, stream=None) -> torch.Tensor | None:
     """A workspace of at least nbytes, kept per (device, stream) so that calls
     which may overlap never share one.
@@ -327,15 +340,10 @@ def workspace_for(nbytes: int, device=None, stream=None) -> torch.Tensor | None:
     if nbytes == 0:
         return None
     dev = torch.device(device) if device is not None else torch.device("cuda", torch.cuda.current_device())
-    key = (dev.index, _stream(stream))
+    target = _torch_stream(dev, stream)
+    key = (dev.index, target.cuda_stream)
     ws = _WORKSPACES.get(key)
     if ws is None or ws.numel() < nbytes:
-        if stream is None:
-            target = torch.cuda.current_stream(dev)
-        elif isinstance(stream, torch.cuda.Stream):
-            target = stream
-        else:
-            target = torch.cuda.ExternalStream(int(stream), device=dev)
         with torch.cuda.stream(target):
             ws = torch.empty(max(nbytes, 1 << 20), dtype=torch.uint8, device=dev)
         _WORKSPACES[key] = ws
@@ -640,20 +648,16 @@ def _slices(name: str, m: int, n: int, K: int, alpha_dtype: int, T: int, workspa
             raise ValueError("workspace must be contiguous and large enough")
         return ws.data_ptr(), ws
     device = torch.device("cuda", dev)
-    if stream is None:
-        handle, target = _raw_stream(dev), contextlib.nullcontext()
-    else:
-        handle = _stream(stream)
-        target = torch.cuda.stream(
-            stream if isinstance(stream, torch.cuda.Stream)
-            else torch.cuda.ExternalStream(handle, device=device))
-    with target:
+    handle = _raw_stream(dev) if stream is None else _stream(stream)
+    # the launch stream current, unless it is
+    here = stream is None and dev == _current_device()
+    with contextlib.nullcontext() if here else torch.cuda.stream(_torch_stream(device, stream)):
         if torch.cuda.is_current_stream_capturing():
             ws = torch.empty(need, dtype=torch.uint8, device=device)
             return ws.data_ptr(), ws
     ws = _WORKSPACES.get((dev, handle))
     if ws is None or ws.numel() < need:
-        ws = workspace_for(need, device, handle)
+        ws = workspace_for(need, device, stream)
     return ws.data_ptr(), ws
 
 
