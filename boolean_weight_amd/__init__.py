@@ -13,6 +13,7 @@ import contextlib
 import ctypes
 import functools
 import os
+import threading
 
 import torch
 
@@ -314,6 +315,7 @@ def mbok_gemv_workspace_bytes(d: mbok_desc) -> int:
 
 
 _WORKSPACES: dict = {}
+_WORKSPACE_LOCKS: dict = {}
 
 
 def _torch_stream(device: torch.device, stream) -> torch.cuda.Stream:
@@ -336,7 +338,11 @@ def workspace_for(nbytes: int, device=None, stream=None) -> torch.Tensor | None:
     The tensor is allocated with the target stream current, so torch's caching
     allocator ties its memory to that stream: when a larger request replaces
     it, the old block is reused only in that stream's order, after the work
-    already enqueued there that reads it."""
+    already enqueued there that reads it.
+
+    The calls below that keep a workspace by themselves enqueue all their
+    kernels before another thread's call on the same stream may use it; two
+    threads that pass one tensor to calls on one stream have to see to that."""
     if nbytes == 0:
         return None
     dev = torch.device(device) if device is not None else torch.device("cuda", torch.cuda.current_device())
@@ -348,6 +354,54 @@ def workspace_for(nbytes: int, device=None, stream=None) -> torch.Tensor | None:
             ws = torch.empty(max(nbytes, 1 << 20), dtype=torch.uint8, device=dev)
         _WORKSPACES[key] = ws
     return ws
+
+
+class _Kept:
+    """The kept workspace of a device and stream (its tensor, None for 0 bytes),
+    for the `with` block's thread alone: a call's kernels, of which the first
+    writes the workspace and the last reads it, are enqueued without another
+    thread's between them (the library's calls run without the interpreter's
+    lock)."""
+    __slots__ = ("nbytes", "device", "stream", "lock")
+
+    def __init__(self, nbytes: int, device: torch.device, stream):
+        self.nbytes, self.device, self.stream = nbytes, device, stream
+
+    def __enter__(self) -> torch.Tensor | None:
+        index, stream = self.device.index, self.stream
+        handle = _raw_stream(index) if stream is None else _stream(stream)
+        key = (index, handle)
+        lock = _WORKSPACE_LOCKS.get(key)
+        if lock is None:
+            lock = _WORKSPACE_LOCKS.setdefault(key, threading.RLock())
+        self.lock = lock
+        lock.acquire()
+        ws = _WORKSPACES.get(key)
+        if ws is not None and ws.numel() >= self.nbytes:
+            return ws
+        try:
+            return workspace_for(self.nbytes, self.device, stream)
+        except BaseException:
+            lock.release()
+            raise
+
+    def __exit__(self, *_):
+        self.lock.release()
+
+
+_NO_WORKSPACE = contextlib.nullcontext()
+
+
+def _given_or_kept(need: int, workspace, device: torch.device, stream):
+    """Context of mbok_gemv's and mbok_gemvt's workspace tensor, or None."""
+    if workspace is None or workspace is False or need == 0:
+        return _NO_WORKSPACE
+    if workspace is True:
+        return _Kept(need, device, stream)
+    _dev(workspace, "workspace")
+    if _nbytes_from(workspace) < need:
+        raise ValueError("workspace too small")
+    return contextlib.nullcontext(workspace)
 
 
 def mbok_gemv(d: mbok_desc, packed: torch.Tensor, x: torch.Tensor, y: torch.Tensor,
@@ -365,18 +419,10 @@ def mbok_gemv(d: mbok_desc, packed: torch.Tensor, x: torch.Tensor, y: torch.Tens
     if y.dtype != torch.float32 or y.numel() < d.m or not y.is_contiguous():
         raise ValueError("y must be contiguous float32 with m elements")
     need = mbok_gemv_workspace_bytes(d)
-    if workspace is True:
-        workspace = workspace_for(need, y.device, stream)
-    elif workspace is False:
-        workspace = None
-    wptr = None
-    if workspace is not None and need > 0:
-        _dev(workspace, "workspace")
-        if _nbytes_from(workspace) < need:
-            raise ValueError("workspace too small")
-        wptr = workspace.data_ptr()
-    _check(load_library().mbok_gemv(ctypes.byref(d), packed.data_ptr(), x.data_ptr(), xd,
-                                    y.data_ptr(), wptr, _stream(stream)), "mbok_gemv")
+    with _given_or_kept(need, workspace, y.device, stream) as ws:
+        _check(load_library().mbok_gemv(ctypes.byref(d), packed.data_ptr(), x.data_ptr(), xd,
+                                        y.data_ptr(), None if ws is None else ws.data_ptr(),
+                                        _stream(stream)), "mbok_gemv")
 
 
 def mbok_gemvt_workspace_bytes(d: mbok_desc) -> int:
@@ -398,18 +444,10 @@ def mbok_gemvt(d: mbok_desc, packed: torch.Tensor, g: torch.Tensor, dx: torch.Te
     if dx.dtype != torch.float32 or dx.numel() < d.n or not dx.is_contiguous():
         raise ValueError("dx must be contiguous float32 with n elements")
     need = mbok_gemvt_workspace_bytes(d)
-    if workspace is True:
-        workspace = workspace_for(need, dx.device, stream)
-    elif workspace is False:
-        workspace = None
-    wptr = None
-    if workspace is not None and need > 0:
-        _dev(workspace, "workspace")
-        if _nbytes_from(workspace) < need:
-            raise ValueError("workspace too small")
-        wptr = workspace.data_ptr()
-    _check(load_library().mbok_gemvt(ctypes.byref(d), packed.data_ptr(), g.data_ptr(), gd,
-                                     dx.data_ptr(), wptr, _stream(stream)), "mbok_gemvt")
+    with _given_or_kept(need, workspace, dx.device, stream) as ws:
+        _check(load_library().mbok_gemvt(ctypes.byref(d), packed.data_ptr(), g.data_ptr(), gd,
+                                         dx.data_ptr(), None if ws is None else ws.data_ptr(),
+                                         _stream(stream)), "mbok_gemvt")
 
 
 def mbok_gemvt_scratch_bytes() -> int:
@@ -630,35 +668,30 @@ def _packed(packed: torch.Tensor, dev: int, m: int, n: int, K: int, alpha_dtype:
 
 def _slices(name: str, m: int, n: int, K: int, alpha_dtype: int, T: int, workspace, dev: int,
             stream):
-    """(pointer, tensor) of the workspace of a call that may split its sum.
+    """Context of the workspace tensor of a call that may split its sum, or None.
 
-    True keeps one per (device, stream) as workspace_for does, except under
-    graph capture: a captured call gets memory of its own from the graph's
-    pool, so that no later call's growth frees it and no two graphs share it."""
+    True keeps one per (device, stream), see _Kept, except under graph capture:
+    a captured call gets memory of its own from the graph's pool, so that no
+    later call's growth frees it and no two graphs share it."""
     if workspace is None or workspace is False:
-        return None, None
+        return _NO_WORKSPACE
     need = _slices_bytes(name, m, n, K, alpha_dtype, T)
     if need == 0:
-        return None, None
+        return _NO_WORKSPACE
     if workspace is not True:
         ws = workspace
         if not isinstance(ws, torch.Tensor) or ws.get_device() != dev:
             _elsewhere(ws, "workspace")
         if not ws.is_contiguous() or ws.numel() * ws.itemsize < need:
             raise ValueError("workspace must be contiguous and large enough")
-        return ws.data_ptr(), ws
+        return contextlib.nullcontext(ws)
     device = torch.device("cuda", dev)
-    handle = _raw_stream(dev) if stream is None else _stream(stream)
     # the launch stream current, unless it is
     here = stream is None and dev == _current_device()
-    with contextlib.nullcontext() if here else torch.cuda.stream(_torch_stream(device, stream)):
+    with _NO_WORKSPACE if here else torch.cuda.stream(_torch_stream(device, stream)):
         if torch.cuda.is_current_stream_capturing():
-            ws = torch.empty(need, dtype=torch.uint8, device=device)
-            return ws.data_ptr(), ws
-    ws = _WORKSPACES.get((dev, handle))
-    if ws is None or ws.numel() < need:
-        ws = workspace_for(need, device, stream)
-    return ws.data_ptr(), ws
+            return contextlib.nullcontext(torch.empty(need, dtype=torch.uint8, device=device))
+    return _Kept(need, device, stream)
 
 
 def mbok_gemmt_workspace_bytes(d: mbok_desc, T: int) -> int:
@@ -683,9 +716,9 @@ def mbok_gemmt(d: mbok_desc, packed: torch.Tensor, dY: torch.Tensor, dX: torch.T
     lddy = _matrix(dY, "dY", dev, T, m, torch.bfloat16)
     lddx = _matrix(dX, "dX", dev, T, n, torch.bfloat16)
     pp = _packed(packed, dev, m, n, K, at)
-    ws, _keep = _slices("mbok_gemmt_workspace_bytes", m, n, K, at, T, workspace, dev, stream)
-    _launch(load_library().mbok_gemmt, "mbok_gemmt", dev, stream, ctypes.byref(d), pp,
-            dY.data_ptr(), T, lddy, dX.data_ptr(), lddx, ws)
+    with _slices("mbok_gemmt_workspace_bytes", m, n, K, at, T, workspace, dev, stream) as ws:
+        _launch(load_library().mbok_gemmt, "mbok_gemmt", dev, stream, ctypes.byref(d), pp,
+                dY.data_ptr(), T, lddy, dX.data_ptr(), lddx, None if ws is None else ws.data_ptr())
 
 
 def mbok_scale_grad(d: mbok_desc, packed: torch.Tensor, dY: torch.Tensor, X: torch.Tensor,
@@ -702,9 +735,10 @@ def mbok_scale_grad(d: mbok_desc, packed: torch.Tensor, dY: torch.Tensor, X: tor
     ldx = _matrix(X, "X", dev, T, n, torch.bfloat16)
     out = _vector(dalpha, "dalpha", dev, K * m * (n // MBOK_GROUP), torch.float32)
     pp = _packed(packed, dev, m, n, K, at)
-    ws, _keep = _slices("mbok_scale_grad_workspace_bytes", m, n, K, at, T, workspace, dev, stream)
-    _launch(load_library().mbok_scale_grad, "mbok_scale_grad", dev, stream, ctypes.byref(d), pp,
-            dY.data_ptr(), T, lddy, X.data_ptr(), ldx, out, int(bool(accumulate)), ws)
+    with _slices("mbok_scale_grad_workspace_bytes", m, n, K, at, T, workspace, dev, stream) as ws:
+        _launch(load_library().mbok_scale_grad, "mbok_scale_grad", dev, stream, ctypes.byref(d),
+                pp, dY.data_ptr(), T, lddy, X.data_ptr(), ldx, out, int(bool(accumulate)),
+                None if ws is None else ws.data_ptr())
 
 
 def mbok_gated_stack(d: mbok_desc) -> mbok_desc:
@@ -767,14 +801,16 @@ def mbok_gated_backward(d: mbok_desc, packed: torch.Tensor, pre: torch.Tensor, d
     lddh = _matrix(dH, "dH", dev, T, m, torch.bfloat16)
     ldpre = _matrix(pre, "pre", dev, T, m2, torch.bfloat16)
     lddpre = _matrix(dpre, "dpre", dev, T, m2, torch.bfloat16)
-    dx_ptr, lddx, ws, _keep = None, 0, None, None
+    pp = _packed(packed, dev, m2, n, K, at)
+    dx_ptr, lddx, held = None, 0, _NO_WORKSPACE
     if dX is not None:
         lddx = _matrix(dX, "dX", dev, T, n, torch.bfloat16)
         dx_ptr = dX.data_ptr()
-        ws, _keep = _slices("mbok_gemmt_workspace_bytes", m2, n, K, at, T, workspace, dev, stream)
-    _launch(load_library().mbok_gated_backward, "mbok_gated_backward", dev, stream,
-            ctypes.byref(d), _packed(packed, dev, m2, n, K, at), pre.data_ptr(), ldpre,
-            dH.data_ptr(), lddh, T, act, dpre.data_ptr(), lddpre, dx_ptr, lddx, ws)
+        held = _slices("mbok_gemmt_workspace_bytes", m2, n, K, at, T, workspace, dev, stream)
+    with held as ws:
+        _launch(load_library().mbok_gated_backward, "mbok_gated_backward", dev, stream,
+                ctypes.byref(d), pp, pre.data_ptr(), ldpre, dH.data_ptr(), lddh, T, act,
+                dpre.data_ptr(), lddpre, dx_ptr, lddx, None if ws is None else ws.data_ptr())
 
 
 def mbok_distill_desc_init(vocab: int, top: int, temperature: float = 1.0) -> mbok_distill_desc:

@@ -72,6 +72,7 @@ class Gpu:
         cuda = torch.cuda
         monkeypatch.setattr(bw, "load_library", lambda: library)
         monkeypatch.setattr(bw, "_WORKSPACES", {})
+        monkeypatch.setattr(bw, "_WORKSPACE_LOCKS", {})
         monkeypatch.setattr(bw, "_raw_stream", lambda dev: self.current().cuda_stream)
         monkeypatch.setattr(bw, "_current_device", lambda: 0)
         monkeypatch.setattr(torch, "empty", alloc)

@@ -1,6 +1,8 @@
 """The workspaces the binding keeps, on the GPU: their memory belongs to the
 launch stream, and what is computed through them is what a caller's own
 workspace gives."""
+import threading
+
 import pytest
 import torch
 
@@ -70,3 +72,25 @@ def test_kept_workspace_belongs_to_the_launch_stream(monkeypatch):
                 torch.cuda.synchronize()
                 assert torch.equal(out, want)
         assert seen == [handle] * 2, (stream, seen)
+
+
+def test_threads_on_one_stream():
+    """Two threads launch on the default stream at once, through its kept
+    workspace: each gets its own result every time."""
+    say("kept workspace and threads")
+    cases = [gemmt_case(512, 512, 16, 5), gemmt_case(2048, 4096, 40, 6)]
+    wrong = []
+
+    def run(call, out, want):
+        for i in range(60):
+            call()
+            if not torch.equal(out, want):
+                wrong.append((tuple(out.shape), i))
+
+    threads = [threading.Thread(target=run, args=c) for c in cases]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert not wrong, wrong[:5]

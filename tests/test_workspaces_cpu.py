@@ -1,5 +1,8 @@
 """The workspaces the binding keeps: which stream their memory belongs to, on a
 recorded GPU (no kernel runs)."""
+import threading
+import time
+
 import pytest
 import torch
 
@@ -59,3 +62,92 @@ def test_workspace_for(gpu, stream, handle):
     assert a.numel() >= 100 and b.numel() >= 2 << 20
     assert bw.workspace_for(300, "cuda:0", stream) is b
     assert [h for h, _ in gpu.allocated] == [handle] * 2
+
+
+def scale_grad(m, stream=None, T=256, n=256):
+    d = bw.mbok_desc(m=m, n=n, K=1, group=128, alpha_dtype=1, layout=1)
+    packed = on_device(bw._packed_bytes(m, n, 1, 1), dtype=torch.uint8)
+    bw.mbok_scale_grad(d, packed, on_device(T, m), on_device(T, n),
+                       on_device(m * (n // 128), dtype=torch.float32), stream=stream)
+
+
+def gated_backward(m, stream=None, T=16, n=1024):
+    d = bw.mbok_desc(m=m, n=n, K=1, group=128, alpha_dtype=1, layout=1)
+    packed = on_device(bw._packed_bytes(2 * m, n, 1, 1), dtype=torch.uint8)
+    bw.mbok_gated_backward(d, packed, on_device(T, 2 * m), on_device(T, m), on_device(T, 2 * m),
+                           on_device(T, n), stream=stream)
+
+
+def gemv(m, stream=None, n=4096):
+    d = bw.mbok_desc(m=m, n=n, K=1, group=128, alpha_dtype=1, layout=1)
+    packed = on_device(bw._packed_bytes(m, n, 1, 1), dtype=torch.uint8)
+    bw.mbok_gemv(d, packed, on_device(n), on_device(m, dtype=torch.float32), stream=stream)
+
+
+class Launches:
+    """Launch times of calls from several threads: each takes a while between its
+    first and its last kernel, as a call of two kernels does."""
+
+    def __init__(self):
+        self.active, self.met, self.lock = [], [], threading.Lock()
+
+    def __call__(self, name, args):
+        ws = args[-2]
+        assert ws, name
+        with self.lock:
+            self.met += [(ws, other) for other in self.active]
+            self.active.append(ws)
+        time.sleep(0.02)
+        with self.lock:
+            self.active.remove(ws)
+
+
+def together(*calls):
+    errors = []
+
+    def run(call):
+        try:
+            call()
+        except BaseException as e:  # noqa: B902
+            errors.append(e)
+    threads = [threading.Thread(target=run, args=(c,)) for c in calls]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join(60)
+    assert not errors, errors
+
+
+@pytest.mark.parametrize("first,m", [(gemmt, 256), (scale_grad, 256), (gated_backward, 256),
+                                     (gemvt, 8192), (gemv, 256)])
+def test_threads_on_one_stream_take_turns_with_the_kept_workspace(monkeypatch, first, m):
+    """Two threads' calls on one stream: no launch of one falls between the two
+    kernels of another."""
+    monkeypatch.setenv("MBOK_GEMV_VARIANT", "split")
+    launches = Launches()
+    gpu = Gpu(monkeypatch, launches)
+    first(m), gemmt(512)  # the kept workspace is there
+    together(*[lambda f=f, k=k, s=s: f(k, s) for f, k in ((first, m), (gemmt, 512))
+               for s in (None, 0, Stream(0))])
+    assert len(gpu.launched) == 8
+    assert launches.met == []
+
+
+def test_threads_on_two_streams_do_not_wait_for_each_other(monkeypatch):
+    both = threading.Barrier(2, timeout=30)
+    Gpu(monkeypatch, lambda name, args: both.wait())
+    together(lambda: gemmt(256, SIDE), lambda: gemmt(256, 0))
+
+
+def test_a_failed_call_gives_the_workspace_back(monkeypatch):
+    def refuse(name, args):
+        raise RuntimeError("no")
+    Gpu(monkeypatch, refuse)
+    with pytest.raises(RuntimeError):
+        gemmt(256)
+    with pytest.raises(RuntimeError):
+        gemvt(8192)
+    calls = []
+    Gpu(monkeypatch, lambda name, args: calls.append(name))
+    together(lambda: gemmt(256), lambda: gemvt(8192))
+    assert sorted(calls) == ["mbok_gemmt", "mbok_gemvt"]
