@@ -338,7 +338,9 @@ def workspace_for(nbytes: int, device=None, stream=None) -> torch.Tensor | None:
     The tensor is allocated with the target stream current, so torch's caching
     allocator ties its memory to that stream: when a larger request replaces
     it, the old block is reused only in that stream's order, after the work
-    already enqueued there that reads it.
+    already enqueued there that reads it.  While that stream is captured
+    into a graph the tensor is a new one of the graph's pool and is not kept:
+    the graph holds its memory, which a kept one's replacement would free.
 
     The calls below that keep a workspace by themselves enqueue all their
     kernels before another thread's call on the same stream may use it; two
@@ -347,12 +349,14 @@ def workspace_for(nbytes: int, device=None, stream=None) -> torch.Tensor | None:
         return None
     dev = torch.device(device) if device is not None else torch.device("cuda", torch.cuda.current_device())
     target = _torch_stream(dev, stream)
-    key = (dev.index, target.cuda_stream)
-    ws = _WORKSPACES.get(key)
-    if ws is None or ws.numel() < nbytes:
-        with torch.cuda.stream(target):
+    with torch.cuda.stream(target):
+        if torch.cuda.is_current_stream_capturing():
+            return torch.empty(nbytes, dtype=torch.uint8, device=dev)
+        key = (dev.index, target.cuda_stream)
+        ws = _WORKSPACES.get(key)
+        if ws is None or ws.numel() < nbytes:
             ws = torch.empty(max(nbytes, 1 << 20), dtype=torch.uint8, device=dev)
-        _WORKSPACES[key] = ws
+            _WORKSPACES[key] = ws
     return ws
 
 
@@ -392,12 +396,24 @@ class _Kept:
 _NO_WORKSPACE = contextlib.nullcontext()
 
 
+def _own_or_kept(need: int, device: torch.device, stream):
+    """The kept workspace, see _Kept; under graph capture one of the call's own,
+    from the graph's pool, so that no later call's growth frees it and no two
+    graphs share it."""
+    # the launch stream current, unless it is
+    here = stream is None and device.index == _current_device()
+    with _NO_WORKSPACE if here else torch.cuda.stream(_torch_stream(device, stream)):
+        if torch.cuda.is_current_stream_capturing():
+            return contextlib.nullcontext(torch.empty(need, dtype=torch.uint8, device=device))
+    return _Kept(need, device, stream)
+
+
 def _given_or_kept(need: int, workspace, device: torch.device, stream):
     """Context of mbok_gemv's and mbok_gemvt's workspace tensor, or None."""
     if workspace is None or workspace is False or need == 0:
         return _NO_WORKSPACE
     if workspace is True:
-        return _Kept(need, device, stream)
+        return _own_or_kept(need, device, stream)
     _dev(workspace, "workspace")
     if _nbytes_from(workspace) < need:
         raise ValueError("workspace too small")
@@ -408,8 +424,9 @@ def mbok_gemv(d: mbok_desc, packed: torch.Tensor, x: torch.Tensor, y: torch.Tens
               workspace: torch.Tensor | None | bool = True, stream=None) -> None:
     """y[m] (fp32, overwritten) = W_hat x for x bf16 / fp32 [n].
 
-    workspace: True (default) uses a cached workspace for this device and
-    stream; a tensor is used as given; None/False runs without one."""
+    workspace: True (default) uses a workspace kept for this device and
+    stream (under graph capture one of the graph's own); a tensor is used as
+    given; None/False runs without one."""
     _dev(packed, "packed"), _dev(x, "x"), _dev(y, "y")
     if _nbytes_from(packed) < mbok_packed_bytes(d):
         raise ValueError("packed buffer too small")
@@ -433,8 +450,9 @@ def mbok_gemvt(d: mbok_desc, packed: torch.Tensor, g: torch.Tensor, dx: torch.Te
                workspace: torch.Tensor | None | bool = True, stream=None) -> None:
     """dx[n] (fp32, overwritten) = W_hat^T g for g bf16 / fp32 [m].
 
-    workspace: True (default) uses a cached workspace for this device and
-    stream; a tensor is used as given; None/False runs without one."""
+    workspace: True (default) uses a workspace kept for this device and
+    stream (under graph capture one of the graph's own); a tensor is used as
+    given; None/False runs without one."""
     _dev(packed, "packed"), _dev(g, "g"), _dev(dx, "dx")
     if _nbytes_from(packed) < mbok_packed_bytes(d):
         raise ValueError("packed buffer too small")
@@ -668,11 +686,7 @@ def _packed(packed: torch.Tensor, dev: int, m: int, n: int, K: int, alpha_dtype:
 
 def _slices(name: str, m: int, n: int, K: int, alpha_dtype: int, T: int, workspace, dev: int,
             stream):
-    """Context of the workspace tensor of a call that may split its sum, or None.
-
-    True keeps one per (device, stream), see _Kept, except under graph capture:
-    a captured call gets memory of its own from the graph's pool, so that no
-    later call's growth frees it and no two graphs share it."""
+    """Context of the workspace tensor of a call that may split its sum, or None."""
     if workspace is None or workspace is False:
         return _NO_WORKSPACE
     need = _slices_bytes(name, m, n, K, alpha_dtype, T)
@@ -685,13 +699,7 @@ def _slices(name: str, m: int, n: int, K: int, alpha_dtype: int, T: int, workspa
         if not ws.is_contiguous() or ws.numel() * ws.itemsize < need:
             raise ValueError("workspace must be contiguous and large enough")
         return contextlib.nullcontext(ws)
-    device = torch.device("cuda", dev)
-    # the launch stream current, unless it is
-    here = stream is None and dev == _current_device()
-    with _NO_WORKSPACE if here else torch.cuda.stream(_torch_stream(device, stream)):
-        if torch.cuda.is_current_stream_capturing():
-            return contextlib.nullcontext(torch.empty(need, dtype=torch.uint8, device=device))
-    return _Kept(need, device, stream)
+    return _own_or_kept(need, torch.device("cuda", dev), stream)
 
 
 def mbok_gemmt_workspace_bytes(d: mbok_desc, T: int) -> int:

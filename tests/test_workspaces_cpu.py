@@ -151,3 +151,33 @@ def test_a_failed_call_gives_the_workspace_back(monkeypatch):
     Gpu(monkeypatch, lambda name, args: calls.append(name))
     together(lambda: gemmt(256), lambda: gemvt(8192))
     assert sorted(calls) == ["mbok_gemmt", "mbok_gemvt"]
+
+
+@pytest.mark.parametrize("call,m", [(gemmt, 256), (scale_grad, 256), (gated_backward, 256),
+                                    (gemvt, 8192), (gemv, 256)])
+@pytest.mark.parametrize("stream", [None, 0, SIDE])
+def test_captured_calls_have_memory_of_their_own(gpu, monkeypatch, call, m, stream):
+    """A graph's workspace is neither the kept one, which a larger request of
+    any other call frees, nor another captured call's, nor kept afterwards."""
+    monkeypatch.setenv("MBOK_GEMV_VARIANT", "split")
+    handle = 0 if not isinstance(stream, Stream) else stream.cuda_stream
+    call(m, stream)
+    gpu.capturing = {handle}
+    call(m, stream), call(m, stream)
+    gpu.capturing = set()
+    gemmt(2048, stream), call(m, stream)
+    used = [args[-2] for _, args in gpu.launched]
+    assert used[1] not in (used[0], used[2], used[3], used[4])
+    assert used[2] not in (used[0], used[3], used[4])
+    assert {w.data_ptr() for w in bw._WORKSPACES.values()} == {used[4]}
+    # each belongs to the launch stream
+    assert {h for h, _ in gpu.allocated} == {handle}
+
+
+def test_workspace_for_under_capture(gpu):
+    kept = bw.workspace_for(100, "cuda:0")
+    gpu.capturing = {0}
+    a, b = (bw.workspace_for(100, "cuda:0") for _ in range(2))
+    gpu.capturing = set()
+    assert len({x.data_ptr() for x in (kept, a, b)}) == 3
+    assert bw.workspace_for(100, "cuda:0") is kept
