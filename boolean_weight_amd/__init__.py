@@ -605,9 +605,11 @@ _FLOATS = {torch.float32: MBOK_F32, torch.float16: MBOK_F16, torch.bfloat16: MBO
 # Python adds to a launch counts: the raw stream handle and current device
 # come from the C functions behind torch.cuda.current_stream() and
 # current_device() (together 1.3 us less per call), tensors are asked for each
-# attribute once, and layer sizes are remembered by shape.
-_raw_stream = torch._C._cuda_getCurrentRawStream
-_current_device = torch._C._cuda_getDevice
+# attribute once, and layer sizes are remembered by shape.  A torch without GPU
+# support has neither function; the host-only calls work there.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
+                      lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
 @functools.lru_cache(maxsize=4096)
