@@ -345,7 +345,8 @@ int mbok_gated_backward(const mbok_desc* d, const void* packed, const void* pre,
 }
 
 static int check_distill(const mbok_distill_desc* d) {
-  if (!d || !std::isfinite(d->temperature) || !(d->temperature > 0.f))
+  // below 2^-126 the kernels' fp32 factor log2(e) / tau is not finite
+  if (!d || !std::isnormal(d->temperature) || !(d->temperature > 0.f))
     return MBOK_ERR_INVALID_ARG;
   if (d->vocab < 1 || d->vocab > MBOK_MAX_VOCAB || d->top < 1 || d->top > MBOK_MAX_TOP)
     return MBOK_ERR_SHAPE;

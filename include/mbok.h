@@ -665,7 +665,7 @@ int mbok_gated_backward(const mbok_desc* d, const void* packed, const void* pre,
 typedef struct mbok_distill_desc {
   int32_t vocab;     /* V, 1 .. MBOK_MAX_VOCAB */
   int32_t top;       /* listed entries per row, 1 .. MBOK_MAX_TOP */
-  float temperature; /* tau, finite and > 0 */
+  float temperature; /* tau, finite and at least 2^-126 */
 } mbok_distill_desc;
 
 /* Host only.  Errors: INVALID_ARG (NULL, temperature), SHAPE (vocab, top). */

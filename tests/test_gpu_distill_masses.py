@@ -216,3 +216,19 @@ def test_rest_far_below_with_bad_values():
     idx[7, :] = -1
     lse = torch.logsumexp(l, -1) + 0.2
     check(Z, l, idx, 1.0, lse)
+
+
+def test_smallest_temperature():
+    """tau = 2^-126: all of q is on the largest logit."""
+    say("distill smallest temperature")
+    Z, l, idx, _ = inputs(3, 100, 5, 2)
+    Z[0, 50] = Z[0].max() + 1.0  # zero shifted logits and others
+    Z[1] -= Z[1].max()
+    tau = 2.0 ** -126
+    l = l / 20  # below 0.5; the largest entry's log-sum is exact
+    l[:, 0] = 0.5
+    for lse in (None, torch.full((3,), 0.5 / tau)):
+        for mode in MODES:
+            loss, dZ = run(Z, l, idx, tau, lse, mode=mode)
+            assert torch.isfinite(loss).all() and torch.isfinite(dZ).all()
+            assert (dZ.abs() <= 2.0 ** -125).all()
