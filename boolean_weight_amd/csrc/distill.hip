@@ -352,7 +352,15 @@ __global__ void __launch_bounds__(kMaxThreads) distill_kernel(
   // that mean is the entropy of q less log sum.  (Carrying it exactly cost
   // two instructions per logit, the subtraction one: 2048 x 32000 bf16 with
   // gradient 76.5 -> 74.1 us.)
+  // A thread adds at most 128 terms in fp32: a row that is read again adds each
+  // vector's sum in float64.
   float sum_z = 0.f;
+  double sum_far = 0.0;
+  auto next_vector = [&] {
+    if (NV > 0) return;
+    sum_far += (double)sum_z;
+    sum_z = 0.f;
+  };
   const float k = zu * r.c_hi;
   const bool near = fabsf(k) < 256.f;
   auto sum = [&](auto near_c) {
@@ -368,11 +376,13 @@ __global__ void __launch_bounds__(kMaxThreads) distill_kernel(
           const float y = ex(x.v[e]);
           sum_z += (m >> e) & 1u ? 0.f : y;
         }
+        next_vector();
       });
     } else {
       each([&](int, const Vec<ZT>& x) {
 #pragma unroll
         for (int e = 0; e < N; ++e) sum_z += ex(x.v[e]);
+        next_vector();
       });
     }
   };
@@ -381,7 +391,7 @@ __global__ void __launch_bounds__(kMaxThreads) distill_kernel(
   {
     const double fix =
         near ? 1.0 - (double)kLn2 * ((double)zu * (double)r.c_hi - (double)k) : 1.0;
-    const double dz = wave_sum((double)sum_z) * fix;
+    const double dz = wave_sum((double)sum_z + sum_far) * fix;
     double dl = 0.0;
     if (rest) {
       const double inv_tau = 1.0 / (double)r.tau;

@@ -232,3 +232,21 @@ def test_smallest_temperature():
             loss, dZ = run(Z, l, idx, tau, lse, mode=mode)
             assert torch.isfinite(loss).all() and torch.isfinite(dZ).all()
             assert (dZ.abs() <= 2.0 ** -125).all()
+
+
+@pytest.mark.parametrize("z", ["f32", "bf16"])
+@pytest.mark.parametrize("V", [131072, 262144, bw.MBOK_MAX_VOCAB])
+def test_small_terms_beside_a_large_one(V, z):
+    """Each 1 in the sum is followed by terms just below half its step: a thread
+    that adds n of them in fp32 loses up to n 2^-24 of S.  With 128 at most log S
+    is off by 2^-17, the exponentials by 2^-23, log2(e) / tau by 2^-24 log V and
+    the loss's rounding by 2^-24 of a value below 16."""
+    say(f"distill small terms V={V} {z}")
+    Z = torch.full((1, V), math.log(0.97 * 2.0 ** -24)).to(TYPES[z])
+    # the first 1024 vectors of 16 bytes hold one logit of 0 each
+    Z[0, :1024 * (4 if z == "f32" else 8):4 if z == "f32" else 8] = 0.0
+    l, idx = torch.zeros(1, 1), torch.zeros(1, 1, dtype=torch.int64)
+    want = float(torch.logsumexp(Z[0].to(F64), 0))
+    for lse in (None, torch.zeros(1)):
+        loss, _ = run(Z, l, idx, 1.0, lse)
+        assert abs(float(loss) - want) <= 2.0 ** -17 + 2.0 ** -23 + 13.2 * 2.0 ** -24 + 2.0 ** -20
