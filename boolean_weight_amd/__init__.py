@@ -662,8 +662,9 @@ def _matrix(t: torch.Tensor, name: str, dev: int, rows: int, cols: int, dtype) -
     if step != 1 and shape[1] > 1:
         raise ValueError(f"{name} rows must be contiguous")
     if rows == 1:
-        # the stride of a single row is arbitrary and never used
-        return (shape[1] + 7) // 8 * 8
+        # the stride of a single row is arbitrary and never used; one value per
+        # operand, so that views of one row are the same matrix to the library
+        return (cols + 7) // 8 * 8
     if ld < cols:
         raise ValueError(f"{name} rows must not overlap")
     return ld
