@@ -27,9 +27,10 @@ __all__ = [
     "mbok_gemvt", "mbok_gemvt_workspace_bytes", "mbok_gemvt_noalloc", "mbok_gemvt_scratch_bytes",
     "mbok_svid_workspace_bytes", "mbok_svid_decompose", "mbok_svid_pack",
     "mbok_svid_gemv_workspace_bytes", "mbok_svid_gemv", "MBOK_MAX_SVID_ITERS",
-    "mbok_gemmt", "mbok_gemmt_workspace_bytes", "mbok_scale_grad",
+    "mbok_gemmt", "mbok_gemmt_precise", "mbok_gemmt_workspace_bytes", "mbok_scale_grad",
     "mbok_scale_grad_workspace_bytes", "MBOK_ACT_SILU", "MBOK_ACT_GELU", "mbok_gated_stack",
-    "mbok_gated_pack", "mbok_gated", "mbok_gated_backward", "mbok_distill_desc",
+    "mbok_gated_pack", "mbok_gated", "mbok_gated_precise", "mbok_gated_backward",
+    "mbok_gated_backward_precise", "mbok_distill_desc",
     "mbok_distill_desc_init", "mbok_distill", "mbok_distill_backward", "MBOK_MAX_TOP",
     "MBOK_MAX_VOCAB", "MBOK_MAX_DISTILL_ROWS", "MBOK_DISTILL_STATS",
     "mbok_version", "workspace_for",
@@ -119,14 +120,18 @@ def load_library() -> ctypes.CDLL:
         "mbok_svid_gemv_workspace_bytes": (SZ, [D]),
         "mbok_svid_gemv": (ctypes.c_int, [D, P, P, P, I32, P, P, P]),
         "mbok_gemmt": (ctypes.c_int, [D, P, P, I64, I64, P, I64, P, P]),
+        "mbok_gemmt_precise": (ctypes.c_int, [D, P, P, I64, I64, P, I64, P, P]),
         "mbok_gemmt_workspace_bytes": (SZ, [D, I64]),
         "mbok_scale_grad": (ctypes.c_int, [D, P, P, I64, I64, P, I64, P, I32, P, P]),
         "mbok_scale_grad_workspace_bytes": (SZ, [D, I64]),
         "mbok_gated_stack": (ctypes.c_int, [D, D]),
         "mbok_gated_pack": (ctypes.c_int, [D, P, P, P, P, P, P]),
         "mbok_gated": (ctypes.c_int, [D, P, P, I32, I64, I64, I32, P, I64, P, I64, P]),
+        "mbok_gated_precise": (ctypes.c_int, [D, P, P, I32, I64, I64, I32, P, I64, P, I64, P]),
         "mbok_gated_backward": (ctypes.c_int, [D, P, P, I64, P, I64, I64, I32, P, I64, P, I64, P,
                                                P]),
+        "mbok_gated_backward_precise": (ctypes.c_int, [D, P, P, I64, P, I64, I64, I32, P, I64, P,
+                                                       I64, P, P]),
         "mbok_distill_desc_init": (ctypes.c_int, [DD, I32, I32, F]),
         "mbok_distill": (ctypes.c_int, [DD, P, I32, I64, I64, P, I32, P, I64, P, P, P, P, P, I32,
                                         I64, P]),
@@ -721,6 +726,17 @@ def mbok_gemmt(d: mbok_desc, packed: torch.Tensor, dY: torch.Tensor, dX: torch.T
     workspace: True (default) uses a workspace kept for this device and
     stream (under graph capture one of the graph's own); a tensor is used as
     given; None/False runs without one."""
+    _gemmt_call("mbok_gemmt", d, packed, dY, dX, workspace, stream)
+
+
+def mbok_gemmt_precise(d: mbok_desc, packed: torch.Tensor, dY: torch.Tensor, dX: torch.Tensor,
+                       workspace: torch.Tensor | None | bool = True, stream=None) -> None:
+    """mbok_gemmt with each weight carried as two bf16 terms (twice the matrix
+    work)."""
+    _gemmt_call("mbok_gemmt_precise", d, packed, dY, dX, workspace, stream)
+
+
+def _gemmt_call(name: str, d: mbok_desc, packed, dY, dX, workspace, stream) -> None:
     dev = _first(dY, "dY")
     m, n, K, at = d.m, d.n, d.K, d.alpha_dtype
     T = dY.shape[0]
@@ -728,7 +744,7 @@ def mbok_gemmt(d: mbok_desc, packed: torch.Tensor, dY: torch.Tensor, dX: torch.T
     lddx = _matrix(dX, "dX", dev, T, n, torch.bfloat16)
     pp = _packed(packed, dev, m, n, K, at)
     with _slices("mbok_gemmt_workspace_bytes", m, n, K, at, T, workspace, dev, stream) as ws:
-        _launch(load_library().mbok_gemmt, "mbok_gemmt", dev, stream, ctypes.byref(d), pp,
+        _launch(getattr(load_library(), name), name, dev, stream, ctypes.byref(d), pp,
                 dY.data_ptr(), T, lddy, dX.data_ptr(), lddx, None if ws is None else ws.data_ptr())
 
 
@@ -783,6 +799,18 @@ def mbok_gated(d: mbok_desc, packed: torch.Tensor, X: torch.Tensor, H: torch.Ten
     """H[T, m] (bf16, overwritten) = act(X Wg^T) (.) (X Wu^T) for X bf16 [T, n];
     d describes one projection, packed is mbok_gated_pack's buffer.  pre bf16
     [T, 16 ceil(m / 8)] receives the pre-activations in the stacked order."""
+    _gated_call("mbok_gated", d, packed, X, H, pre, act, stream)
+
+
+def mbok_gated_precise(d: mbok_desc, packed: torch.Tensor, X: torch.Tensor, H: torch.Tensor,
+                       pre: torch.Tensor | None = None, act: int = MBOK_ACT_SILU,
+                       stream=None) -> None:
+    """mbok_gated with each weight carried as two bf16 terms for T > 16 (twice
+    the matrix work)."""
+    _gated_call("mbok_gated_precise", d, packed, X, H, pre, act, stream)
+
+
+def _gated_call(name: str, d: mbok_desc, packed, X, H, pre, act, stream) -> None:
     dev = _first(X, "X")
     m, n = d.m, d.n
     T, m2 = X.shape[0], 16 * ((m + 7) // 8)
@@ -792,7 +820,7 @@ def mbok_gated(d: mbok_desc, packed: torch.Tensor, X: torch.Tensor, H: torch.Ten
     if pre is not None:
         ldpre = _matrix(pre, "pre", dev, T, m2, torch.bfloat16)
         pre_ptr = pre.data_ptr()
-    _launch(load_library().mbok_gated, "mbok_gated", dev, stream, ctypes.byref(d),
+    _launch(getattr(load_library(), name), name, dev, stream, ctypes.byref(d),
             _packed(packed, dev, m2, n, d.K, d.alpha_dtype), X.data_ptr(), MBOK_BF16, T, ldx, act,
             H.data_ptr(), ldh, pre_ptr, ldpre)
 
@@ -806,6 +834,22 @@ def mbok_gated_backward(d: mbok_desc, packed: torch.Tensor, pre: torch.Tensor, d
     mbok_gated wrote it and dH bf16 [T, m].
 
     workspace: as for mbok_gemmt."""
+    _gated_backward_call("mbok_gated_backward", d, packed, pre, dH, dpre, dX, act, workspace,
+                         stream)
+
+
+def mbok_gated_backward_precise(d: mbok_desc, packed: torch.Tensor, pre: torch.Tensor,
+                                dH: torch.Tensor, dpre: torch.Tensor,
+                                dX: torch.Tensor | None = None, act: int = MBOK_ACT_SILU,
+                                workspace: torch.Tensor | None | bool = True,
+                                stream=None) -> None:
+    """mbok_gated_backward with dX as mbok_gemmt_precise computes it."""
+    _gated_backward_call("mbok_gated_backward_precise", d, packed, pre, dH, dpre, dX, act,
+                         workspace, stream)
+
+
+def _gated_backward_call(name: str, d: mbok_desc, packed, pre, dH, dpre, dX, act, workspace,
+                         stream) -> None:
     dev = _first(dH, "dH")
     m, n, K, at = d.m, d.n, d.K, d.alpha_dtype
     T, m2 = dH.shape[0], 16 * ((m + 7) // 8)
@@ -819,9 +863,9 @@ def mbok_gated_backward(d: mbok_desc, packed: torch.Tensor, pre: torch.Tensor, d
         dx_ptr = dX.data_ptr()
         held = _slices("mbok_gemmt_workspace_bytes", m2, n, K, at, T, workspace, dev, stream)
     with held as ws:
-        _launch(load_library().mbok_gated_backward, "mbok_gated_backward", dev, stream,
-                ctypes.byref(d), pp, pre.data_ptr(), ldpre, dH.data_ptr(), lddh, T, act,
-                dpre.data_ptr(), lddpre, dx_ptr, lddx, None if ws is None else ws.data_ptr())
+        _launch(getattr(load_library(), name), name, dev, stream, ctypes.byref(d), pp,
+                pre.data_ptr(), ldpre, dH.data_ptr(), lddh, T, act, dpre.data_ptr(), lddpre,
+                dx_ptr, lddx, None if ws is None else ws.data_ptr())
 
 
 def mbok_distill_desc_init(vocab: int, top: int, temperature: float = 1.0) -> mbok_distill_desc:

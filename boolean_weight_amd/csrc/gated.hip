@@ -51,16 +51,18 @@ __global__ void __launch_bounds__(256) gated_backward_kernel(
 }  // namespace
 
 int launch_gated(const mbok_desc* d, const void* packed, const void* X, int64_t T, int64_t ldx,
-                 int act, void* H, int64_t ldh, void* pre, int64_t ldpre, hipStream_t stream) {
+                 int act, void* H, int64_t ldh, void* pre, int64_t ldpre, int passes,
+                 hipStream_t stream) {
   const mbok_desc stacked = gated_stacked(d);
   const GatedOut out = {reinterpret_cast<uint16_t*>(H), ldh, reinterpret_cast<uint16_t*>(pre),
                         ldpre, d->m, act};
-  return launch_gated_stacked(&stacked, packed, X, T, ldx, out, stream);
+  return launch_gated_stacked(&stacked, packed, X, T, ldx, out, passes, stream);
 }
 
 int launch_gated_backward(const mbok_desc* d, const void* packed, const void* pre, int64_t ldpre,
                           const void* dH, int64_t lddh, int64_t T, int act, void* dpre,
-                          int64_t lddpre, void* dX, int64_t lddx, void* ws, hipStream_t stream) {
+                          int64_t lddpre, void* dX, int64_t lddx, void* ws, int passes,
+                          hipStream_t stream) {
   const int64_t items = T * ((d->m + 7) / 8);
   const int64_t blocks = (items + 255) / 256;
   if (blocks > UINT32_MAX / 256) return MBOK_ERR_SHAPE;  // a launch has 2^32 threads at most
@@ -71,7 +73,7 @@ int launch_gated_backward(const mbok_desc* d, const void* packed, const void* pr
   if (hipGetLastError() != hipSuccess) return MBOK_ERR_HIP;
   if (!dX) return MBOK_OK;
   const mbok_desc stacked = gated_stacked(d);
-  return launch_gemmt(&stacked, packed, dpre, T, lddpre, dX, lddx, ws, stream);
+  return launch_gemmt(&stacked, packed, dpre, T, lddpre, dX, lddx, ws, passes, stream);
 }
 
 }  // namespace mbok

@@ -62,7 +62,10 @@ struct Tile {
   static_assert(threads == 2 * BN, "a thread unpacks one 32-column word of a row");
 };
 
-template <typename AT, int K, typename P>
+// TWO: each 64 columns are two steps with the same activations, the levels
+// rounded to bf16 and then the bf16 rounding of what that left (16 significant
+// bits together): twice the matrix work.
+template <typename AT, int K, typename P, bool TWO>
 __device__ __forceinline__ void gated_tile(const uint32_t* __restrict__ bits,
                                            const AT* __restrict__ scales,
                                            const uint16_t* __restrict__ X, int64_t ldx,
@@ -71,7 +74,8 @@ __device__ __forceinline__ void gated_tile(const uint32_t* __restrict__ bits,
   constexpr int TI = P::TI, NU = P::NU, kThreads = P::threads, kBT = P::BT;
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int S = 2 * G;  // steps
+  const int S = (TWO ? 4 : 2) * G;  // steps
+  auto block = [](int s) { return TWO ? s >> 1 : s; };  // 64 columns of a step
   auto xbuf = [&](int b) { return smem + b * (P::kX + P::kW); };
   auto wbuf = [&](int b) { return smem + b * (P::kX + P::kW) + P::kX; };
 
@@ -108,7 +112,7 @@ __device__ __forceinline__ void gated_tile(const uint32_t* __restrict__ bits,
   auto copy_x = [&](int s, int b) {
 #pragma unroll
     for (int u = 0; u < NU; ++u)
-      copy_to_lds(tile_x + s * kBK, xoff[u], xbuf(b) + (u * kThreads + wave * kWave) * 8);
+      copy_to_lds(tile_x + block(s) * kBK, xoff[u], xbuf(b) + (u * kThreads + wave * kWave) * 8);
   };
   struct Signs {
     uint32_t w[K];
@@ -116,8 +120,8 @@ __device__ __forceinline__ void gated_tile(const uint32_t* __restrict__ bits,
   };
   Signs R0, R1;
   auto load_w = [&](int s, Signs& R) {
-    const int g = s >> 1;
-    const char* wb = tile_w + (int64_t)g * (K * kRowBlock * 16) + 8 * (s & 1);
+    const int g = block(s) >> 1;
+    const char* wb = tile_w + (int64_t)g * (K * kRowBlock * 16) + 8 * (block(s) & 1);
     const char* sb = tile_s + (int64_t)g * (int)(K * kRowBlock * sizeof(AT));
 #pragma unroll
     for (int k = 0; k < K; ++k) {
@@ -127,7 +131,7 @@ __device__ __forceinline__ void gated_tile(const uint32_t* __restrict__ bits,
   };
 
   // one step's weights in kChunks pieces of a few instructions; the levels of
-  // a scale group serve its two steps
+  // a scale group serve its two steps (TWO: are formed for each of the four)
   constexpr int kChunks = 24;
   float af[K];
   uint32_t pairs[2], V[4], lo = 0, hi = 0, o4[4];
@@ -136,13 +140,14 @@ __device__ __forceinline__ void gated_tile(const uint32_t* __restrict__ bits,
     *reinterpret_cast<u32x4*>(wbuf(b) + wput + 8 * ((4 * word + p) ^ wkey)) =
         u32x4{o4[0], o4[1], o4[2], o4[3]};
   };
-  auto form = [&](int b, const Signs& R, int c, bool levels) {
+  auto form = [&](int b, const Signs& R, int c, bool levels, bool lo_levels) {
     if (levels && c == 0) {
 #pragma unroll
       for (int k = 0; k < K; ++k) af[k] = alpha_to_f32<AT>(R.a[k]);
     }
     if constexpr (K <= 3) {
-      if (levels && c < 2) pairs[c] = upper_pair<K>(af, c);
+      if (levels && c < 2)
+        pairs[c] = lo_levels ? upper_pair<K, true>(af, c) : upper_pair<K>(af, c);
       if (levels && c == 2) L = pack_levels<K>(pairs[0], pairs[1]);
       if (c >= 3 && c < 6) word_selectors_part<K>(R.w, V, c - 3);
       const int h = (c - 8) >> 1;  // quad of the word
@@ -159,7 +164,8 @@ __device__ __forceinline__ void gated_tile(const uint32_t* __restrict__ bits,
     } else if (c >= 8 && (c & 3) == 0) {
       const int p = (c - 8) >> 2;
       uint32_t o32[16];
-      unpack_word_k4<false>(R.w, af, o32);
+      if (lo_levels) unpack_word_k4<true>(R.w, af, o32);
+      else unpack_word_k4<false>(R.w, af, o32);
 #pragma unroll
       for (int e = 0; e < 4; ++e) o4[e] = o32[4 * p + e];
       put(b, p);
@@ -206,7 +212,7 @@ __device__ __forceinline__ void gated_tile(const uint32_t* __restrict__ bits,
   load_w(0, R0);
   load_w(1, R1);
 #pragma unroll
-  for (int c = 0; c < kChunks; ++c) form(0, R0, c, true);
+  for (int c = 0; c < kChunks; ++c) form(0, R0, c, true, false);
   copies_done();
   pin<K>(R1);
   __syncthreads();
@@ -218,7 +224,7 @@ __device__ __forceinline__ void gated_tile(const uint32_t* __restrict__ bits,
   for (int i = 0; i < TI; ++i) read_x(0, 0, i);
   // Step s: its products from buffer b = s % 2 while the weights of step s + 1
   // are formed from R in the other; even steps of the contraction begin a
-  // scale group.
+  // scale group (TWO: odd ones are the residues').
   auto step = [&](int s, int b, Signs& R) {
 #pragma unroll
     for (int q = 0; q < 3; ++q)
@@ -226,7 +232,7 @@ __device__ __forceinline__ void gated_tile(const uint32_t* __restrict__ bits,
         const int y = q * NX + x;
 #pragma unroll
         for (int c = 0; c < kChunks; ++c)
-          if (c * 3 * NX / kChunks == y) form(b ^ 1, R, c, b == 1);
+          if (c * 3 * NX / kChunks == y) form(b ^ 1, R, c, TWO || b == 1, TWO && b == 0);
       });
     copies_done();
     __syncthreads();
@@ -294,7 +300,7 @@ __device__ __forceinline__ void gated_tile(const uint32_t* __restrict__ bits,
   }
 }
 
-template <typename AT, int K, typename P>
+template <typename AT, int K, typename P, bool TWO>
 __global__ void __launch_bounds__(P::threads) gated_mfma_kernel(
     const uint32_t* __restrict__ bits, const AT* __restrict__ scales,
     const uint16_t* __restrict__ X, int64_t ldx, GatedOut out, int T, int m_pad, int G, int ntx,
@@ -305,11 +311,11 @@ __global__ void __launch_bounds__(P::threads) gated_mfma_kernel(
   const int even = blocks & ~7;
   const int p = b < even ? (b & 7) * (even >> 3) + (b >> 3) : b;
   const int tile = tile_at(p, ntx, nty);
-  gated_tile<AT, K, P>(bits, scales, X, ldx, out, T, m_pad, G, (tile / ntx) * P::BT,
-                       (tile % ntx) * P::BN, smem);
+  gated_tile<AT, K, P, TWO>(bits, scales, X, ldx, out, T, m_pad, G, (tile / ntx) * P::BT,
+                            (tile % ntx) * P::BN, smem);
 }
 
-template <typename AT, int K>
+template <typename AT, int K, bool TWO>
 void launch_k(const Geom& geo, const void* packed, const uint16_t* X, int64_t T, int64_t ldx,
               const GatedOut& out, hipStream_t stream) {
   const uint32_t* bits = reinterpret_cast<const uint32_t*>(packed);
@@ -319,7 +325,7 @@ void launch_k(const Geom& geo, const void* packed, const uint16_t* X, int64_t T,
   auto go = [&](auto tile) {
     using P = decltype(tile);
     const int ntx = (geo.m + P::BN - 1) / P::BN, nty = (int)((T + P::BT - 1) / P::BT);
-    hipLaunchKernelGGL((gated_mfma_kernel<AT, K, P>), dim3((unsigned)ntx * (unsigned)nty),
+    hipLaunchKernelGGL((gated_mfma_kernel<AT, K, P, TWO>), dim3((unsigned)ntx * (unsigned)nty),
                        dim3(P::threads), P::lds, stream, bits, scales, X, ldx, out, (int)T,
                        geo.RB * kRowBlock, geo.G, ntx, nty);
   };
@@ -331,14 +337,14 @@ void launch_k(const Geom& geo, const void* packed, const uint16_t* X, int64_t T,
   else go(Tile<2, 1, 1>{});
 }
 
-template <typename AT>
+template <typename AT, bool TWO>
 void launch_t(const Geom& geo, const void* packed, const uint16_t* X, int64_t T, int64_t ldx,
               const GatedOut& out, hipStream_t stream) {
   switch (geo.K) {
-    case 1: launch_k<AT, 1>(geo, packed, X, T, ldx, out, stream); break;
-    case 2: launch_k<AT, 2>(geo, packed, X, T, ldx, out, stream); break;
-    case 3: launch_k<AT, 3>(geo, packed, X, T, ldx, out, stream); break;
-    default: launch_k<AT, 4>(geo, packed, X, T, ldx, out, stream); break;
+    case 1: launch_k<AT, 1, TWO>(geo, packed, X, T, ldx, out, stream); break;
+    case 2: launch_k<AT, 2, TWO>(geo, packed, X, T, ldx, out, stream); break;
+    case 3: launch_k<AT, 3, TWO>(geo, packed, X, T, ldx, out, stream); break;
+    default: launch_k<AT, 4, TWO>(geo, packed, X, T, ldx, out, stream); break;
   }
 }
 
@@ -347,15 +353,18 @@ void launch_t(const Geom& geo, const void* packed, const uint16_t* X, int64_t T,
 // d: the stacked layer.  The kernel's offsets inside the layer's signs and
 // inside a tile's activations are 32 bits.
 int launch_gated_mfma(const mbok_desc* d, const void* packed, const void* X, int64_t T,
-                      int64_t ldx, const GatedOut& out, hipStream_t stream) {
+                      int64_t ldx, const GatedOut& out, int passes, hipStream_t stream) {
   const Geom geo = make_geom(d);
   if (geo.bits_bytes / 4 >= (int64_t(1) << 32)) return MBOK_ERR_SHAPE;
   if (ldx >= (int64_t(1) << 32) / 512) return MBOK_ERR_INVALID_ARG;
   const uint16_t* x = reinterpret_cast<const uint16_t*>(X);
-  if (d->alpha_dtype == MBOK_F16)
-    launch_t<uint16_t>(geo, packed, x, T, ldx, out, stream);
-  else
-    launch_t<float>(geo, packed, x, T, ldx, out, stream);
+  auto go = [&](auto scale) {
+    using AT = decltype(scale);
+    if (passes == 2) launch_t<AT, true>(geo, packed, x, T, ldx, out, stream);
+    else launch_t<AT, false>(geo, packed, x, T, ldx, out, stream);
+  };
+  if (d->alpha_dtype == MBOK_F16) go(uint16_t{});
+  else go(float{});
   return hipGetLastError() == hipSuccess ? MBOK_OK : MBOK_ERR_HIP;
 }
 

@@ -650,8 +650,8 @@ TokenKernel token_kernel(const mbok_desc* d, int64_t T) {
 // 13824x5120, K = 3 19.5 / 34.4; two 4096x4096, K = 2 8.8 / 7.7; its two-octet
 // form for 16 tokens 21.9 / 21.8).
 int launch_gated_stacked(const mbok_desc* d, const void* packed, const void* X, int64_t T,
-                         int64_t ldx, const GatedOut& out, hipStream_t stream) {
-  if (T > skinny_max_tokens()) return launch_gated_mfma(d, packed, X, T, ldx, out, stream);
+                         int64_t ldx, const GatedOut& out, int passes, hipStream_t stream) {
+  if (T > skinny_max_tokens()) return launch_gated_mfma(d, packed, X, T, ldx, out, passes, stream);
   if (T == 1) return launch_gated_f4(d, packed, X, T, ldx, out, stream);
   if ((T - 1) * ldx + d->n <= INT32_MAX && T <= gated_f4_max_tokens()) {
     const char* v = getenv("MBOK_SKINNY_VARIANT");

@@ -72,7 +72,10 @@ __device__ __forceinline__ bf16x8 read_tr(const uint16_t* p, const uint16_t* p4)
 }
 
 // SLICED: every tile is (full = 0), which leaves the other epilogue out.
-template <typename AT, int K, typename TL, bool ALIGNED, bool SLICED>
+// TWO: each row block is two steps, W_hat's levels rounded to bf16 and then the
+// bf16 rounding of what that left (16 significant bits together), with the same
+// dY tile: twice the matrix work.
+template <typename AT, int K, typename TL, bool ALIGNED, bool SLICED, bool TWO>
 __global__ void __launch_bounds__(kThreads) gemmt_kernel(
     const uint32_t* __restrict__ bits, const AT* __restrict__ scales,
     const uint16_t* __restrict__ dY, int64_t lddy, uint16_t* __restrict__ dX, int64_t lddx,
@@ -104,7 +107,7 @@ __global__ void __launch_bounds__(kThreads) gemmt_kernel(
   const int rb1 = (int)((uint32_t)RB * (slice + 1) / parts);
   // steps over whole row blocks; a partial last block is the tail
   const int full_end = min(rb1, m / kRowBlock);
-  const int S = full_end - rb0;  // may be 0 or less
+  const int S = (full_end - rb0) * (TWO ? 2 : 1);  // may be 0 or less
   const bool tail = rb1 > full_end;
 
   // unpack role: row `lane` of the step's block, 32-column word `wave` of the tile
@@ -209,7 +212,8 @@ __global__ void __launch_bounds__(kThreads) gemmt_kernel(
     *reinterpret_cast<u32x4*>(wbuf(b) + wput + 8 * (q ^ wkey)) =
         u32x4{out[0], out[1], out[2], out[3]};
   };
-  auto form = [&](int b, const StepRegs& R, int c) {
+  // lo: the residues' step
+  auto form = [&](int b, const StepRegs& R, int c, bool lo_levels) {
     if (c == 0) {
 #pragma unroll
       for (int k = 0; k < K; ++k) af[k] = alpha_to_f32<AT>(R.a[k]);
@@ -219,7 +223,7 @@ __global__ void __launch_bounds__(kThreads) gemmt_kernel(
         *reinterpret_cast<u32x4*>(abuf(b) + (c * kThreads + tid) * 8) = R.x[c];
     }
     if constexpr (K <= 3) {
-      if (c < 2) pairs[c] = upper_pair<K>(af, c);
+      if (c < 2) pairs[c] = lo_levels ? upper_pair<K, true>(af, c) : upper_pair<K>(af, c);
       if (c == 2) L = pack_levels<K>(pairs[0], pairs[1]);
       if (c >= 3 && c < 6) word_selectors_part<K>(R.w, V, c - 3);
       if (c >= 8) {
@@ -236,15 +240,16 @@ __global__ void __launch_bounds__(kThreads) gemmt_kernel(
     } else if (c >= 8 && (c & 3) == 0) {
       uint32_t o32[16];
       const int q = (c - 8) >> 2;
-      unpack_word_k4<false>(R.w, af, o32);
+      if (lo_levels) unpack_word_k4<true>(R.w, af, o32);
+      else unpack_word_k4<false>(R.w, af, o32);
 #pragma unroll
       for (int e = 0; e < 4; ++e) out[e] = o32[4 * q + e];
       w_piece(b, q);
     }
   };
-  auto form_all = [&](int b, const StepRegs& R) {
+  auto form_all = [&](int b, const StepRegs& R, bool lo_levels) {
 #pragma unroll
-    for (int c = 0; c < kChunks; ++c) form(b, R, c);
+    for (int c = 0; c < kChunks; ++c) form(b, R, c, lo_levels);
   };
 
   bf16x8 pa[2][TI], pb[2][TJ];
@@ -290,12 +295,13 @@ __global__ void __launch_bounds__(kThreads) gemmt_kernel(
 
   if (S > 0) {
     const int last = full_end - 1;
-    auto at = [&](int s) { return min(rb0 + s, last); };  // the extra steps at the end are unused
+    // the row block of a step; the extra steps at the end are unused
+    auto at = [&](int s) { return min(rb0 + (TWO ? s >> 1 : s), last); };
     load_a(at(0), 0, R0);
     load_w(at(0), R0);
     if constexpr (!ALIGNED) load_a(at(1), 1, R1);
     load_w(at(1), R1);
-    form_all(0, R0);
+    form_all(0, R0, false);
     copies_done();
     pin<K>(R1);
     __syncthreads();
@@ -314,7 +320,7 @@ __global__ void __launch_bounds__(kThreads) gemmt_kernel(
           const int y = q * NX + x;
 #pragma unroll
           for (int c = 0; c < kChunks; ++c)
-            if (c * 3 * NX / kChunks == y) form(b ^ 1, R, c);
+            if (c * 3 * NX / kChunks == y) form(b ^ 1, R, c, TWO && b == 0);
         });
       copies_done();
       __syncthreads();
@@ -340,11 +346,15 @@ __global__ void __launch_bounds__(kThreads) gemmt_kernel(
       for (int u = 0; u < NA; ++u)
         if (a_live) R0.x[u] = *reinterpret_cast<const u32x4*>(abuf(0) + (u * kThreads + tid) * 8);
     }
-    form_all(0, R0);
-    __syncthreads();
-    first_operands(0);
 #pragma unroll
-    for (int q = 0; q < 4; ++q) products(q, 0, q < 3 ? q + 1 : -1, [](int) {});
+    for (int pass = 0; pass < (TWO ? 2 : 1); ++pass) {
+      if (pass) __syncthreads();
+      form_all(0, R0, pass == 1);
+      __syncthreads();
+      first_operands(0);
+#pragma unroll
+      for (int q = 0; q < 4; ++q) products(q, 0, q < 3 ? q + 1 : -1, [](int) {});
+    }
   }
 
   // C layout: lane l, register r -> token 8 (r / 4) + 4 (l / 32) + r % 4, column l % 32
@@ -453,7 +463,8 @@ Split gemmt_split(const Geom& geo, int64_t T, bool workspace) {
 
 template <typename AT, int K>
 int launch_k(const Geom& geo, const void* packed, const uint16_t* dY, int64_t T, int64_t lddy,
-             uint16_t* dX, int64_t lddx, float* part, const Split& s, hipStream_t stream) {
+             uint16_t* dX, int64_t lddx, float* part, const Split& s, bool two,
+             hipStream_t stream) {
   // straight copies to LDS take 16-byte aligned rows at 32-bit offsets
   const bool aligned =
       ((uintptr_t)dY & 15) == 0 && (lddy % 8) == 0 && lddy < (int64_t(1) << 32) / 512;
@@ -467,12 +478,15 @@ int launch_k(const Geom& geo, const void* packed, const uint16_t* dY, int64_t T,
                          TL::kLds, stream, bits, scales, dY, lddy, dX, lddx, part, (int)T, geo.m,
                          geo.n, geo.RB, s.full, s.rest, s.slices);
     };
-    if (s.full == 0) {
-      if (aligned) launch(gemmt_kernel<AT, K, TL, true, true>);
-      else launch(gemmt_kernel<AT, K, TL, false, true>);
+    if (two) {
+      if (aligned) launch(gemmt_kernel<AT, K, TL, true, false, true>);
+      else launch(gemmt_kernel<AT, K, TL, false, false, true>);
+    } else if (s.full == 0) {
+      if (aligned) launch(gemmt_kernel<AT, K, TL, true, true, false>);
+      else launch(gemmt_kernel<AT, K, TL, false, true, false>);
     } else {
-      if (aligned) launch(gemmt_kernel<AT, K, TL, true, false>);
-      else launch(gemmt_kernel<AT, K, TL, false, false>);
+      if (aligned) launch(gemmt_kernel<AT, K, TL, true, false, false>);
+      else launch(gemmt_kernel<AT, K, TL, false, false, false>);
     }
   };
   switch (s.bt) {
@@ -491,14 +505,14 @@ int launch_k(const Geom& geo, const void* packed, const uint16_t* dY, int64_t T,
 
 template <typename AT>
 int launch_t(const Geom& geo, const void* packed, const void* dY, int64_t T, int64_t lddy,
-             void* dX, int64_t lddx, float* part, const Split& s, hipStream_t stream) {
+             void* dX, int64_t lddx, float* part, const Split& s, bool two, hipStream_t stream) {
   const uint16_t* g = reinterpret_cast<const uint16_t*>(dY);
   uint16_t* o = reinterpret_cast<uint16_t*>(dX);
   switch (geo.K) {
-    case 1: return launch_k<AT, 1>(geo, packed, g, T, lddy, o, lddx, part, s, stream);
-    case 2: return launch_k<AT, 2>(geo, packed, g, T, lddy, o, lddx, part, s, stream);
-    case 3: return launch_k<AT, 3>(geo, packed, g, T, lddy, o, lddx, part, s, stream);
-    default: return launch_k<AT, 4>(geo, packed, g, T, lddy, o, lddx, part, s, stream);
+    case 1: return launch_k<AT, 1>(geo, packed, g, T, lddy, o, lddx, part, s, two, stream);
+    case 2: return launch_k<AT, 2>(geo, packed, g, T, lddy, o, lddx, part, s, two, stream);
+    case 3: return launch_k<AT, 3>(geo, packed, g, T, lddy, o, lddx, part, s, two, stream);
+    default: return launch_k<AT, 4>(geo, packed, g, T, lddy, o, lddx, part, s, two, stream);
   }
 }
 
@@ -510,13 +524,14 @@ size_t gemmt_workspace_bytes(const mbok_desc* d, int64_t T) {
 }
 
 int launch_gemmt(const mbok_desc* d, const void* packed, const void* dY, int64_t T, int64_t lddy,
-                 void* dX, int64_t lddx, void* ws, hipStream_t stream) {
+                 void* dX, int64_t lddx, void* ws, int passes, hipStream_t stream) {
   const Geom geo = make_geom(d);
   const Split s = gemmt_split(geo, T, ws != nullptr);
   float* part = reinterpret_cast<float*>(ws);
+  const bool two = passes == 2;
   if (d->alpha_dtype == MBOK_F16)
-    return launch_t<uint16_t>(geo, packed, dY, T, lddy, dX, lddx, part, s, stream);
-  return launch_t<float>(geo, packed, dY, T, lddy, dX, lddx, part, s, stream);
+    return launch_t<uint16_t>(geo, packed, dY, T, lddy, dX, lddx, part, s, two, stream);
+  return launch_t<float>(geo, packed, dY, T, lddy, dX, lddx, part, s, two, stream);
 }
 
 }  // namespace mbok

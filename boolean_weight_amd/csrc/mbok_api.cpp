@@ -243,8 +243,9 @@ int mbok_gemm_precise(const mbok_desc* d, const void* packed, const void* X, int
   return gemm_checked(d, packed, X, x_dtype, T, ldx, Y, ldy, 2, stream);
 }
 
-int mbok_gemmt(const mbok_desc* d, const void* packed, const void* dY, int64_t T, int64_t lddy,
-               void* dX, int64_t lddx, void* workspace, void* stream) {
+static int gemmt_checked(const mbok_desc* d, const void* packed, const void* dY, int64_t T,
+                         int64_t lddy, void* dX, int64_t lddx, void* workspace, int passes,
+                         void* stream) {
   int st = check_desc(d);
   if (st != MBOK_OK) return st;
   if (!packed || !dY || !dX) return MBOK_ERR_INVALID_ARG;
@@ -253,7 +254,18 @@ int mbok_gemmt(const mbok_desc* d, const void* packed, const void* dY, int64_t T
   if (!aligned(packed, 16) || !aligned(dY, 2) || !aligned(dX, 16) || (lddx % 8) != 0 ||
       (workspace && !aligned(workspace, 256)))
     return MBOK_ERR_ALIGN;
-  return mbok::launch_gemmt(d, packed, dY, T, lddy, dX, lddx, workspace, (hipStream_t)stream);
+  return mbok::launch_gemmt(d, packed, dY, T, lddy, dX, lddx, workspace, passes,
+                            (hipStream_t)stream);
+}
+
+int mbok_gemmt(const mbok_desc* d, const void* packed, const void* dY, int64_t T, int64_t lddy,
+               void* dX, int64_t lddx, void* workspace, void* stream) {
+  return gemmt_checked(d, packed, dY, T, lddy, dX, lddx, workspace, 1, stream);
+}
+
+int mbok_gemmt_precise(const mbok_desc* d, const void* packed, const void* dY, int64_t T,
+                       int64_t lddy, void* dX, int64_t lddx, void* workspace, void* stream) {
+  return gemmt_checked(d, packed, dY, T, lddy, dX, lddx, workspace, 2, stream);
 }
 
 size_t mbok_gemmt_workspace_bytes(const mbok_desc* d, int64_t T) {
@@ -304,9 +316,9 @@ int mbok_gated_pack(const mbok_desc* d, const int8_t* signs_gate, const void* al
                                  (hipStream_t)stream);
 }
 
-int mbok_gated(const mbok_desc* d, const void* packed, const void* X, int32_t x_dtype, int64_t T,
-               int64_t ldx, int32_t act, void* H, int64_t ldh, void* pre, int64_t ldpre,
-               void* stream) {
+static int gated_checked(const mbok_desc* d, const void* packed, const void* X, int32_t x_dtype,
+                         int64_t T, int64_t ldx, int32_t act, void* H, int64_t ldh, void* pre,
+                         int64_t ldpre, int passes, void* stream) {
   mbok_desc stacked;
   int st = mbok_gated_stack(d, &stacked);
   if (st != MBOK_OK) return st;
@@ -319,12 +331,26 @@ int mbok_gated(const mbok_desc* d, const void* packed, const void* X, int32_t x_
   if (!aligned(packed, 16) || !aligned(X, 16) || (ldx % 8) != 0 || !aligned(H, 2) ||
       (pre && (!aligned(pre, 16) || (ldpre % 8) != 0)))
     return MBOK_ERR_ALIGN;
-  return mbok::launch_gated(d, packed, X, T, ldx, act, H, ldh, pre, ldpre, (hipStream_t)stream);
+  return mbok::launch_gated(d, packed, X, T, ldx, act, H, ldh, pre, ldpre, passes,
+                            (hipStream_t)stream);
 }
 
-int mbok_gated_backward(const mbok_desc* d, const void* packed, const void* pre, int64_t ldpre,
-                        const void* dH, int64_t lddh, int64_t T, int32_t act, void* dpre,
-                        int64_t lddpre, void* dX, int64_t lddx, void* workspace, void* stream) {
+int mbok_gated(const mbok_desc* d, const void* packed, const void* X, int32_t x_dtype, int64_t T,
+               int64_t ldx, int32_t act, void* H, int64_t ldh, void* pre, int64_t ldpre,
+               void* stream) {
+  return gated_checked(d, packed, X, x_dtype, T, ldx, act, H, ldh, pre, ldpre, 1, stream);
+}
+
+int mbok_gated_precise(const mbok_desc* d, const void* packed, const void* X, int32_t x_dtype,
+                       int64_t T, int64_t ldx, int32_t act, void* H, int64_t ldh, void* pre,
+                       int64_t ldpre, void* stream) {
+  return gated_checked(d, packed, X, x_dtype, T, ldx, act, H, ldh, pre, ldpre, 2, stream);
+}
+
+static int gated_backward_checked(const mbok_desc* d, const void* packed, const void* pre,
+                                  int64_t ldpre, const void* dH, int64_t lddh, int64_t T,
+                                  int32_t act, void* dpre, int64_t lddpre, void* dX, int64_t lddx,
+                                  void* workspace, int passes, void* stream) {
   mbok_desc stacked;
   int st = mbok_gated_stack(d, &stacked);
   if (st != MBOK_OK) return st;
@@ -341,7 +367,22 @@ int mbok_gated_backward(const mbok_desc* d, const void* packed, const void* pre,
       (dX && (!aligned(dX, 16) || (lddx % 8) != 0)) || (workspace && !aligned(workspace, 256)))
     return MBOK_ERR_ALIGN;
   return mbok::launch_gated_backward(d, packed, pre, ldpre, dH, lddh, T, act, dpre, lddpre, dX,
-                                     lddx, workspace, (hipStream_t)stream);
+                                     lddx, workspace, passes, (hipStream_t)stream);
+}
+
+int mbok_gated_backward(const mbok_desc* d, const void* packed, const void* pre, int64_t ldpre,
+                        const void* dH, int64_t lddh, int64_t T, int32_t act, void* dpre,
+                        int64_t lddpre, void* dX, int64_t lddx, void* workspace, void* stream) {
+  return gated_backward_checked(d, packed, pre, ldpre, dH, lddh, T, act, dpre, lddpre, dX, lddx,
+                                workspace, 1, stream);
+}
+
+int mbok_gated_backward_precise(const mbok_desc* d, const void* packed, const void* pre,
+                                int64_t ldpre, const void* dH, int64_t lddh, int64_t T,
+                                int32_t act, void* dpre, int64_t lddpre, void* dX, int64_t lddx,
+                                void* workspace, void* stream) {
+  return gated_backward_checked(d, packed, pre, ldpre, dH, lddh, T, act, dpre, lddpre, dX, lddx,
+                                workspace, 2, stream);
 }
 
 static int check_distill(const mbok_distill_desc* d) {

@@ -57,8 +57,10 @@ int allocate_kernels(int L, const int64_t* sizes, const double* errors, int kmax
 int launch_gemm(const mbok_desc* d, const void* packed, const void* X, int64_t T, int64_t ldx,
                 float* Y, int64_t ldy, int passes, hipStream_t stream);
 
+// passes: 1 = weight levels rounded to bf16; 2 = plus their bf16 residues, here
+// and in the gated block's calls below
 int launch_gemmt(const mbok_desc* d, const void* packed, const void* dY, int64_t T, int64_t lddy,
-                 void* dX, int64_t lddx, void* ws, hipStream_t stream);
+                 void* dX, int64_t lddx, void* ws, int passes, hipStream_t stream);
 size_t gemmt_workspace_bytes(const mbok_desc* d, int64_t T);
 int launch_scale_grad(const mbok_desc* d, const void* packed, const void* dY, int64_t T,
                       int64_t lddy, const void* X, int64_t ldx, float* dalpha, bool accumulate,
@@ -70,21 +72,23 @@ int launch_gated_pack(const mbok_desc* d, const int8_t* signs_gate, const void* 
                       const int8_t* signs_up, const void* alpha_up, void* packed,
                       hipStream_t stream);
 int launch_gated(const mbok_desc* d, const void* packed, const void* X, int64_t T, int64_t ldx,
-                 int act, void* H, int64_t ldh, void* pre, int64_t ldpre, hipStream_t stream);
+                 int act, void* H, int64_t ldh, void* pre, int64_t ldpre, int passes,
+                 hipStream_t stream);
 // the block's kernels, on the stacked layer (mbok_gated.h)
 struct GatedOut;
 int launch_gated_stacked(const mbok_desc* d, const void* packed, const void* X, int64_t T,
-                         int64_t ldx, const GatedOut& out, hipStream_t stream);
+                         int64_t ldx, const GatedOut& out, int passes, hipStream_t stream);
 int launch_gated_f4(const mbok_desc* d, const void* packed, const void* X, int64_t T, int64_t ldx,
                     const GatedOut& out, hipStream_t stream);
 int gated_f4_max_tokens();
 int launch_gated_skinny(const mbok_desc* d, const void* packed, const void* X, int64_t T,
                         int64_t ldx, const GatedOut& out, hipStream_t stream);
 int launch_gated_mfma(const mbok_desc* d, const void* packed, const void* X, int64_t T,
-                      int64_t ldx, const GatedOut& out, hipStream_t stream);
+                      int64_t ldx, const GatedOut& out, int passes, hipStream_t stream);
 int launch_gated_backward(const mbok_desc* d, const void* packed, const void* pre, int64_t ldpre,
                           const void* dH, int64_t lddh, int64_t T, int act, void* dpre,
-                          int64_t lddpre, void* dX, int64_t lddx, void* ws, hipStream_t stream);
+                          int64_t lddpre, void* dX, int64_t lddx, void* ws, int passes,
+                          hipStream_t stream);
 // the caller's arrays of one distillation call (dZ, stats, dloss may be null)
 struct DistillArgs {
   const void* Z;

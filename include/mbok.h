@@ -532,6 +532,14 @@ int mbok_gemm_precise(const mbok_desc* d, const void* packed, const void* X,
 int mbok_gemmt(const mbok_desc* d, const void* packed, const void* dY, int64_t T,
                int64_t lddy, void* dX, int64_t lddx, void* workspace, void* stream);
 
+/*
+ * mbok_gemmt with each W_hat value carried as two bf16 terms (hi = bf16(v), lo
+ * = bf16(v - hi), off by at most 2^-16 |v|), as mbok_gemm_precise is to
+ * mbok_gemm: twice the matrix work.  Same arguments, workspace and errors.
+ */
+int mbok_gemmt_precise(const mbok_desc* d, const void* packed, const void* dY, int64_t T,
+                       int64_t lddy, void* dX, int64_t lddx, void* workspace, void* stream);
+
 /* Bytes of the workspace mbok_gemmt uses for this layer and T rows (0 when it
  * needs none).  Host only; 0 for a NULL or invalid descriptor or T. */
 size_t mbok_gemmt_workspace_bytes(const mbok_desc* d, int64_t T);
@@ -633,6 +641,15 @@ int mbok_gated(const mbok_desc* d, const void* packed, const void* X, int32_t x_
                int64_t ldpre, void* stream);
 
 /*
+ * mbok_gated with each weight carried as two bf16 terms for T > 16 (see
+ * mbok_gemmt_precise), so that no token count rounds the weights; for T <= 16
+ * the same kernels.  Same arguments and errors.
+ */
+int mbok_gated_precise(const mbok_desc* d, const void* packed, const void* X, int32_t x_dtype,
+                       int64_t T, int64_t ldx, int32_t act, void* H, int64_t ldh, void* pre,
+                       int64_t ldpre, void* stream);
+
+/*
  * Backward of the gated block.  With g, u from pre and s = dH:
  *     dg = s u act'(g),  du = s act(g)      (fp32, rounded once to bf16)
  *     dX = dg Wg + du Wu                    (mbok_gemmt of the stacked layer)
@@ -653,6 +670,15 @@ int mbok_gated_backward(const mbok_desc* d, const void* packed, const void* pre,
                         int64_t ldpre, const void* dH, int64_t lddh, int64_t T, int32_t act,
                         void* dpre, int64_t lddpre, void* dX, int64_t lddx, void* workspace,
                         void* stream);
+
+/*
+ * mbok_gated_backward with dX by mbok_gemmt_precise (dpre is the same: rounded
+ * once to bf16).  Same arguments, workspace and errors.
+ */
+int mbok_gated_backward_precise(const mbok_desc* d, const void* packed, const void* pre,
+                                int64_t ldpre, const void* dH, int64_t lddh, int64_t T,
+                                int32_t act, void* dpre, int64_t lddpre, void* dX, int64_t lddx,
+                                void* workspace, void* stream);
 
 /* Largest number of listed teacher entries and largest vocabulary of
  * mbok_distill, its most rows, and floats of statistics per row. */

@@ -7,7 +7,7 @@ import sys
 
 from test_abi_sanitized import HERE, ROOT, _env, sanitized  # noqa: F401  (a fixture)
 
-FILES = ["test_finetune_cpu.py", "test_distill_desc_cpu.py"]
+FILES = ["test_finetune_cpu.py", "test_distill_desc_cpu.py", "test_finetune_precise_cpu.py"]
 
 
 def test_refusals_pass_under_sanitizers(sanitized):  # noqa: F811
