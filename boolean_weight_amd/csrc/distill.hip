@@ -9,10 +9,10 @@
 // where p is the softmax of the listed l / tau (then p_r = 0 and s = 1), or
 // with t_lse exp(l / tau - t_lse) and p_r = 1 - sum p the mass of what is not
 // listed; s = sum p + p_r is 1 as well unless p_r is cut off at 0 (an index
-// listed twice, a t_lse that is too small) or its class drops out.  What is
-// not listed may lie far below the largest logit, so its sum R is taken
-// relative to its own largest logit zu: log q_r keeps its digits at any
-// distance, and the factor of exp((z_v - zu) / tau),
+// listed twice, a t_lse that is too small) or its class drops out.  Where what
+// is not listed lies far below the largest logit, its sum R is taken relative
+// to its own largest logit zu: log q_r keeps its digits at any distance, and
+// the factor of exp((z_v - zu) / tau) in dz_v,
 //     s exp((zu - zmax) / tau) / S - p_r / R,
 // stays below s + p_r where p_r / q_r overflows.
 //
@@ -229,7 +229,9 @@ struct GradScale {
   }
 };
 
-template <typename ZT, typename OT, int NV, bool GRAD>
+// REST: with t_lse (one kernel for both: 512 x 128256 bf16 logits without, 136
+// against 127 us)
+template <typename ZT, typename OT, int NV, bool GRAD, bool REST>
 __global__ void __launch_bounds__(kMaxThreads) distill_kernel(
     const ZT* Z, int64_t ldz, const void* __restrict__ t_logits, int t_dtype,
     const int32_t* __restrict__ t_index, int64_t ldt, const float* __restrict__ t_lse,
@@ -237,7 +239,7 @@ __global__ void __launch_bounds__(kMaxThreads) distill_kernel(
     RowStats* __restrict__ stats, OT* dZ, int64_t lddz) {
   constexpr int N = Vec<ZT>::N;
   extern __shared__ __attribute__((aligned(16))) uint32_t smem[];
-  __shared__ float red_f[2 * kMaxThreads / kWave];
+  __shared__ float red_f[kMaxThreads / kWave];
   __shared__ double red_d[2 * kMaxThreads / kWave];
   __shared__ RowStats sh;
   __shared__ int twice_any;
@@ -295,139 +297,131 @@ __global__ void __launch_bounds__(kMaxThreads) distill_kernel(
     zl[j] = v < 0 ? 0.f : to_f32(row[v]);
   }
 
-  bool twice = false;
-  auto mark = [&] {
-    for (int j = tid; j < r.top; j += nt)
-      if (s.idx[j] >= 0) twice |= mark_entry(s.bits, s.idx[j]);
-    if (twice) twice_any = 1;
-  };
   auto listed_at = [&](int v) { return s.bits[(v * N) >> 5] >> ((v * N) & 31); };
-  // largest logit mx (a NaN is dropped here: it makes the sums below NaN), and
-  // zu, from which the main passes count: the largest one, or, with t_lse, the
-  // largest of what is not listed (0 if that is -inf)
-  const bool rest = t_lse != nullptr;
-  float mx = -INFINITY, zu = -INFINITY;
-  if (rest) {
-    __syncthreads();  // lists and cleared bits are in LDS
-    mark();
-    __syncthreads();
-    each([&](int v, const Vec<ZT>& x) {
-      const uint32_t m = listed_at(v);
+  // largest logit (a NaN is dropped here: it makes the sum below NaN)
+  float mx = -INFINITY;
+  each([&](int, const Vec<ZT>& x) {
 #pragma unroll
-      for (int e = 0; e < N; ++e) zu = fmaxf(zu, (m >> e) & 1u ? -INFINITY : to_f32(x.v[e]));
-    });
-    for (int j = tid; j < r.top; j += nt)
-      if (s.idx[j] >= 0) mx = fmaxf(mx, zl[j]);
-    zu = wave_max(zu);
-    mx = wave_max(mx);
-    if (lane == 0) red_f[2 * wave] = zu, red_f[2 * wave + 1] = mx;
-    __syncthreads();
-    for (int i = 0; i < nw; ++i) {
-      zu = fmaxf(zu, red_f[2 * i]);
-      mx = fmaxf(mx, red_f[2 * i + 1]);
-    }
-    mx = fmaxf(mx, zu);
-    if (!(zu > -INFINITY)) zu = 0.f;
-  } else {
-    each([&](int, const Vec<ZT>& x) {
-#pragma unroll
-      for (int e = 0; e < N; ++e) mx = fmaxf(mx, to_f32(x.v[e]));
-    });
-    mx = wave_max(mx);
-    if (lane == 0) red_f[wave] = mx;
-    __syncthreads();  // also: lists and cleared bits are in LDS
-    mx = red_f[0];
-    for (int i = 1; i < nw; ++i) mx = fmaxf(mx, red_f[i]);
-    zu = mx;
-    mark();
-    __syncthreads();
-  }
+    for (int e = 0; e < N; ++e) mx = fmaxf(mx, to_f32(x.v[e]));
+  });
+  mx = wave_max(mx);
+  if (lane == 0) red_f[wave] = mx;
+  __syncthreads();  // also: lists and cleared bits are in LDS
+  mx = red_f[0];
+  for (int i = 1; i < nw; ++i) mx = fmaxf(mx, red_f[i]);
 
-  // Sums of exponentials: all, or (with t_lse) the unlisted ones and apart from
-  // them the listed ones, each index once.  The scaled argument (z - zu) c is
-  // one fma, z c - k with k = zu c rounded, where k is small (2^klo then
-  // corrects the sum for that rounding, |klo| <= 2^-17: to first order), else
-  // subtracted first.  That c is log2(e) / tau rounded (2^-24 relative at most)
-  // moves log sum by at most 2^-24 E_q[(max - z) / tau] <= 2^-24 log V, since
-  // that mean is the entropy of q less log sum.  (Carrying it exactly cost
-  // two instructions per logit, the subtraction one: 2048 x 32000 bf16 with
-  // gradient 76.5 -> 74.1 us.)
+  bool twice = false;
+  for (int j = tid; j < r.top; j += nt)
+    if (s.idx[j] >= 0) twice |= mark_entry(s.bits, s.idx[j]);
+  if (twice) twice_any = 1;
+  __syncthreads();
+
+  // Sums of exponentials: all, and (with t_lse) the unlisted ones.  The scaled
+  // argument (z - max) c is one fma, z c - k with k = max c rounded, where k is
+  // small (2^klo then corrects the sums for that rounding, |klo| <= 2^-17: to
+  // first order), else subtracted first.  That c is log2(e) / tau rounded
+  // (2^-24 relative at most) moves log sum by at most 2^-24 E_q[(max - z) / tau]
+  // <= 2^-24 log V, since that mean is the entropy of q less log sum.  (Carrying
+  // it exactly cost two instructions per logit, the subtraction one: 2048 x
+  // 32000 bf16 with gradient 76.5 -> 74.1 us.)
   // A thread adds at most 128 terms in fp32: a row that is read again adds each
-  // vector's sum in float64.
-  float sum_z = 0.f;
-  double sum_far = 0.0;
+  // vector's sums in float64.
+  float sum_z = 0.f, sum_r = 0.f;
+  double far_z = 0.0, far_r = 0.0;
   auto next_vector = [&] {
     if (NV > 0) return;
-    sum_far += (double)sum_z;
-    sum_z = 0.f;
+    far_z += (double)sum_z;
+    far_r += (double)sum_r;
+    sum_z = sum_r = 0.f;
   };
-  const float k = zu * r.c_hi;
+  const float k = mx * r.c_hi;
   const bool near = fabsf(k) < 256.f;
   auto sum = [&](auto near_c) {
     auto ex = [&](ZT z) {
       return __builtin_amdgcn_exp2f(decltype(near_c)::value ? fmaf(to_f32(z), r.c_hi, -k)
-                                                            : (to_f32(z) - zu) * r.c_hi);
+                                                            : (to_f32(z) - mx) * r.c_hi);
     };
-    if (rest) {
-      each([&](int v, const Vec<ZT>& x) {
-        const uint32_t m = listed_at(v);
+    each([&](int v, const Vec<ZT>& x) {
+      const uint32_t m = REST ? listed_at(v) : 0u;
 #pragma unroll
-        for (int e = 0; e < N; ++e) {
-          const float y = ex(x.v[e]);
-          sum_z += (m >> e) & 1u ? 0.f : y;
-        }
-        next_vector();
-      });
-    } else {
-      each([&](int, const Vec<ZT>& x) {
-#pragma unroll
-        for (int e = 0; e < N; ++e) sum_z += ex(x.v[e]);
-        next_vector();
-      });
-    }
+      for (int e = 0; e < N; ++e) {
+        const float y = ex(x.v[e]);
+        sum_z += y;
+        if (REST) sum_r += (m >> e) & 1u ? 0.f : y;
+      }
+      next_vector();
+    });
   };
   if (near) sum(std::true_type{});
   else sum(std::false_type{});
   {
     const double fix =
-        near ? 1.0 - (double)kLn2 * ((double)zu * (double)r.c_hi - (double)k) : 1.0;
-    const double dz = wave_sum((double)sum_z + sum_far) * fix;
-    double dl = 0.0;
-    if (rest) {
-      const double inv_tau = 1.0 / (double)r.tau;
-      for (int j = tid; j < r.top; j += nt) {
-        const int v = s.idx[j];
-        bool first = v >= 0;
-        if (twice_any)
-          for (int i = 0; i < j; ++i) first &= s.idx[i] != v;
-        if (first) dl += (double)exp_fine(((double)zl[j] - (double)mx) * inv_tau);
-      }
-      dl = wave_sum(dl);
-    }
+        near ? 1.0 - (double)kLn2 * ((double)mx * (double)r.c_hi - (double)k) : 1.0;
+    const double dz = wave_sum((double)sum_z + far_z) * fix;
+    const double dr = REST ? wave_sum((double)sum_r + far_r) * fix : 0.0;
     if (lane == 0) {
       red_d[2 * wave] = dz;
-      red_d[2 * wave + 1] = dl;
+      red_d[2 * wave + 1] = dr;
     }
   }
   __syncthreads();
 
+  // What is not listed has next to nothing relative to the largest logit: its sum
+  // again, relative to its own largest (0 if that is -inf).  Below 2^-30, so
+  // that what the first sum and the gradient flush, exponentials below 2^-126,
+  // is less than 2^-96 of the rest.  (Taking the unlisted maximum of every row
+  // instead: 512 x 128256 bf16 139 -> 169 us.)
+  float zu = mx;
+  if (REST) {
+    double R = 0.0;
+    for (int i = 0; i < nw; ++i) R += red_d[2 * i + 1];
+    if (R < 0x1p-30) {
+      zu = -INFINITY;
+      for (int v = tid; v < nvec; v += nt) {
+        const Vec<ZT> x = load_vec(row, v, r.V);
+        const uint32_t m = listed_at(v);
+#pragma unroll
+        for (int e = 0; e < N; ++e) zu = fmaxf(zu, (m >> e) & 1u ? -INFINITY : to_f32(x.v[e]));
+      }
+      zu = wave_max(zu);
+      if (lane == 0) red_f[wave] = zu;
+      __syncthreads();  // also: every thread has its R
+      zu = red_f[0];
+      for (int i = 1; i < nw; ++i) zu = fmaxf(zu, red_f[i]);
+      if (!(zu > -INFINITY)) zu = 0.f;
+      double far = 0.0;
+      for (int v = tid; v < nvec; v += nt) {
+        const Vec<ZT> x = load_vec(row, v, r.V);
+        const uint32_t m = listed_at(v);
+        float part = 0.f;
+#pragma unroll
+        for (int e = 0; e < N; ++e)
+          part += (m >> e) & 1u ? 0.f
+                                : __builtin_amdgcn_exp2f((to_f32(x.v[e]) - zu) * r.c_hi);
+        far += (double)part;
+      }
+      far = wave_sum(far);
+      if (lane == 0) red_d[2 * wave + 1] = far;
+      __syncthreads();
+    }
+  }
+
   // the first wavefront: teacher, loss, statistics
   if (wave == 0) {
-    // R: the sum of the main pass, relative to zu; S: the whole row's, to zmax
-    double S = 0.0, R = 0.0, up = 1.0;
+    // S: the row's sum, relative to zmax; R: the unlisted part's, relative to zu
+    double S = 0.0, R = 0.0;
     for (int i = 0; i < nw; ++i) {
-      R += red_d[2 * i];
-      S += red_d[2 * i + 1];
+      S += red_d[2 * i];
+      R += red_d[2 * i + 1];
     }
     const double inv_tau = 1.0 / (double)r.tau;
-    if (rest) up = R != 0.0 ? exp(((double)zu - (double)mx) * inv_tau) : 0.0;
-    S += R * up;
-    if (!(mx > -INFINITY)) S = __builtin_nan("");  // only -inf
+    const double up =
+        zu == mx ? 1.0 : R > 0.0 ? exp(((double)zu - (double)mx) * inv_tau) : 0.0;
     RowStats st = {};
     st.zmax = mx;
     st.zu = zu;
     double log_n, shift, Nsum = 1.0;  // log p_j = (l_j - shift) / tau - log_n
-    if (rest) {
+    if (REST) {
       shift = 0.0;
       log_n = (double)t_lse[t];
       st.inv_n = 1.f;
@@ -456,7 +450,7 @@ __global__ void __launch_bounds__(kMaxThreads) distill_kernel(
         const float l = s.p[j];
         double p;
         double log_p = 0.0;
-        if (rest) {
+        if (REST) {
           log_p = (double)l * inv_tau - log_n;
           p = (double)exp_fine(log_p);
         } else {
@@ -475,8 +469,8 @@ __global__ void __launch_bounds__(kMaxThreads) distill_kernel(
       for (int j = lane; j < r.top; j += kWave) s.p[j] = 0.f;
     }
     if (S != S) kl = S;
-    double mass = rest ? psum : Nsum == Nsum ? 1.0 : Nsum, take = 0.0;
-    const double pr = rest ? fmax(0.0, 1.0 - psum) : 0.0;
+    double mass = REST ? psum : Nsum == Nsum ? 1.0 : Nsum, take = 0.0;
+    const double pr = REST ? fmax(0.0, 1.0 - psum) : 0.0;
     if (pr > 0.0 && R > 0.0) {
       kl += pr * (log(pr) - (((double)zu - (double)mx) * inv_tau + log(R) - log_s));
       mass += pr;
@@ -598,16 +592,20 @@ int launch_rows(const mbok_distill_desc* d, const DistillArgs& a, float* loss, f
                        a.ldt, a.t_lse, a.weight, r, loss, reinterpret_cast<RowStats*>(stats),
                        reinterpret_cast<OT*>(a.dZ), a.lddz);
   };
-  auto by_nv = [&](auto grad) {
-    constexpr bool G = decltype(grad)::value;
-    if (per <= 2) go(distill_kernel<ZT, OT, 2, G>);
-    else if (per <= 4) go(distill_kernel<ZT, OT, 4, G>);
-    else if (per <= 8) go(distill_kernel<ZT, OT, 8, G>);
-    else if (per <= 16) go(distill_kernel<ZT, OT, 16, G>);
-    else go(distill_kernel<ZT, OT, 0, G>);
+  auto by_nv = [&](auto grad, auto rest) {
+    constexpr bool G = decltype(grad)::value, R = decltype(rest)::value;
+    if (per <= 2) go(distill_kernel<ZT, OT, 2, G, R>);
+    else if (per <= 4) go(distill_kernel<ZT, OT, 4, G, R>);
+    else if (per <= 8) go(distill_kernel<ZT, OT, 8, G, R>);
+    else if (per <= 16) go(distill_kernel<ZT, OT, 16, G, R>);
+    else go(distill_kernel<ZT, OT, 0, G, R>);
   };
-  if (a.dZ) by_nv(std::true_type{});
-  else by_nv(std::false_type{});
+  auto by_rest = [&](auto grad) {
+    if (a.t_lse) by_nv(grad, std::true_type{});
+    else by_nv(grad, std::false_type{});
+  };
+  if (a.dZ) by_rest(std::true_type{});
+  else by_rest(std::false_type{});
   return hipGetLastError() == hipSuccess ? MBOK_OK : MBOK_ERR_HIP;
 }
 

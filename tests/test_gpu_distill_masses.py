@@ -250,3 +250,30 @@ def test_small_terms_beside_a_large_one(V, z):
     for lse in (None, torch.zeros(1)):
         loss, _ = run(Z, l, idx, 1.0, lse)
         assert abs(float(loss) - want) <= 2.0 ** -17 + 2.0 ** -23 + 13.2 * 2.0 ** -24 + 2.0 ** -20
+
+
+@pytest.mark.parametrize("shift", [-5.0e4, -300.0, 0.0, 2.0e4])
+def test_unlisted_masked_far_from_zero(shift):
+    """Nothing unlisted is left and the listed logits lie anywhere: no factor of
+    what is not there gets into the row."""
+    for z, grad in (("f32", "f32"), ("f32", "bf16"), ("bf16", "bf16")):
+        say(f"distill unlisted masked at {shift} {z}->{grad}")
+        Z, l, idx, teacher = inputs(3, 300, 6, 25, "f32")
+        Z = (Z + shift).to(TYPES[z])
+        for t in range(3):
+            free = torch.ones(300, dtype=torch.bool)
+            free[idx[t]] = False
+            Z[t, free] = -math.inf
+        check(Z, l, idx, 1.0, torch.logsumexp(teacher, -1), grad=TYPES[grad])
+        check(Z, l, idx, 0.25, torch.logsumexp(teacher * 4, -1) - 0.5, grad=TYPES[grad])
+
+
+@pytest.mark.parametrize("gap", [15.0, 20.0, 20.8, 25.0, 30.0])
+def test_rest_around_the_second_sum(gap):
+    """On both sides of the unlisted share from which its sum is taken again."""
+    for z, grad, V in (("f32", "f32", 1000), ("bf16", "bf16", 33001), ("f32", "bf16", 140003)):
+        say(f"distill gap={gap} V={V} {z}->{grad}")
+        Z, l, idx, _ = inputs(4, V, 12, 19, "f32", scale=1.0)
+        Z = (Z + torch.zeros(4, V).scatter_(1, idx, gap + math.log(V))).to(TYPES[z])
+        lse = torch.logsumexp(l, -1) - math.log(0.95)
+        check(Z, l, idx, 1.0, lse, torch.full((4,), 100.0), TYPES[grad])
