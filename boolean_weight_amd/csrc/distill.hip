@@ -20,11 +20,15 @@
 // workgroup takes one row and keeps it in registers as loaded (NV 16-byte
 // vectors per thread), so the maximum, the sum of exponentials and the
 // gradient cost one read (2048 rows of 32000 bf16 logits with the gradient:
-// 74 us, 3.5 TB/s read and written, against 53 us for a copy; what is left are
-// ~12 vector instructions per logit).  Rows of more than 16 vectors for each of 1024
-// threads (131072 16-bit logits) are read again for each pass.  Rows start
-// at any element: the 16-byte accesses need no alignment on this part, and
-// the last, partial vector of a row goes element by element.
+// 74 us, 3.5 TB/s read and written, against 53 us for a copy).  What is left:
+// ~12 vector instructions per logit, and 118 registers with 8 vectors, so two
+// rows per compute unit to hide one's arithmetic behind the other's traffic.
+// 16 vectors of 16-bit logits (vocabularies of 65537 to 131072) do not all fit
+// with what else is live: 55 to 60 registers go through scratch memory (512 x
+// 128256 with the gradient 127 us, 2.1 TB/s).  Rows of more than 16 vectors for
+// each of 1024 threads are read again for each pass (512 x 262144 186 us).
+// Rows start at any element: the 16-byte accesses need no alignment on this
+// part, and the last, partial vector of a row goes element by element.
 //
 // Membership of a token in the list is one bit per token in LDS.  The main
 // pass writes every dz_v as if v had no p_j; after a barrier the threads of
@@ -568,8 +572,8 @@ size_t row_lds_bytes(const mbok_distill_desc* d) {
   return ((size_t)d->top * 3 + ((size_t)d->vocab + 31) / 32) * 4;
 }
 
-// Threads of a row's workgroup for `want` vectors each; a launch has fewer than
-// 2^32 threads (256 for each of MBOK_MAX_DISTILL_ROWS rows are 2^31).
+// Threads of a row's workgroup for `want` vectors each, 256 to 1024; a launch has
+// fewer than 2^32 threads (256 for each of MBOK_MAX_DISTILL_ROWS rows are 2^31).
 int row_threads(int64_t T, int nvec, int want) {
   int threads = 256;
   while (threads < kMaxThreads && threads * want < nvec && T * threads * 2 <= UINT32_MAX)
@@ -583,7 +587,12 @@ int launch_rows(const mbok_distill_desc* d, const DistillArgs& a, float* loss, f
   const int nvec = (d->vocab + Vec<ZT>::N - 1) / Vec<ZT>::N;
   const size_t lds = row_lds_bytes(d);
   const DistillRow r = row_of(d);
-  // 8 vectors per thread; with few rows, where latency counts, 2
+  // 8 vectors per thread; with few rows, where latency counts, 2 (step, us, for 2
+  // / 8: 32000 bf16 logits 1 row 9.6 / 10.0, 128 rows 11.1 / 11.8, 256 rows 12.6
+  // / 13.5, 512 rows 23.5 / 17.7, 2048 rows 97.9 / 75.5; 12345 fp32 logits 256
+  // rows 10.6 / 10.2, 512 rows 19.9 / 14.1; 4000 bf16 logits the same for both).
+  // From 257 rows to 511, past one row per compute unit, 8 is the faster one
+  // too (384 rows 21.9 / 16.8, fp32 18.3 / 12.8).
   const int threads = row_threads(a.T, nvec, a.T < 512 ? 2 : 8);
   const int per = (nvec + threads - 1) / threads;
   auto go = [&](auto kernel) {
@@ -613,6 +622,9 @@ template <typename ZT, typename OT>
 int launch_rows_backward(const mbok_distill_desc* d, const DistillArgs& a, const float* stats,
                          const float* dloss, hipStream_t stream) {
   const int nvec = (d->vocab + Vec<ZT>::N - 1) / Vec<ZT>::N;
+  // 4 vectors per thread: of 2, 4 and 8 the loss and gradient calls together
+  // take 95.6, 95.4 and 97.2 us for 2048 x 32000 bf16, 23.8, 23.6 and 24.1 for
+  // 512 rows, 20.2, 19.5 and 19.8 for 512 x 12345 fp32
   const int threads = row_threads(a.T, nvec, 4);
   hipLaunchKernelGGL((distill_backward_kernel<ZT, OT>), dim3((unsigned)a.T), dim3(threads),
                      row_lds_bytes(d), stream, reinterpret_cast<const ZT*>(a.Z), a.ldz,

@@ -64,7 +64,8 @@ struct Tile {
 
 // TWO: each 64 columns are two steps with the same activations, the levels
 // rounded to bf16 and then the bf16 rounding of what that left (16 significant
-// bits together): twice the matrix work.
+// bits together): twice the matrix work (11008 x 4096, 2048 tokens with the
+// pre-activations 607 us, 64 tokens 76 us).
 template <typename AT, int K, typename P, bool TWO>
 __device__ __forceinline__ void gated_tile(const uint32_t* __restrict__ bits,
                                            const AT* __restrict__ scales,

@@ -645,10 +645,13 @@ TokenKernel token_kernel(const mbok_desc* d, int64_t T) {
 // The gated block's kernel (d: the stacked layer) by the same rule, except that
 // its one-token form is always the matrix-core decode kernel, and that 7 and 8
 // tokens, the rest of the octet one product holds, stay on the per-group form
-// where the layer has at least 2^27 sign bits (measured, us, per-group form
-// against bf16 +-1: two 11008x4096, K = 3 13.9 / 20.0 at 8 tokens; two
-// 13824x5120, K = 3 19.5 / 34.4; two 4096x4096, K = 2 8.8 / 7.7; its two-octet
-// form for 16 tokens 21.9 / 21.8).
+// where the layer has at least 2^27 sign bits (8 tokens, us, per-group form
+// against bf16 +-1, two projections: 4096x4096, K = 2 (2^26 bits) 9.1 / 7.7;
+// 11008x4096, K = 1 (2^26.4) 10.4 / 9.8; 4096x4096, K = 3 (2^26.6) 9.7 / 9.2;
+// 5120x5120, K = 2 (2^26.6) 11.7 / 14.6; 4096x4096, K = 4 (2^27) 10.3 / 11.4;
+// 5504x4096, K = 3 (2^27) 11.0 / 11.9; 6912x5120, K = 2 (2^27.1) 12.7 / 21.0;
+// 11008x4096, K = 2 (2^27.4) 12.1 / 15.2, K = 3 14.2 / 20.2; 13824x5120, K = 3
+// 19.4 / 34.6; 7 tokens alike).  Its two-octet form for 16 tokens 21.9 / 21.8.
 int launch_gated_stacked(const mbok_desc* d, const void* packed, const void* X, int64_t T,
                          int64_t ldx, const GatedOut& out, int passes, hipStream_t stream) {
   if (T > skinny_max_tokens()) return launch_gated_mfma(d, packed, X, T, ldx, out, passes, stream);

@@ -21,7 +21,9 @@
 // steps of a slice, one LDS round trip each (5120 x 5120, 16 tokens: 12.7 us
 // against 1.8 us of reading).  256 columns because a weight is then formed once
 // per 256 tokens; the tokens of a tile by tile_tokens, the slices by
-// gemmt_split.
+// gemmt_split.  dY rows that are not 16-byte aligned go by way of registers, of
+// which 9 to 30 of a 256-token tile then go through scratch memory (4001 rows x
+// 4096 columns, 2048 tokens: 96 us, 4000 rows 81 us, without the joining).
 //
 // Rows past m have zero weights, and dY is read inside its m columns only: a
 // partial last row block is a step of its own with element-wise loads.
@@ -74,7 +76,7 @@ __device__ __forceinline__ bf16x8 read_tr(const uint16_t* p, const uint16_t* p4)
 // SLICED: every tile is (full = 0), which leaves the other epilogue out.
 // TWO: each row block is two steps, W_hat's levels rounded to bf16 and then the
 // bf16 rounding of what that left (16 significant bits together), with the same
-// dY tile: twice the matrix work.
+// dY tile: twice the matrix work (4096 x 11008, 2048 tokens 310 us).
 template <typename AT, int K, typename TL, bool ALIGNED, bool SLICED, bool TWO>
 __global__ void __launch_bounds__(kThreads) gemmt_kernel(
     const uint32_t* __restrict__ bits, const AT* __restrict__ scales,
@@ -427,7 +429,12 @@ __global__ void __launch_bounds__(256) gemmt_reduce_kernel(const float* __restri
 constexpr int kUnits = 256;  // workgroups that fill the part (one per compute unit)
 
 // Tokens per tile: as many as there are, up to 256, but fewer where tiles and
-// slices of at least four steps would leave most compute units idle.
+// slices of at least four steps would leave most compute units idle: below 96
+// workgroups (K = 3, us, never fewer / as it is: 2048 tokens of 256 x 512 17.4 /
+// 14.5, 512 of 512 x 512 13.9 / 10.5, 796 of 34 x 512 8.6 / 6.5, 300 of 640 x
+// 1024 15.3 / 11.4).  Limits of 64 and 128 are within 1 us of it there; one of
+// 192 is faster where 96 to 191 workgroups are left (257 tokens of 2048 x 2048
+// 27.2 against 22.2, 200 of 1024 x 4096 24.0 against 18.1).
 int tile_tokens(const Geom& geo, int64_t T) {
   const int64_t cols = (geo.n + kBN - 1) / kBN, most = geo.RB < 8 ? 1 : geo.RB / 4;
   int bt = T <= 32 ? 32 : T <= 64 ? 64 : T <= 128 ? 128 : 256;

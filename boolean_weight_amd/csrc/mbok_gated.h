@@ -34,7 +34,8 @@ template <bool DERIV>
 __device__ __forceinline__ float activation(int act, float g, float& deriv) {
   if (act == MBOK_ACT_SILU) {
     const float s = sigmoid(g);
-    // g (1 - s) is 0 at +inf's limit; s is exactly 0 for very negative g
+    // s is exactly 1 for large g and exactly 0 for very negative g; infinite g
+    // gives NaN (infinity times 0), as the formula does
     if (DERIV) deriv = s * fmaf(g, 1.f - s, 1.f);
     return g * s;
   }

@@ -47,6 +47,9 @@ __device__ __forceinline__ u32x4 load_piece(const uint16_t* p, int live, bool ba
 // transposing LDS read of any buffer, i.e. at once.)  The wait counts the
 // compiler inserts for its own loads stay right: loads return in order, so
 // an uncounted copy in flight only makes a wait longer.
+// m0 is the statement's alone: it is reserved, so the compiler takes no clobber
+// of it, and nothing else in the kernels that use this writes or reads it (LDS
+// accesses need none on this part).
 // The source is base (the wavefront's) + off bytes (the lane's).
 __device__ __forceinline__ void copy_to_lds(const void* base, uint32_t off, const uint16_t* dst) {
   const uint32_t at =

@@ -41,7 +41,8 @@
  *    error return means nothing was launched and no output was touched.
  *    MBOK_ERR_HIP is returned when a launch itself fails (hipGetLastError).
  *  - Results are deterministic: the same inputs give the same output bits
- *    (no atomics, fixed reduction order).
+ *    (fixed reduction order; no atomics but mbok_distill's, which set bits in
+ *    LDS and so come out the same in any order).
  *
  * Packed layout MBOK_LAYOUT_L64 (what mbok_pack writes and mbok_gemv /
  * mbok_gemm read)
@@ -723,7 +724,8 @@ int mbok_distill_desc_init(mbok_distill_desc* d, int32_t vocab, int32_t top,
  * or +inf among a row's logits or its listed teacher logits, and rows of only
  * -inf, give NaN (the loss and the row's gradient).
  * Row maxima, sums and logarithms are at least fp32 (the sums of a row and
- * the loss in float64 at the end).
+ * the loss in float64 at the end).  Gradient terms below 2^-90 w tau may be
+ * written as 0.
  *  Z        device [T, ldz] of z_dtype (MBOK_F32, MBOK_F16, MBOK_BF16).
  *  T        1 .. MBOK_MAX_DISTILL_ROWS.
  *  t_logits device [T, ldt] of t_dtype (any of the three), l.
