@@ -373,7 +373,8 @@ __global__ void __launch_bounds__(kMaxThreads) distill_kernel(
   // What is not listed has next to nothing relative to the largest logit: its sum
   // again, relative to its own largest (0 if that is -inf).  Below 2^-30, so
   // that what the first sum and the gradient flush, exponentials below 2^-126,
-  // is less than 2^-96 of the rest.  (Taking the unlisted maximum of every row
+  // is less than 2^-96 of the rest.  (2048 x 32000 bf16 78 us, 114 when every row
+  // is read again.  Taking the unlisted maximum of every row in the first pass
   // instead: 512 x 128256 bf16 139 -> 169 us.)
   float zu = mx;
   if (REST) {
