@@ -33,11 +33,18 @@ __all__ = [
     "mbok_gated_backward_precise", "mbok_distill_desc",
     "mbok_distill_desc_init", "mbok_distill", "mbok_distill_backward", "MBOK_MAX_TOP",
     "MBOK_MAX_VOCAB", "MBOK_MAX_DISTILL_ROWS", "MBOK_DISTILL_STATS",
+    "MBOK_ACT_NONE", "mbok_linear", "mbok_linear_precise", "mbok_linear_backward",
+    "mbok_linear_backward_precise", "mbok_linear_backward_workspace_bytes",
+    "mbok_logp_desc", "mbok_logp_desc_init", "mbok_logp", "mbok_logp_backward",
+    "MBOK_LOGP_STATS", "mbok_policy_desc", "mbok_policy_desc_init", "mbok_policy",
+    "mbok_preference_desc", "mbok_preference_desc_init", "mbok_preference", "MBOK_MAX_PAIRS",
+    "MBOK_E4M3", "MBOK_ADAMW_BLOCK", "MBOK_MAX_ADAMW_TENSORS", "mbok_adamw_plan",
+    "mbok_adamw_plan_init", "mbok_adamw",
     "mbok_version", "workspace_for",
     "alpha_torch_dtype", "quantize_and_pack", "allocate_for_budget",
 ]
 
-MBOK_F32, MBOK_F16, MBOK_BF16 = 0, 1, 2
+MBOK_F32, MBOK_F16, MBOK_BF16, MBOK_E4M3 = 0, 1, 2, 3
 MBOK_GROUP = 128
 MBOK_ROW_BLOCK = 64
 MBOK_MAX_K = 4
@@ -45,11 +52,15 @@ MBOK_MAX_T = 65536
 MBOK_LAYOUT_L64 = 1
 MBOK_MAX_REFIT_ROUNDS = 64
 MBOK_MAX_SVID_ITERS = 1000
-MBOK_ACT_SILU, MBOK_ACT_GELU = 0, 1
+MBOK_ACT_SILU, MBOK_ACT_GELU, MBOK_ACT_NONE = 0, 1, 2
 MBOK_MAX_TOP = 1024
 MBOK_MAX_VOCAB = 1 << 19
 MBOK_MAX_DISTILL_ROWS = 1 << 23
 MBOK_DISTILL_STATS = 8
+MBOK_LOGP_STATS = 4
+MBOK_MAX_PAIRS = 1 << 23
+MBOK_ADAMW_BLOCK = 256
+MBOK_MAX_ADAMW_TENSORS = 65536
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 _LIB = None
@@ -80,6 +91,51 @@ class mbok_distill_desc(ctypes.Structure):
                 f"temperature={self.temperature})")
 
 
+class mbok_logp_desc(ctypes.Structure):
+    _fields_ = [("vocab", ctypes.c_int32), ("temperature", ctypes.c_float)]
+
+    def __repr__(self):
+        return f"mbok_logp_desc(vocab={self.vocab}, temperature={self.temperature})"
+
+
+class mbok_policy_desc(ctypes.Structure):
+    _fields_ = [("vocab", ctypes.c_int32), ("temperature", ctypes.c_float),
+                ("clip_low", ctypes.c_float), ("clip_high", ctypes.c_float),
+                ("kl", ctypes.c_float)]
+
+    def __repr__(self):
+        return (f"mbok_policy_desc(vocab={self.vocab}, temperature={self.temperature}, "
+                f"clip_low={self.clip_low}, clip_high={self.clip_high}, kl={self.kl})")
+
+
+class mbok_preference_desc(ctypes.Structure):
+    _fields_ = [("beta", ctypes.c_float), ("smoothing", ctypes.c_float),
+                ("margin", ctypes.c_float), ("mean", ctypes.c_int32), ("vocab", ctypes.c_int32)]
+
+    def __repr__(self):
+        return (f"mbok_preference_desc(beta={self.beta}, smoothing={self.smoothing}, "
+                f"margin={self.margin}, mean={self.mean}, vocab={self.vocab})")
+
+
+class _AdamwTensor(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("param", "grad", "m", "v", "m_scale", "v_scale",
+                                               "out", "layer")] + \
+        [("count", ctypes.c_int64), ("weight_decay", ctypes.c_double),
+         ("grad_dtype", ctypes.c_int32), ("state_dtype", ctypes.c_int32),
+         ("out_dtype", ctypes.c_int32)]
+
+
+class _AdamwPlan(ctypes.Structure):
+    _fields_ = [("table_bytes", ctypes.c_int64), ("tensors", ctypes.c_int32),
+                ("parts", ctypes.c_int32), ("lds_bytes", ctypes.c_int32)]
+
+
+class _AdamwStep(ctypes.Structure):
+    _fields_ = [("lr", ctypes.c_double), ("beta1", ctypes.c_double), ("beta2", ctypes.c_double),
+                ("eps", ctypes.c_double), ("step", ctypes.c_int64),
+                ("grad_scale", ctypes.c_float), ("seed", ctypes.c_uint32)]
+
+
 def library_path() -> str:
     return os.environ.get("MBOK_LIBRARY", os.path.join(_HERE, "libmbok.so"))
 
@@ -97,6 +153,11 @@ def load_library() -> ctypes.CDLL:
     P, I32, I64, SZ = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t
     D = ctypes.POINTER(mbok_desc)
     DD, F = ctypes.POINTER(mbok_distill_desc), ctypes.c_float
+    DL, DP = ctypes.POINTER(mbok_logp_desc), ctypes.POINTER(mbok_policy_desc)
+    DR, AT = ctypes.POINTER(mbok_preference_desc), ctypes.POINTER(_AdamwTensor)
+    AP, AS = ctypes.POINTER(_AdamwPlan), ctypes.POINTER(_AdamwStep)
+    linear = [D, P, P, I32, I64, I64, P, I32, I32, P, I64, P, I32, I64, P, I64, P]
+    linear_backward = [D, P, P, I64, P, I64, I64, I32, P, I64, P, I32, P, I64, P, P]
     sigs = {
         "mbok_desc_init": (ctypes.c_int, [D, I32, I32, I32, I32]),
         "mbok_packed_bytes": (SZ, [D]),
@@ -137,6 +198,22 @@ def load_library() -> ctypes.CDLL:
                                         I64, P]),
         "mbok_distill_backward": (ctypes.c_int, [DD, P, I32, I64, I64, P, I32, P, I64, P, P, P, P,
                                                  P, I32, I64, P]),
+        "mbok_linear": (ctypes.c_int, linear),
+        "mbok_linear_precise": (ctypes.c_int, linear),
+        "mbok_linear_backward": (ctypes.c_int, linear_backward),
+        "mbok_linear_backward_precise": (ctypes.c_int, linear_backward),
+        "mbok_linear_backward_workspace_bytes": (SZ, [D, I64]),
+        "mbok_logp_desc_init": (ctypes.c_int, [DL, I32, F]),
+        "mbok_logp": (ctypes.c_int, [DL, P, I32, I64, I64, P, P, P, P]),
+        "mbok_logp_backward": (ctypes.c_int, [DL, P, I32, I64, I64, P, P, P, P, I32, I64, P]),
+        "mbok_policy_desc_init": (ctypes.c_int, [DP, I32, F, F, F, F]),
+        "mbok_policy": (ctypes.c_int, [DP, P, I32, I64, I64, P, P, P, P, P, P, P, P, P, P, I32,
+                                       I64, P]),
+        "mbok_preference_desc_init": (ctypes.c_int, [DR, F, F, F, I32, I32]),
+        "mbok_preference": (ctypes.c_int, [DR, P, I64, P, P, P, I64, P, P, P, P]),
+        "mbok_adamw_table_bytes": (SZ, [AT, I32]),
+        "mbok_adamw_plan_init": (ctypes.c_int, [AP, AT, I32, P]),
+        "mbok_adamw": (ctypes.c_int, [AP, P, AS, P, P]),
         "mbok_status_str": (ctypes.c_char_p, [ctypes.c_int]),
         "mbok_version": (ctypes.c_char_p, []),
     }
@@ -935,6 +1012,331 @@ def mbok_distill_backward(d: mbok_distill_desc, Z: torch.Tensor, t_logits: torch
             _vector(stats, "stats", dev, T * MBOK_DISTILL_STATS, torch.float32),
             _vector(dloss, "dloss", dev, T, torch.float32),
             *_distill_grad(dZ, dev, T, vocab, Z.dtype))
+
+
+# ------------------------------------------------------- the layer with its epilogue
+
+def mbok_linear(d: mbok_desc, packed: torch.Tensor, X: torch.Tensor, Y: torch.Tensor,
+                bias: torch.Tensor | None = None, act: int = MBOK_ACT_NONE,
+                residual: torch.Tensor | None = None, pre: torch.Tensor | None = None,
+                stream=None) -> None:
+    """Y[T, m] (bf16 or fp32, overwritten) = residual + act(X W_hat^T + bias) for X
+    bf16 [T, n]; bias [m] fp32, fp16 or bf16; residual of Y's dtype, and may be Y.
+    pre bf16 [T, m] receives the pre-activations for mbok_linear_backward."""
+    _linear_call("mbok_linear", d, packed, X, Y, bias, act, residual, pre, stream)
+
+
+def mbok_linear_precise(d: mbok_desc, packed: torch.Tensor, X: torch.Tensor, Y: torch.Tensor,
+                        bias: torch.Tensor | None = None, act: int = MBOK_ACT_NONE,
+                        residual: torch.Tensor | None = None, pre: torch.Tensor | None = None,
+                        stream=None) -> None:
+    """mbok_linear with each weight carried as two bf16 terms for T > 16 (twice the
+    matrix work)."""
+    _linear_call("mbok_linear_precise", d, packed, X, Y, bias, act, residual, pre, stream)
+
+
+def _linear_call(name: str, d: mbok_desc, packed, X, Y, bias, act, residual, pre, stream) -> None:
+    dev = _first(X, "X")
+    m, n = d.m, d.n
+    T = X.shape[0]
+    ldx = _matrix(X, "X", dev, T, n, torch.bfloat16)
+    if not isinstance(Y, torch.Tensor):
+        raise TypeError("Y must be a torch.Tensor")
+    yt = Y.dtype
+    if yt != torch.bfloat16 and yt != torch.float32:
+        raise ValueError(f"Y must be bfloat16 or float32, got {yt}")
+    ldy = _matrix(Y, "Y", dev, T, m, yt)
+    b_ptr, bt, r_ptr, ldr, p_ptr, ldpre = None, MBOK_F32, None, 0, None, 0
+    if bias is not None:
+        if not isinstance(bias, torch.Tensor):
+            raise TypeError("bias must be a torch.Tensor")
+        bt = _FLOATS.get(bias.dtype)
+        if bt is None:
+            raise ValueError(f"bias must be float32, float16 or bfloat16, got {bias.dtype}")
+        b_ptr = _vector(bias, "bias", dev, m, bias.dtype)
+    if residual is not None:
+        ldr = _matrix(residual, "residual", dev, T, m, yt)
+        r_ptr = residual.data_ptr()
+    if pre is not None:
+        ldpre = _matrix(pre, "pre", dev, T, m, torch.bfloat16)
+        p_ptr = pre.data_ptr()
+    _launch(getattr(load_library(), name), name, dev, stream, ctypes.byref(d),
+            _packed(packed, dev, m, n, d.K, d.alpha_dtype), X.data_ptr(), MBOK_BF16, T, ldx,
+            b_ptr, bt, act, r_ptr, ldr, Y.data_ptr(), _FLOATS[yt], ldy, p_ptr, ldpre)
+
+
+def mbok_linear_backward_workspace_bytes(d: mbok_desc, T: int) -> int:
+    return int(load_library().mbok_linear_backward_workspace_bytes(ctypes.byref(d), T))
+
+
+def mbok_linear_backward(d: mbok_desc, packed: torch.Tensor, dY: torch.Tensor,
+                         pre: torch.Tensor | None = None, dpre: torch.Tensor | None = None,
+                         dbias: torch.Tensor | None = None, dX: torch.Tensor | None = None,
+                         act: int = MBOK_ACT_NONE, accumulate: bool = False,
+                         workspace: torch.Tensor | None | bool = True, stream=None) -> None:
+    """Gradients of mbok_linear from dY bf16 [T, m]: dpre bf16 [T, m] (with an
+    activation; from pre, and may be pre or dY), dbias fp32 [m] (accumulate: added
+    to) and dX bf16 [T, n], each where asked for.  The residual's is dY.
+
+    workspace: as for mbok_gemmt."""
+    _linear_backward_call("mbok_linear_backward", d, packed, dY, pre, dpre, dbias, dX, act,
+                          accumulate, workspace, stream)
+
+
+def mbok_linear_backward_precise(d: mbok_desc, packed: torch.Tensor, dY: torch.Tensor,
+                                 pre: torch.Tensor | None = None,
+                                 dpre: torch.Tensor | None = None,
+                                 dbias: torch.Tensor | None = None,
+                                 dX: torch.Tensor | None = None, act: int = MBOK_ACT_NONE,
+                                 accumulate: bool = False,
+                                 workspace: torch.Tensor | None | bool = True,
+                                 stream=None) -> None:
+    """mbok_linear_backward with dX as mbok_gemmt_precise computes it."""
+    _linear_backward_call("mbok_linear_backward_precise", d, packed, dY, pre, dpre, dbias, dX,
+                          act, accumulate, workspace, stream)
+
+
+def _linear_backward_call(name: str, d: mbok_desc, packed, dY, pre, dpre, dbias, dX, act,
+                          accumulate, workspace, stream) -> None:
+    dev = _first(dY, "dY")
+    m, n, K, at = d.m, d.n, d.K, d.alpha_dtype
+    T = dY.shape[0]
+    lddy = _matrix(dY, "dY", dev, T, m, torch.bfloat16)
+    ptrs, lds = [None, None, None], [0, 0, 0]
+    for i, (t, what, cols) in enumerate(((pre, "pre", m), (dpre, "dpre", m), (dX, "dX", n))):
+        if t is not None:
+            lds[i] = _matrix(t, what, dev, T, cols, torch.bfloat16)
+            ptrs[i] = t.data_ptr()
+    b_ptr = None if dbias is None else _vector(dbias, "dbias", dev, m, torch.float32)
+    with _slices("mbok_linear_backward_workspace_bytes", m, n, K, at, T, workspace, dev,
+                 stream) as ws:
+        _launch(getattr(load_library(), name), name, dev, stream, ctypes.byref(d),
+                _packed(packed, dev, m, n, K, at), ptrs[0], lds[0], dY.data_ptr(), lddy, T, act,
+                ptrs[1], lds[1], b_ptr, int(bool(accumulate)), ptrs[2], lds[2],
+                None if ws is None else ws.data_ptr())
+
+
+# -------------------------------------- log-probabilities, policy and preference losses
+
+def mbok_logp_desc_init(vocab: int, temperature: float = 1.0) -> mbok_logp_desc:
+    d = mbok_logp_desc()
+    _check(load_library().mbok_logp_desc_init(ctypes.byref(d), vocab, temperature),
+           "mbok_logp_desc_init")
+    return d
+
+
+def _rows(Z, label, vocab):
+    """(device, rows, the arguments the calls on rows of logits begin with), checked."""
+    dev = _first(Z, "Z")
+    T, zt = Z.shape[0], _FLOATS.get(Z.dtype)
+    if zt is None:
+        raise ValueError("Z must be float32, float16 or bfloat16")
+    ldz = _matrix(Z, "Z", dev, T, vocab, Z.dtype)
+    return dev, T, (Z.data_ptr(), zt, T, ldz, _vector(label, "label", dev, T, torch.int32))
+
+
+def _optional(t, name: str, dev: int, count: int):
+    return None if t is None else _vector(t, name, dev, count, torch.float32)
+
+
+def mbok_logp(d: mbok_logp_desc, Z: torch.Tensor, label: torch.Tensor, logp: torch.Tensor,
+              stats: torch.Tensor | None = None, stream=None) -> None:
+    """logp[T] (fp32, overwritten): log-probability of each row's token label[T]
+    (int32; negative: none, logp 0) under softmax(Z / tau).  stats fp32 [T,
+    MBOK_LOGP_STATS] is what mbok_logp_backward takes."""
+    dev, T, args = _rows(Z, label, d.vocab)
+    _launch(load_library().mbok_logp, "mbok_logp", dev, stream, ctypes.byref(d), *args,
+            _vector(logp, "logp", dev, T, torch.float32),
+            _optional(stats, "stats", dev, T * MBOK_LOGP_STATS))
+
+
+def mbok_logp_backward(d: mbok_logp_desc, Z: torch.Tensor, label: torch.Tensor,
+                       stats: torch.Tensor, dlogp: torch.Tensor, dZ: torch.Tensor,
+                       stream=None) -> None:
+    """dZ (dtype of Z or bf16; may be Z) = the gradient of sum(dlogp * logp) after
+    mbok_logp or mbok_policy with stats on the same inputs; dlogp fp32 [T]."""
+    vocab = d.vocab
+    dev, T, args = _rows(Z, label, vocab)
+    _launch(load_library().mbok_logp_backward, "mbok_logp_backward", dev, stream,
+            ctypes.byref(d), *args, _vector(stats, "stats", dev, T * MBOK_LOGP_STATS,
+                                            torch.float32),
+            _vector(dlogp, "dlogp", dev, T, torch.float32),
+            *_distill_grad(dZ, dev, T, vocab, Z.dtype))
+
+
+def mbok_policy_desc_init(vocab: int, temperature: float = 1.0, clip_low: float = 0.2,
+                          clip_high: float = 0.2, kl: float = 0.0) -> mbok_policy_desc:
+    d = mbok_policy_desc()
+    _check(load_library().mbok_policy_desc_init(ctypes.byref(d), vocab, temperature, clip_low,
+                                                clip_high, kl), "mbok_policy_desc_init")
+    return d
+
+
+def mbok_policy(d: mbok_policy_desc, Z: torch.Tensor, label: torch.Tensor,
+                advantage: torch.Tensor, loss: torch.Tensor,
+                old_logp: torch.Tensor | None = None, ref_logp: torch.Tensor | None = None,
+                weight: torch.Tensor | None = None, logp: torch.Tensor | None = None,
+                stats: torch.Tensor | None = None, dlogp: torch.Tensor | None = None,
+                dZ: torch.Tensor | None = None, stream=None) -> None:
+    """loss[T] (fp32, overwritten): clipped policy loss with a KL term of each
+    row's token, from advantage [T], the log-probabilities old_logp [T] it was
+    sampled with (None: the present ones), a reference model's ref_logp [T] (None: no
+    KL term) and weight [T].  dZ (dtype of Z or bf16; may be Z) receives the gradient
+    of sum(loss) in the same pass; logp, stats and dlogp are as for mbok_logp and
+    mbok_logp_backward."""
+    vocab = d.vocab
+    dev, T, args = _rows(Z, label, vocab)
+    grad = (None, args[1], 0) if dZ is None else _distill_grad(dZ, dev, T, vocab, Z.dtype)
+    _launch(load_library().mbok_policy, "mbok_policy", dev, stream, ctypes.byref(d), *args,
+            _vector(advantage, "advantage", dev, T, torch.float32),
+            _optional(old_logp, "old_logp", dev, T), _optional(ref_logp, "ref_logp", dev, T),
+            _optional(weight, "weight", dev, T), _vector(loss, "loss", dev, T, torch.float32),
+            _optional(logp, "logp", dev, T), _optional(stats, "stats", dev, T * MBOK_LOGP_STATS),
+            _optional(dlogp, "dlogp", dev, T), *grad)
+
+
+def mbok_preference_desc_init(beta: float, smoothing: float = 0.0, margin: float = 0.0,
+                              mean: bool = False,
+                              vocab: int = MBOK_MAX_VOCAB) -> mbok_preference_desc:
+    d = mbok_preference_desc()
+    _check(load_library().mbok_preference_desc_init(ctypes.byref(d), beta, smoothing, margin,
+                                                    int(bool(mean)), vocab),
+           "mbok_preference_desc_init")
+    return d
+
+
+def mbok_preference(d: mbok_preference_desc, offsets: torch.Tensor, logp: torch.Tensor,
+                    loss: torch.Tensor, ref_logp: torch.Tensor | None = None,
+                    label: torch.Tensor | None = None, weight: torch.Tensor | None = None,
+                    dlogp: torch.Tensor | None = None, stream=None) -> None:
+    """loss[pairs] (fp32, overwritten) of paired log ratios: sequences 2p (chosen)
+    and 2p + 1 (rejected) are rows offsets[s] .. offsets[s + 1] - 1 (int32 [2 pairs +
+    1]) of logp [T], less the reference model's ref_logp [T]; rows without a token
+    (label) do not count.  dlogp [T] receives the gradient for mbok_logp_backward."""
+    dev = _first(logp, "logp")
+    T = logp.numel()
+    if not isinstance(offsets, torch.Tensor):
+        raise TypeError("offsets must be a torch.Tensor")
+    if offsets.dim() != 1 or offsets.numel() < 3 or offsets.numel() % 2 == 0:
+        raise ValueError("offsets must be [2 pairs + 1]")
+    pairs = offsets.numel() // 2
+    _launch(load_library().mbok_preference, "mbok_preference", dev, stream, ctypes.byref(d),
+            _vector(offsets, "offsets", dev, 2 * pairs + 1, torch.int32), pairs,
+            _vector(logp, "logp", dev, T, torch.float32),
+            _optional(ref_logp, "ref_logp", dev, T),
+            None if label is None else _vector(label, "label", dev, T, torch.int32), T,
+            _optional(weight, "weight", dev, pairs),
+            _vector(loss, "loss", dev, pairs, torch.float32), _optional(dlogp, "dlogp", dev, T))
+
+
+# ------------------------------------------------------------------ the optimizer step
+
+class mbok_adamw_plan:
+    """The tensors of an optimizer step (mbok_adamw_plan_init): the library's plan,
+    its table on the device, and the tensors, which it keeps alive."""
+
+    def __init__(self, plan, table: torch.Tensor, tensors: list):
+        self._plan, self.table, self.tensors = plan, table, tensors
+        self._args = (ctypes.byref(plan), table.data_ptr())
+        self.device = table.get_device()
+
+    def __repr__(self):
+        return f"mbok_adamw_plan({self._plan.tensors} tensors, {self._plan.parts} parts)"
+
+
+_ADAMW_KEYS = {"param", "grad", "m", "v", "m_scale", "v_scale", "out", "layer", "weight_decay"}
+
+
+def _adamw_tensor(i: int, t: dict, dev: int) -> _AdamwTensor:
+    unknown = set(t) - _ADAMW_KEYS
+    missing = {"param", "grad", "m", "v"} - set(t)
+    if unknown or missing:
+        raise ValueError(f"tensor {i}: unknown {sorted(unknown)}, missing {sorted(missing)}")
+
+    def flat(name, dtype, count):
+        x = t[name]
+        if isinstance(x, torch.Tensor) and x.numel() != count:
+            raise ValueError(f"tensor {i}: {name} must have {count} elements, got {x.numel()}")
+        return _vector(x, f"tensor {i}: {name}", dev, count, dtype)
+
+    if not isinstance(t["grad"], torch.Tensor) or not isinstance(t["m"], torch.Tensor):
+        raise TypeError(f"tensor {i}: grad and m must be torch.Tensors")
+    count = t["param"].numel()
+    a = _AdamwTensor()
+    a.count, a.weight_decay = count, float(t.get("weight_decay", 0.0))
+    a.param = flat("param", torch.float32, count)
+    gt = _FLOATS.get(t["grad"].dtype)
+    if gt is None:
+        raise ValueError(f"tensor {i}: grad must be float32, float16 or bfloat16")
+    a.grad, a.grad_dtype = flat("grad", t["grad"].dtype, count), gt
+    eight = t["m"].dtype == torch.float8_e4m3fn
+    st = torch.float8_e4m3fn if eight else torch.float32
+    a.m, a.v = flat("m", st, count), flat("v", st, count)
+    a.state_dtype = MBOK_E4M3 if eight else MBOK_F32
+    scales = [t.get(k) is not None for k in ("m_scale", "v_scale")]
+    if scales != [eight, eight]:
+        raise ValueError(f"tensor {i}: 8-bit states, and they alone, have m_scale and v_scale")
+    if eight:
+        blocks = (count + MBOK_ADAMW_BLOCK - 1) // MBOK_ADAMW_BLOCK
+        a.m_scale = flat("m_scale", torch.float32, blocks)
+        a.v_scale = flat("v_scale", torch.float32, blocks)
+    layer, out = t.get("layer"), t.get("out")
+    if layer is not None:
+        if out is None:
+            raise ValueError(f"tensor {i}: a layer's scales need its packed buffer as out")
+        a.layer = ctypes.addressof(layer)
+        a.out = _packed(out, dev, layer.m, layer.n, layer.K, layer.alpha_dtype)
+    elif out is not None:
+        if not isinstance(out, torch.Tensor):
+            raise TypeError(f"tensor {i}: out must be a torch.Tensor")
+        ot = _FLOATS.get(out.dtype)
+        if ot is None:
+            raise ValueError(f"tensor {i}: out must be float32, float16 or bfloat16")
+        a.out, a.out_dtype = flat("out", out.dtype, count), ot
+    return a
+
+
+def mbok_adamw_plan_init(tensors) -> mbok_adamw_plan:
+    """The plan of a step over many tensors.  Each is a dict of contiguous tensors:
+    param (fp32), grad (fp32, fp16 or bf16), m and v (both fp32, or both
+    float8_e4m3fn with fp32 m_scale and v_scale of one value per MBOK_ADAMW_BLOCK;
+    8-bit v holds the second moment's root), optionally out (a copy in fp32, fp16 or
+    bf16; with layer, a mbok_desc, the layer's packed buffer, whose scales the step
+    writes from param [K, m, n/128]) and weight_decay.  The plan holds their
+    addresses: gradients are expected in the same tensors at every step."""
+    tensors = [dict(t) for t in tensors]
+    if not tensors:
+        raise ValueError("a plan needs at least one tensor")
+    if "param" not in tensors[0]:
+        raise ValueError("tensor 0: missing ['param']")
+    dev = _first(tensors[0]["param"], "tensor 0: param")
+    for i, t in enumerate(tensors):
+        if not isinstance(t.get("param"), torch.Tensor):
+            raise TypeError(f"tensor {i}: param must be a torch.Tensor")
+    items = (_AdamwTensor * len(tensors))(*(_adamw_tensor(i, t, dev)
+                                            for i, t in enumerate(tensors)))
+    lib, plan = load_library(), _AdamwPlan()
+    host = torch.zeros(max(16, lib.mbok_adamw_table_bytes(items, len(tensors))),
+                       dtype=torch.uint8)
+    _check(lib.mbok_adamw_plan_init(ctypes.byref(plan), items, len(tensors), host.data_ptr()),
+           "mbok_adamw_plan_init")
+    return mbok_adamw_plan(plan, host.to(torch.device("cuda", dev)), tensors)
+
+
+def mbok_adamw(plan: mbok_adamw_plan, lr: float, step: int, beta1: float = 0.9,
+               beta2: float = 0.999, eps: float = 1e-8, grad_scale: float = 1.0, seed: int = 0,
+               live: torch.Tensor | None = None, stream=None) -> None:
+    """One AdamW step on every tensor of the plan, in one launch; step counts from
+    1.  Gradients are multiplied by grad_scale.  live fp32 [4] on the device (lr,
+    grad_scale, step, skip) is read in place of those arguments when the step runs,
+    for steps captured into a graph."""
+    if not isinstance(plan, mbok_adamw_plan):
+        raise TypeError("plan must be mbok_adamw_plan_init's")
+    dev = plan.device
+    ptr = None if live is None else _vector(live, "live", dev, 4, torch.float32)
+    s = _AdamwStep(lr, beta1, beta2, eps, step, grad_scale, seed & 0xffffffff)
+    _launch(load_library().mbok_adamw, "mbok_adamw", dev, stream, *plan._args, ctypes.byref(s),
+            ptr)
 
 
 # ---------------------------------------------------------------- conveniences

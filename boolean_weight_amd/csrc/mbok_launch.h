@@ -109,4 +109,52 @@ int launch_distill(const mbok_distill_desc* d, const DistillArgs& a, float* loss
 int launch_distill_backward(const mbok_distill_desc* d, const DistillArgs& a, const float* stats,
                             const float* dloss, hipStream_t stream);
 
+// the layer with its epilogue (mbok_linear.h)
+struct LinearOut;
+int launch_linear(const mbok_desc* d, const void* packed, const void* X, int64_t T, int64_t ldx,
+                  const LinearOut& out, int passes, hipStream_t stream);
+int launch_linear_f4(const mbok_desc* d, const void* packed, const void* X, int64_t T,
+                     int64_t ldx, const LinearOut& out, hipStream_t stream);
+int launch_linear_skinny(const mbok_desc* d, const void* packed, const void* X, int64_t T,
+                         int64_t ldx, const LinearOut& out, hipStream_t stream);
+int launch_linear_mfma(const mbok_desc* d, const void* packed, const void* X, int64_t T,
+                       int64_t ldx, const LinearOut& out, int passes, hipStream_t stream);
+// the caller's arrays of one backward call (pre, dpre, dbias, dX may be null)
+struct LinearGrad {
+  const void* dY;
+  int64_t lddy;
+  const void* pre;
+  int64_t ldpre;
+  void* dpre;
+  int64_t lddpre;
+  float* dbias;
+  void* dX;
+  int64_t lddx;
+};
+int launch_linear_backward(const mbok_desc* d, const void* packed, const LinearGrad& g, int64_t T,
+                           int act, int accumulate, void* ws, int passes, hipStream_t stream);
+size_t linear_backward_workspace_bytes(const mbok_desc* d, int64_t T);
+// the caller's rows of logits of one call (dZ may be null)
+struct RowArgs {
+  const void* Z;
+  int32_t z_dtype;
+  int64_t T, ldz;
+  const int32_t* label;
+  void* dZ;
+  int32_t dz_dtype;
+  int64_t lddz;
+};
+int launch_logp(const mbok_logp_desc* d, const RowArgs& a, float* logp, float* stats,
+                hipStream_t stream);
+int launch_logp_backward(const mbok_logp_desc* d, const RowArgs& a, const float* stats,
+                         const float* dlogp, hipStream_t stream);
+int launch_policy(const mbok_policy_desc* d, const RowArgs& a, const float* advantage,
+                  const float* old_logp, const float* ref_logp, const float* weight, float* loss,
+                  float* logp, float* stats, float* dlogp, hipStream_t stream);
+int launch_preference(const mbok_preference_desc* d, const int32_t* offsets, int64_t pairs,
+                      const float* logp, const float* ref_logp, const int32_t* label, int64_t T,
+                      const float* weight, float* loss, float* dlogp, hipStream_t stream);
+int launch_adamw(const mbok_adamw_plan* plan, const void* table, const mbok_adamw_step* step,
+                 const float* live, hipStream_t stream);
+
 }  // namespace mbok

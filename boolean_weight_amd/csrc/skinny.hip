@@ -41,6 +41,7 @@
 
 #include "mbok_exact.h"
 #include "mbok_gated.h"
+#include "mbok_linear.h"
 #include "mbok_lanes.h"
 #include "mbok_launch.h"
 
@@ -185,11 +186,11 @@ __global__ void __launch_bounds__(1024) gemm_skinny_kernel(
   skinny_body<AT, K>(bits, scales, X, ldx, RowsOut{Y, ldy, m}, T, G);
 }
 
-// the gated feed-forward block on its stacked layer
-template <typename AT, int K>
-__global__ void __launch_bounds__(1024) gated_skinny_kernel(
+// an epilogue of the caller's (GatedOut, on the stacked layer; LinearOut)
+template <typename AT, int K, typename Out>
+__global__ void __launch_bounds__(1024) out_skinny_kernel(
     const u32x4* __restrict__ bits, const AT* __restrict__ scales,
-    const uint16_t* __restrict__ X, int64_t ldx, int T, int G, GatedOut out) {
+    const uint16_t* __restrict__ X, int64_t ldx, int T, int G, Out out) {
   skinny_body<AT, K>(bits, scales, X, ldx, out, T, G);
 }
 
@@ -423,12 +424,12 @@ __global__ void __launch_bounds__(512) gemm_skinny_stream_kernel(
                                       RowsOut{Y, ldy, m}, sv_x, sv_xf32, sv_sin);
 }
 
-// the gated feed-forward block on its stacked layer
-template <typename AT, int K, int JMAX>
-__global__ void __launch_bounds__(512) gated_skinny_stream_kernel(
+// an epilogue of the caller's
+template <typename AT, int K, int JMAX, typename Out>
+__global__ void __launch_bounds__(512) out_skinny_stream_kernel(
     const u32x4* __restrict__ bits, const AT* __restrict__ scales,
     const uint16_t* __restrict__ X, int64_t ldx, int T, int G, int slab_groups, int tiles,
-    int grid, int tw, GatedOut out) {
+    int grid, int tw, Out out) {
   skinny_stream_body<AT, K, JMAX, false>(bits, scales, X, ldx, T, G, slab_groups, tiles, grid, tw,
                                          out, nullptr, 0, (const AT*)nullptr);
 }
@@ -438,14 +439,14 @@ int env_int(const char* name, int fallback) {
   return (v && *v) ? atoi(v) : fallback;
 }
 
-template <typename AT, int K>
+template <typename AT, int K, typename Out>
 void launch_k(const Geom& geo, const u32x4* bits, const AT* scales, const uint16_t* X,
-              int64_t ldx, float* Y, int64_t ldy, int T, int NW, const GatedOut* gated,
+              int64_t ldx, float* Y, int64_t ldy, int T, int NW, const Out* out,
               hipStream_t stream) {
   const size_t lds = (size_t)NW * 256 * sizeof(float);
-  if (gated) {
-    hipLaunchKernelGGL((gated_skinny_kernel<AT, K>), dim3(geo.RB * 4), dim3(64 * NW), lds, stream,
-                       bits, scales, X, ldx, T, geo.G, *gated);
+  if constexpr (!std::is_same<Out, RowsOut>::value) {
+    hipLaunchKernelGGL((out_skinny_kernel<AT, K, Out>), dim3(geo.RB * 4), dim3(64 * NW), lds,
+                       stream, bits, scales, X, ldx, T, geo.G, *out);
     return;
   }
   hipLaunchKernelGGL((gemm_skinny_kernel<AT, K>), dim3(geo.RB * 4), dim3(64 * NW), lds, stream,
@@ -454,11 +455,11 @@ void launch_k(const Geom& geo, const u32x4* bits, const AT* scales, const uint16
 
 constexpr int kSkinnyJ = 8;  // tiles per persistent workgroup (registers)
 
-template <typename AT, int K, bool SV = false>
+template <typename AT, int K, bool SV = false, typename Out = RowsOut>
 void launch_stream_k(const Geom& geo, const u32x4* bits, const AT* scales, const uint16_t* X,
                      int64_t ldx, float* Y, int64_t ldy, int T, hipStream_t stream,
                      const void* sv_x = nullptr, int sv_xf32 = 0, const AT* sv_sin = nullptr,
-                     const GatedOut* gated = nullptr) {
+                     const Out* out = nullptr) {
   // slabs of at most 32 groups: one wavefront per block of 4 groups, at most 8
   const int nslabs = (geo.G + 31) / 32;
   const int slab = (geo.G + nslabs - 1) / nslabs;
@@ -470,9 +471,9 @@ void launch_stream_k(const Geom& geo, const u32x4* bits, const AT* scales, const
   if (SV) lds += (size_t)NW * 4 * K * 2 * kGroup * sizeof(uint16_t);
   static_assert(kSkinnyJ <= 15, "tiles per workgroup are packed in 4 bits");
   const int tw = tiles / grid | NW << 4 | (tiles % grid) << 8;
-  if (gated) {
-    hipLaunchKernelGGL((gated_skinny_stream_kernel<AT, K, kSkinnyJ>), dim3(grid), dim3(64 * NW),
-                       lds, stream, bits, scales, X, ldx, T, geo.G, slab, tiles, grid, tw, *gated);
+  if constexpr (!std::is_same<Out, RowsOut>::value) {
+    hipLaunchKernelGGL((out_skinny_stream_kernel<AT, K, kSkinnyJ, Out>), dim3(grid), dim3(64 * NW),
+                       lds, stream, bits, scales, X, ldx, T, geo.G, slab, tiles, grid, tw, *out);
     return;
   }
   hipLaunchKernelGGL((gemm_skinny_stream_kernel<AT, K, kSkinnyJ, SV>), dim3(grid), dim3(64 * NW), lds,
@@ -480,9 +481,10 @@ void launch_stream_k(const Geom& geo, const u32x4* bits, const AT* scales, const
                      sv_x, sv_xf32, sv_sin);
 }
 
-template <typename AT>
+// out: where the sums go, unless Out is RowsOut (Y, ldy)
+template <typename AT, typename Out = RowsOut>
 int launch_at(const Geom& geo, const void* packed, const void* X, int64_t ldx, float* Y,
-              int64_t ldy, int T, const GatedOut* gated, hipStream_t stream) {
+              int64_t ldy, int T, const Out* out, hipStream_t stream) {
   const u32x4* bits = reinterpret_cast<const u32x4*>(packed);
   const AT* scales = reinterpret_cast<const AT*>(reinterpret_cast<const char*>(packed) +
                                                  geo.bits_bytes);
@@ -496,8 +498,8 @@ int launch_at(const Geom& geo, const void* packed, const void* X, int64_t ldx, f
   if (v && strcmp(v, "stream") == 0) streaming = true;
   if (streaming) {
     auto stream_k = [&](auto k) {
-      launch_stream_k<AT, decltype(k)::value>(geo, bits, scales, Xb, ldx, Y, ldy, T, stream,
-                                              nullptr, 0, nullptr, gated);
+      launch_stream_k<AT, decltype(k)::value, false, Out>(geo, bits, scales, Xb, ldx, Y, ldy, T,
+                                                          stream, nullptr, 0, nullptr, out);
     };
     switch (geo.K) {
       case 1: stream_k(std::integral_constant<int, 1>{}); break;
@@ -515,10 +517,10 @@ int launch_at(const Geom& geo, const void* packed, const void* X, int64_t ldx, f
   if (NW > geo.G) NW = geo.G;
   if (NW < 1) NW = 1;
   switch (geo.K) {
-    case 1: launch_k<AT, 1>(geo, bits, scales, Xb, ldx, Y, ldy, T, NW, gated, stream); break;
-    case 2: launch_k<AT, 2>(geo, bits, scales, Xb, ldx, Y, ldy, T, NW, gated, stream); break;
-    case 3: launch_k<AT, 3>(geo, bits, scales, Xb, ldx, Y, ldy, T, NW, gated, stream); break;
-    default: launch_k<AT, 4>(geo, bits, scales, Xb, ldx, Y, ldy, T, NW, gated, stream); break;
+    case 1: launch_k<AT, 1>(geo, bits, scales, Xb, ldx, Y, ldy, T, NW, out, stream); break;
+    case 2: launch_k<AT, 2>(geo, bits, scales, Xb, ldx, Y, ldy, T, NW, out, stream); break;
+    case 3: launch_k<AT, 3>(geo, bits, scales, Xb, ldx, Y, ldy, T, NW, out, stream); break;
+    default: launch_k<AT, 4>(geo, bits, scales, Xb, ldx, Y, ldy, T, NW, out, stream); break;
   }
   return hipGetLastError() == hipSuccess ? MBOK_OK : MBOK_ERR_HIP;
 }
@@ -563,18 +565,29 @@ int launch_skinny(const mbok_desc* d, const void* packed, const void* X, int64_t
   if (T < 1 || T > kMaxSkinnyTokens) return MBOK_ERR_SHAPE;
   const Geom geo = make_geom(d);
   if (d->alpha_dtype == MBOK_F16)
-    return launch_at<uint16_t>(geo, packed, X, ldx, Y, ldy, (int)T, nullptr, stream);
-  return launch_at<float>(geo, packed, X, ldx, Y, ldy, (int)T, nullptr, stream);
+    return launch_at<uint16_t>(geo, packed, X, ldx, Y, ldy, (int)T, (const RowsOut*)nullptr, stream);
+  return launch_at<float>(geo, packed, X, ldx, Y, ldy, (int)T, (const RowsOut*)nullptr, stream);
 }
 
-// d: the stacked layer
-int launch_gated_skinny(const mbok_desc* d, const void* packed, const void* X, int64_t T,
-                        int64_t ldx, const GatedOut& out, hipStream_t stream) {
+template <typename Out>
+static int launch_out_skinny(const mbok_desc* d, const void* packed, const void* X, int64_t T,
+                             int64_t ldx, const Out& out, hipStream_t stream) {
   if (T < 1 || T > kMaxSkinnyTokens) return MBOK_ERR_SHAPE;
   const Geom geo = make_geom(d);
   if (d->alpha_dtype == MBOK_F16)
     return launch_at<uint16_t>(geo, packed, X, ldx, nullptr, 0, (int)T, &out, stream);
   return launch_at<float>(geo, packed, X, ldx, nullptr, 0, (int)T, &out, stream);
+}
+
+// d: the stacked layer
+int launch_gated_skinny(const mbok_desc* d, const void* packed, const void* X, int64_t T,
+                        int64_t ldx, const GatedOut& out, hipStream_t stream) {
+  return launch_out_skinny(d, packed, X, T, ldx, out, stream);
+}
+
+int launch_linear_skinny(const mbok_desc* d, const void* packed, const void* X, int64_t T,
+                         int64_t ldx, const LinearOut& out, hipStream_t stream) {
+  return launch_out_skinny(d, packed, X, T, ldx, out, stream);
 }
 
 }  // namespace mbok

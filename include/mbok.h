@@ -101,8 +101,9 @@ enum {
   MBOK_ERR_SCRATCH = -8      /* more scratch needed than the static scratch holds */
 };
 
-/* Element types. */
-enum { MBOK_F32 = 0, MBOK_F16 = 1, MBOK_BF16 = 2 };
+/* Element types.  MBOK_E4M3 (8-bit float, 4 exponent and 3 mantissa bits,
+ * largest value 448) is taken by mbok_adamw's states alone. */
+enum { MBOK_F32 = 0, MBOK_F16 = 1, MBOK_BF16 = 2, MBOK_E4M3 = 3 };
 
 /* Packed layouts. */
 enum { MBOK_LAYOUT_L64 = 1 };
@@ -578,10 +579,11 @@ int mbok_scale_grad(const mbok_desc* d, const void* packed, const void* dY, int6
  * only; 0 for a NULL or invalid descriptor or T. */
 size_t mbok_scale_grad_workspace_bytes(const mbok_desc* d, int64_t T);
 
-/* Activations of the gated block. */
+/* Activations of the gated block and (with MBOK_ACT_NONE) of mbok_linear. */
 enum {
   MBOK_ACT_SILU = 0, /* x / (1 + exp(-x)) */
-  MBOK_ACT_GELU = 1  /* x (1 + tanh(sqrt(2/pi) (x + 0.044715 x^3))) / 2 */
+  MBOK_ACT_GELU = 1, /* x (1 + tanh(sqrt(2/pi) (x + 0.044715 x^3))) / 2 */
+  MBOK_ACT_NONE = 2  /* x; mbok_linear and its backward only */
 };
 
 /*
@@ -681,6 +683,84 @@ int mbok_gated_backward_precise(const mbok_desc* d, const void* packed, const vo
                                 int32_t act, void* dpre, int64_t lddpre, void* dX, int64_t lddx,
                                 void* workspace, void* stream);
 
+/*
+ * One layer with what follows it in a block:
+ *     z[t, i] = sum_j W_hat[i, j] X[t, j] + bias[i]
+ *     Y[t, i] = residual[t, i] + act(z[t, i])
+ * The product as mbok_gated computes its own for T rows (exact per scale for T
+ * <= 16, levels rounded to bf16 for larger T), then bias, activation and
+ * residual in fp32 and one rounding to Y's type.
+ *  packed    device, MBOK_LAYOUT_L64 buffer of this descriptor.
+ *  X         device bf16 [T, ldx], ldx >= n, ldx % 8 == 0, 16-byte aligned.
+ *  T         1 .. MBOK_MAX_T.
+ *  bias      device [m] of bias_dtype (MBOK_F32, MBOK_F16 or MBOK_BF16), or NULL.
+ *  act       MBOK_ACT_NONE, MBOK_ACT_SILU or MBOK_ACT_GELU.
+ *  residual  device [T, ldr] of y_dtype, ldr >= m, or NULL.  May be Y itself
+ *            (same leading dimension): the residual stream updated in place.
+ *  Y         device [T, ldy] of y_dtype (MBOK_BF16 or MBOK_F32), ldy >= m;
+ *            overwritten.
+ *  pre       device bf16 [T, ldpre], ldpre >= m, or NULL: z rounded once, for
+ *            mbok_linear_backward.
+ * residual, Y and pre rows start at any element (16-byte aligned rows run
+ * faster).  Y and pre must not overlap X or each other.  Non-finite activations
+ * as for mbok_gated.
+ * Errors: INVALID_ARG (NULL, act, leading dimensions, residual = Y with another
+ * one; ldx >= 2^23 for T > 16), SHAPE (T; a layer of 2^32 or more sign words, or
+ * an output of 2^32 or more tiles' threads, for T > 16), DTYPE (x_dtype other
+ * than MBOK_BF16, y_dtype, bias_dtype), ALIGN (packed and X 16 bytes, ldx % 8,
+ * the others to their element), HIP, and the descriptor's.
+ */
+int mbok_linear(const mbok_desc* d, const void* packed, const void* X, int32_t x_dtype,
+                int64_t T, int64_t ldx, const void* bias, int32_t bias_dtype, int32_t act,
+                const void* residual, int64_t ldr, void* Y, int32_t y_dtype, int64_t ldy,
+                void* pre, int64_t ldpre, void* stream);
+
+/* mbok_linear with each weight carried as two bf16 terms for T > 16 (see
+ * mbok_gated_precise).  Same arguments and errors. */
+int mbok_linear_precise(const mbok_desc* d, const void* packed, const void* X, int32_t x_dtype,
+                        int64_t T, int64_t ldx, const void* bias, int32_t bias_dtype,
+                        int32_t act, const void* residual, int64_t ldr, void* Y,
+                        int32_t y_dtype, int64_t ldy, void* pre, int64_t ldpre, void* stream);
+
+/*
+ * Backward of mbok_linear (the residual's gradient is dY itself):
+ *     dpre = dY act'(pre)          (fp32, rounded once to bf16)
+ *     dbias[i] = sum_t dpre[t, i]  (fp32, of the values before that rounding)
+ *     dX = dpre W_hat              (mbok_gemmt)
+ *  dY    device bf16 [T, lddy], lddy >= m.
+ *  pre   device bf16 [T, ldpre], as mbok_linear wrote it.
+ *  dpre  device bf16 [T, lddpre]; overwritten: the dY of mbok_scale_grad.  May be
+ *        pre or dY itself (same leading dimension).
+ *        With MBOK_ACT_NONE pre and dpre are NULL: dY is dpre.
+ *  dbias device fp32 [m] or NULL; accumulate 0 overwrites it, otherwise the sums
+ *        are added to it (as for mbok_scale_grad).
+ *  dX    device bf16 [T, lddx], lddx >= n, lddx % 8 == 0, 16-byte aligned, or
+ *        NULL.  Must not overlap dY or dpre.
+ *  workspace  device, mbok_linear_backward_workspace_bytes(d, T) bytes, 256-byte
+ *        aligned, or NULL, as for mbok_gemmt: with it the rows are split into
+ *        slices for dbias too, whose sums are added in a fixed order.
+ * Errors: INVALID_ARG (NULL, act, leading dimensions; nothing asked for: no
+ * activation, dbias and dX NULL), SHAPE (T), ALIGN (packed and dX 16 bytes,
+ * lddx % 8, dY, pre, dpre 2 bytes, dbias 4, workspace 256 bytes), HIP, and the
+ * descriptor's.
+ */
+int mbok_linear_backward(const mbok_desc* d, const void* packed, const void* pre, int64_t ldpre,
+                         const void* dY, int64_t lddy, int64_t T, int32_t act, void* dpre,
+                         int64_t lddpre, float* dbias, int32_t accumulate, void* dX,
+                         int64_t lddx, void* workspace, void* stream);
+
+/* mbok_linear_backward with dX by mbok_gemmt_precise.  Same arguments, workspace
+ * and errors. */
+int mbok_linear_backward_precise(const mbok_desc* d, const void* packed, const void* pre,
+                                 int64_t ldpre, const void* dY, int64_t lddy, int64_t T,
+                                 int32_t act, void* dpre, int64_t lddpre, float* dbias,
+                                 int32_t accumulate, void* dX, int64_t lddx, void* workspace,
+                                 void* stream);
+
+/* Bytes of the workspace mbok_linear_backward uses for this layer and T rows (0
+ * when it needs none).  Host only; 0 for a NULL or invalid descriptor or T. */
+size_t mbok_linear_backward_workspace_bytes(const mbok_desc* d, int64_t T);
+
 /* Largest number of listed teacher entries and largest vocabulary of
  * mbok_distill, its most rows, and floats of statistics per row. */
 #define MBOK_MAX_TOP 1024
@@ -759,6 +839,242 @@ int mbok_distill_backward(const mbok_distill_desc* d, const void* Z, int32_t z_d
                           const int32_t* t_index, int64_t ldt, const float* t_lse,
                           const float* weight, const float* stats, const float* dloss,
                           void* dZ, int32_t dz_dtype, int64_t lddz, void* stream);
+
+/* ------------------------------------------------------------------------
+ * Log-probabilities of a batch's tokens and two losses on them: what follows
+ * distillation when a model is tuned on answers and their value.
+ * ------------------------------------------------------------------------ */
+
+/* Floats of statistics per row of mbok_logp and mbok_policy, and the most pairs
+ * of one mbok_preference call. */
+#define MBOK_LOGP_STATS 4
+#define MBOK_MAX_PAIRS (1 << 23)
+
+/* Rows of logits and the temperature that divides them.  Fill it with
+ * mbok_logp_desc_init. */
+typedef struct mbok_logp_desc {
+  int32_t vocab;     /* V, 1 .. MBOK_MAX_VOCAB */
+  float temperature; /* tau, finite and at least 2^-126 */
+} mbok_logp_desc;
+
+/* Host only.  Errors: INVALID_ARG (NULL, temperature), SHAPE (vocab). */
+int mbok_logp_desc_init(mbok_logp_desc* d, int32_t vocab, float temperature);
+
+/*
+ * logp[t] = z_a / tau - log sum_v exp(z_v / tau) of row t's token a = label[t].
+ * A row whose label is negative or >= V has no token: it is not read, logp 0.
+ * A NaN or +inf among a row's logits, and a row of only -inf, give NaN; z_a =
+ * -inf beside finite logits gives -inf.  Row sums are float64 at the end.
+ *  Z      device [T, ldz] of z_dtype (MBOK_F32, MBOK_F16, MBOK_BF16).
+ *  T      1 .. MBOK_MAX_DISTILL_ROWS.
+ *  label  device int32 [T].
+ *  logp   device fp32 [T]; overwritten.
+ *  stats  device fp32 [T][MBOK_LOGP_STATS] or NULL; overwritten: what
+ *         mbok_logp_backward needs of this pass.  16-byte aligned.
+ * Errors: INVALID_ARG (NULL, ldz), SHAPE (T, the descriptor's), DTYPE, ALIGN (Z to
+ * its element, label and logp 4 bytes, stats 16 bytes), HIP.
+ */
+int mbok_logp(const mbok_logp_desc* d, const void* Z, int32_t z_dtype, int64_t T, int64_t ldz,
+              const int32_t* label, float* logp, float* stats, void* stream);
+
+/*
+ * The logits' gradient of sum_t dlogp[t] logp[t]:
+ *     dZ[t, v] = dlogp[t] / tau ([v = a] - q_v),  q = softmax(z / tau),
+ * after mbok_logp (or mbok_policy) with stats on the same Z, label and descriptor
+ * values.  Rows without a token and rows whose dlogp is 0 are written as 0.
+ * Terms below 2^-126 dlogp / tau of the largest may be written as 0.
+ *  dlogp  device fp32 [T].
+ *  dZ     device [T, lddz] of dz_dtype (z_dtype or MBOK_BF16); overwritten.  May
+ *         be Z itself (same dtype and leading dimension).
+ * Errors: as mbok_logp; INVALID_ARG (lddz), ALIGN (dZ to its element).
+ */
+int mbok_logp_backward(const mbok_logp_desc* d, const void* Z, int32_t z_dtype, int64_t T,
+                       int64_t ldz, const int32_t* label, const float* stats,
+                       const float* dlogp, void* dZ, int32_t dz_dtype, int64_t lddz,
+                       void* stream);
+
+/* Shape and constants of one clipped policy loss.  Fill it with
+ * mbok_policy_desc_init. */
+typedef struct mbok_policy_desc {
+  int32_t vocab;     /* V, 1 .. MBOK_MAX_VOCAB */
+  float temperature; /* tau, finite and at least 2^-126 */
+  float clip_low;    /* the ratio is clipped to 1 - clip_low (0 .. 1) ... */
+  float clip_high;   /* ... and 1 + clip_high (0 or more; may be infinite) */
+  float kl;          /* beta, weight of the KL term, finite, 0 or more */
+} mbok_policy_desc;
+
+/* Host only.  Errors: INVALID_ARG (NULL, a constant out of its range or NaN),
+ * SHAPE (vocab). */
+int mbok_policy_desc_init(mbok_policy_desc* d, int32_t vocab, float temperature,
+                          float clip_low, float clip_high, float kl);
+
+/*
+ * Clipped policy loss with a KL term, per token, and the logits' gradient in the
+ * same pass.  With logp as mbok_logp's and r = exp(logp - old_logp):
+ *     loss[t] = w ( -min(r A, clip(r, 1 - clip_low, 1 + clip_high) A)
+ *                   + beta (exp(x) - x - 1) ),   x = ref_logp - logp
+ *     dlogp[t] = w ( -(r A, or 0 where the clipped side is the smaller)
+ *                    + beta (1 - exp(x)) )
+ *     dZ[t, v] = dlogp[t] / tau ([v = a] - q_v)
+ * r = 1 + clip_high and r = 1 - clip_low count as not clipped.  An advantage of 0
+ * gains nothing at any ratio.  A row without a token has loss, logp and gradient
+ * 0; a row of weight 0 has loss and gradient 0 and is read only where logp or
+ * stats are asked for.  Non-finite logits as for mbok_logp.
+ *  Z, z_dtype, T, ldz, label, logp (or NULL), stats (or NULL): as for mbok_logp.
+ *  advantage  device fp32 [T], A.
+ *  old_logp   device fp32 [T] or NULL: the log-probabilities when the tokens were
+ *             sampled; NULL takes the present ones (r = 1, its slope kept).
+ *  ref_logp   device fp32 [T] or NULL: a reference model's (NULL: no KL term).
+ *  weight     device fp32 [T] or NULL (all 1): w.
+ *  loss       device fp32 [T]; overwritten.
+ *  dlogp      device fp32 [T] or NULL; overwritten: with stats, what
+ *             mbok_logp_backward takes for the gradient alone later.
+ *  dZ         device [T, lddz] of dz_dtype, or NULL, as for mbok_logp_backward:
+ *             the gradient of sum_t loss[t].
+ * Errors: INVALID_ARG (NULL, leading dimensions), SHAPE (T, the descriptor's),
+ * DTYPE, ALIGN (Z and dZ to their element, stats 16 bytes, the others 4), HIP.
+ */
+int mbok_policy(const mbok_policy_desc* d, const void* Z, int32_t z_dtype, int64_t T,
+                int64_t ldz, const int32_t* label, const float* advantage,
+                const float* old_logp, const float* ref_logp, const float* weight, float* loss,
+                float* logp, float* stats, float* dlogp, void* dZ, int32_t dz_dtype,
+                int64_t lddz, void* stream);
+
+/* Constants of one preference loss.  Fill it with mbok_preference_desc_init. */
+typedef struct mbok_preference_desc {
+  float beta;      /* finite, above 0 */
+  float smoothing; /* share of pairs taken to be the wrong way round, 0 .. 0.5 */
+  float margin;    /* what h has to exceed, finite */
+  int32_t mean;    /* 0: sums over a sequence's tokens; else their means */
+  int32_t vocab;   /* labels outside 0 .. vocab - 1 are no tokens */
+} mbok_preference_desc;
+
+/* Host only.  Errors: INVALID_ARG (NULL, a constant out of its range or NaN),
+ * SHAPE (vocab not in 1 .. MBOK_MAX_VOCAB). */
+int mbok_preference_desc_init(mbok_preference_desc* d, float beta, float smoothing,
+                              float margin, int32_t mean, int32_t vocab);
+
+/*
+ * Loss of paired log ratios.  Sequence 2p is pair p's chosen one, 2p + 1 its
+ * rejected one; sequence s is rows offsets[s] .. offsets[s + 1] - 1.  With S_s the
+ * sum (mean) of logp - ref_logp over the sequence's rows that hold a token:
+ *     h = beta (S_2p - S_2p+1) - margin
+ *     loss[p] = w ((1 - smoothing) log(1 + exp(-h)) + smoothing log(1 + exp(h)))
+ *     dlogp[t] = +-w beta (smoothing sig(h) - (1 - smoothing) sig(-h)) (/ tokens)
+ * with + for rows of the chosen sequence and - for the rejected one's; rows
+ * without a token get 0.  A sequence without tokens has S = 0.  Sums are float64.
+ * dlogp goes to mbok_logp_backward; its rows outside every sequence are left as
+ * they were.
+ *  offsets  device int32 [2 pairs + 1], not decreasing, within 0 .. T (values
+ *           outside are cut to that range, a decreasing one to the one before).
+ *  pairs    1 .. MBOK_MAX_PAIRS.
+ *  logp     device fp32 [T], of mbok_logp.
+ *  ref_logp device fp32 [T] or NULL (all 0): the reference model's.
+ *  label    device int32 [T] or NULL (every row holds a token), as for mbok_logp.
+ *  T        1 .. MBOK_MAX_DISTILL_ROWS.
+ *  weight   device fp32 [pairs] or NULL (all 1): w.  A pair of weight 0 has loss
+ *           and dlogp 0.
+ *  loss     device fp32 [pairs]; overwritten.
+ *  dlogp    device fp32 [T] or NULL.
+ * Errors: INVALID_ARG (NULL, the descriptor's constants), SHAPE (T, pairs, the
+ * descriptor's), ALIGN (4 bytes each), HIP.
+ */
+int mbok_preference(const mbok_preference_desc* d, const int32_t* offsets, int64_t pairs,
+                    const float* logp, const float* ref_logp, const int32_t* label, int64_t T,
+                    const float* weight, float* loss, float* dlogp, void* stream);
+
+/* ------------------------------------------------------------------------
+ * The optimizer step ([RN] 训练策略: the scales are tuned).
+ * ------------------------------------------------------------------------ */
+
+/* Values of an 8-bit state that share a scale, and limits of one plan. */
+#define MBOK_ADAMW_BLOCK 256
+#define MBOK_MAX_ADAMW_TENSORS 65536
+#define MBOK_MAX_ADAMW_VALUES ((int64_t)1 << 32)
+
+/*
+ * One tensor of a step.  All pointers are device memory.
+ *  param        fp32 [count], updated: the master values.
+ *  grad         [count] of grad_dtype (MBOK_F32, MBOK_F16, MBOK_BF16).
+ *  state_dtype  MBOK_F32: m and v fp32 [count], the moments; m_scale, v_scale NULL.
+ *               MBOK_E4M3: m and v are codes [count], m_scale and v_scale fp32
+ *               [ceil(count / MBOK_ADAMW_BLOCK)]: the first moment is m m_scale
+ *               and the SQUARE ROOT of the second v v_scale of the value's
+ *               block.  Zeros are the states before the first step, either way.
+ *  layer        NULL: out is NULL or a flat copy of the new values [count] of
+ *               out_dtype (MBOK_F32, MBOK_F16, MBOK_BF16).  Else the descriptor of
+ *               a layer (read by mbok_adamw_plan_init alone): param are its
+ *               scales in mbok_pack's order [K][m][n/128], count = K m n/128, and
+ *               out is its packed buffer, in which the step writes the scales, in
+ *               the layer's alpha_dtype (rounded once; no signs and no padding
+ *               are touched).  out_dtype is not read then.
+ *  weight_decay wd, finite, 0 or more.
+ */
+typedef struct mbok_adamw_tensor {
+  float* param;
+  const void* grad;
+  void* m;
+  void* v;
+  float* m_scale;
+  float* v_scale;
+  void* out;
+  const mbok_desc* layer;
+  int64_t count;
+  double weight_decay;
+  int32_t grad_dtype, state_dtype, out_dtype;
+} mbok_adamw_tensor;
+
+/* What mbok_adamw needs of a set of tensors beside the table. */
+typedef struct mbok_adamw_plan {
+  int64_t table_bytes;
+  int32_t tensors, parts, lds_bytes;
+} mbok_adamw_plan;
+
+/* Bytes of the table of n tensors; 0 if mbok_adamw_plan_init would refuse them.
+ * Host only. */
+size_t mbok_adamw_table_bytes(const mbok_adamw_tensor* tensors, int32_t n);
+
+/*
+ * Fills *plan and the table of n tensors (1 .. MBOK_MAX_ADAMW_TENSORS), in HOST
+ * memory of mbok_adamw_table_bytes(tensors, n) bytes; the caller copies it to the
+ * device.  Host only.  Errors: INVALID_ARG (NULL; a pointer missing or, of
+ * scales, given without 8-bit states; weight_decay; count < 1; two written
+ * ranges, of one tensor or of two, that overlap, or one written that is another's
+ * gradient), SHAPE (n; more than MBOK_MAX_ADAMW_VALUES values; count is not the
+ * layer's), DTYPE, ALIGN (each pointer to its element, out of a layer 16 bytes),
+ * and the layer descriptor's.
+ */
+int mbok_adamw_plan_init(mbok_adamw_plan* plan, const mbok_adamw_tensor* tensors, int32_t n,
+                         void* table);
+
+/* Constants of one step. */
+typedef struct mbok_adamw_step {
+  double lr, beta1, beta2, eps; /* finite; beta in [0, 1), eps at least 2^-126 */
+  int64_t step;                 /* t, 1 for the first, below 2^53 */
+  float grad_scale;             /* c: gradients are multiplied by it */
+  uint32_t seed;                /* of the stochastic rounding of 8-bit states */
+} mbok_adamw_step;
+
+/*
+ * One step of AdamW on every tensor of a plan, in one kernel:
+ *     g' = c g,  m = beta1 m + (1 - beta1) g',  v = beta2 v + (1 - beta2) g'^2
+ *     p = p (1 - lr wd) - lr / (1 - beta1^t) m / (sqrt(v) / sqrt(1 - beta2^t) + eps)
+ * in fp32; the same inputs give the same bits.  8-bit states are rounded
+ * stochastically to e4m3 with a power-of-two scale per block that puts its
+ * largest magnitude in [128, 256); the random bits are a hash of seed, t, the
+ * tensor's place in the plan and the value's.  A value that is not finite makes
+ * its block's scale NaN.  A root of the second moment that is not 0 never becomes
+ * 0.  Scales are at least 2^-87.
+ *  table  device, the plan's table, 16-byte aligned.
+ *  live   device fp32 [4] or NULL: lr, grad_scale, t (a whole number below 2^24)
+ *         and a flag, read when the step runs (so that a captured step follows
+ *         them) instead of the constants of `step`; a flag other than 0 (an
+ *         overflow was found) skips the step: nothing is written.
+ * Errors: INVALID_ARG (NULL, constants out of range, a plan that is none), ALIGN
+ * (table 16 bytes, live 4), HIP.
+ */
+int mbok_adamw(const mbok_adamw_plan* plan, const void* table, const mbok_adamw_step* step,
+               const float* live, void* stream);
 
 /* Static description of a status code ("unknown status" for others). */
 const char* mbok_status_str(int status);
