@@ -89,13 +89,25 @@ __global__ void __launch_bounds__(kThreads) linear_backward_kernel(
   *out = accumulate ? *out + total : total;
 }
 
+// Adds the slices' sums: 32 columns per workgroup, whose 8 rows of threads take
+// every eighth slice each.
+constexpr int kJoinColumns = 32;
 __global__ void __launch_bounds__(256) bias_join_kernel(const float* __restrict__ sums, int slices,
                                                         int m, float* __restrict__ dbias,
                                                         int accumulate) {
-  const int c = (int)(blockIdx.x * 256 + threadIdx.x);
-  if (c >= m) return;
+  __shared__ float part[8][kJoinColumns];
+  const int x = threadIdx.x % kJoinColumns, y = threadIdx.x / kJoinColumns;
+  const int c = (int)blockIdx.x * kJoinColumns + x;
   float total = 0.f;
-  for (int i = 0; i < slices; ++i) total += sums[(int64_t)i * m + c];
+  if (c < m) {
+#pragma unroll 4
+    for (int i = y; i < slices; i += 8) total += sums[(int64_t)i * m + c];
+  }
+  part[y][x] = total;
+  __syncthreads();
+  if (y || c >= m) return;
+#pragma unroll
+  for (int i = 1; i < 8; ++i) total += part[i][x];
   dbias[c] = accumulate ? dbias[c] + total : total;
 }
 
@@ -155,8 +167,8 @@ int launch_linear_backward(const mbok_desc* d, const void* packed, const LinearG
     else if (g.dbias) go(linear_backward_kernel<true, true>);
     else go(linear_backward_kernel<true, false>);
     if (g.dbias && s.slices > 1)
-      hipLaunchKernelGGL(bias_join_kernel, dim3((d->m + 255) / 256), dim3(256), 0, stream, sums,
-                         s.slices, d->m, g.dbias, accumulate);
+      hipLaunchKernelGGL(bias_join_kernel, dim3((d->m + kJoinColumns - 1) / kJoinColumns),
+                         dim3(256), 0, stream, sums, s.slices, d->m, g.dbias, accumulate);
     if (hipGetLastError() != hipSuccess) return MBOK_ERR_HIP;
   }
   if (!g.dX) return MBOK_OK;

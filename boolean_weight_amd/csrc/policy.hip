@@ -14,9 +14,7 @@
 //
 // Bound: the row of logits, read once and (gradient) written once.  As in the
 // distillation loss one workgroup takes a row and keeps it in registers, so
-// maximum, sum and gradient cost one read.  The exponentials of the sum are
-// kept in fp32 and become the gradient by one product, half the
-// transcendental work of taking them again.
+// maximum, sum and gradient cost one read.
 // The ratio stands next to a border (1 + hi), so what is formed from the row's
 // sum is float64.
 #include <math.h>
@@ -43,6 +41,7 @@ static_assert(sizeof(RowStats) == MBOK_LOGP_STATS * sizeof(float), "stats row");
 struct RowShape {
   int V;
   float tau, c;  // c = log2(e) / tau
+  bool stream;   // gradient rows start 16-byte aligned (see store_row)
 };
 
 // Reduction buffers of one row's workgroup.
@@ -52,11 +51,37 @@ struct RowLds {
   float slope, inv_sum, rest;
 };
 
-// exp((z - zmax) / tau) of a vector
-template <typename T, int N>
-__device__ __forceinline__ void exps(const RowVec<T>& x, float zmax, float c, float (&e)[N]) {
+// exp((z - zmax) / tau) of a vector.  The scaled argument is one fma, z c - k with
+// k = zmax c rounded, where k is small (the factor 2^(zmax c - k) that all
+// exponentials of the row then lack is 1 to 2^-17, and is put back where their
+// sum is used alone), else subtracted first.
+struct Exps {
+  float zmax, c, k;
+  bool near;
+  __device__ __forceinline__ Exps(float zmax_, float c_)
+      : zmax(zmax_), c(c_), k(zmax_ * c_), near(fabsf(k) < 256.f) {}
+  // log of the row's sum of true exponentials from the sum of these
+  __device__ __forceinline__ double log_sum(double S) const {
+    const double fix = near ? (double)kLn2 * ((double)k - (double)zmax * (double)c) : 0.0;
+    return log(S) + fix;
+  }
+  template <typename T, int N>
+  __device__ __forceinline__ void operator()(const RowVec<T>& x, float (&e)[N]) const {
+    if (near) {
 #pragma unroll
-  for (int i = 0; i < N; ++i) e[i] = __builtin_amdgcn_exp2f(((float)x.v[i] - zmax) * c);
+      for (int i = 0; i < N; ++i) e[i] = __builtin_amdgcn_exp2f(fmaf(x.at(i), c, -k));
+    } else {
+#pragma unroll
+      for (int i = 0; i < N; ++i) e[i] = __builtin_amdgcn_exp2f((x.at(i) - zmax) * c);
+    }
+  }
+};
+
+// the larger of three, NaN dropped (fmaxf quiets its operands first)
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("v_max3_f32 %0, %1, %2, %3" : "=v"(r) : "v"(a), "v"(b), "v"(c));
+  return r;
 }
 
 // What the first wavefront forms of a row: log-probability, loss and its slope.
@@ -90,8 +115,8 @@ struct Policy {
 struct NoLoss {};
 
 // LOSS: Policy or NoLoss (log-probabilities alone).  GRAD: with dZ.
-template <typename ZT, typename OT, int NV, bool GRAD, typename Loss>
-__global__ void __launch_bounds__(kMaxThreads) row_kernel(
+template <typename ZT, typename OT, int NV, int THREADS, bool GRAD, typename Loss>
+__global__ void __launch_bounds__(THREADS, NV <= 8 ? 8 : 4) row_kernel(
     const ZT* Z, int64_t ldz, const int32_t* __restrict__ label, RowShape s,
     float* __restrict__ logp_out, RowStats* __restrict__ stats, OT* dZ, int64_t lddz, Loss loss) {
   constexpr int N = RowVec<ZT>::N;
@@ -109,7 +134,7 @@ __global__ void __launch_bounds__(kMaxThreads) row_kernel(
   if constexpr (POLICY) w = loss.weight ? loss.weight[t] : 1.f;
   auto zeros = [&] {
     const float zero[N] = {};
-    for (int v = tid; v < nvec; v += nt) store_row<OT, N>(drow, v, s.V, zero);
+    for (int v = tid; v < nvec; v += nt) store_row<OT, N>(drow, v, s.V, zero, s.stream);
   };
 
   // a row without a token, or one that nothing is asked of
@@ -140,7 +165,7 @@ __global__ void __launch_bounds__(kMaxThreads) row_kernel(
   float top = -INFINITY;
   auto max_of = [&](const RowVec<ZT>& x) {
 #pragma unroll
-    for (int e = 0; e < N; ++e) top = fmaxf(top, (float)x.v[e]);
+    for (int e = 0; e < N; e += 2) top = max3(top, x.at(e), x.at(e + 1));
   };
   if (NV > 0) {
 #pragma unroll
@@ -155,29 +180,25 @@ __global__ void __launch_bounds__(kMaxThreads) row_kernel(
   top = lds.top[0];
   for (int i = 1; i < nw; ++i) top = fmaxf(top, lds.top[i]);
 
-  // sum of exponentials; a thread adds at most 8 NV <= 128 terms in fp32
-  constexpr bool KEEP = GRAD && NV > 0 && NV * N <= 32;
-  float kept[KEEP ? NV : 1][N];
-  float part = 0.f;
+  // sum of exponentials; a thread adds at most 128 terms in fp32
+  const Exps exps(top, s.c);
   double sum = 0.0;
   if (NV > 0) {
+    float part = 0.f;
 #pragma unroll
     for (int u = 0; u < NV; ++u) {
       if (tid + u * nt >= nvec) continue;
+      held[u].forget();
       float e[N];
-      exps(held[u], top, s.c, e);
+      exps(held[u], e);
 #pragma unroll
-      for (int i = 0; i < N; ++i) {
-        part += e[i];
-        if (KEEP) kept[u][i] = e[i];
-      }
+      for (int i = 0; i < N; ++i) part += e[i];
     }
     sum = (double)part;
   } else {
     for (int v = tid; v < nvec; v += nt) {
-      float e[N];
-      exps(load_row(row, v, s.V), top, s.c, e);
-      part = 0.f;
+      float e[N], part = 0.f;
+      exps(load_row(row, v, s.V), e);
 #pragma unroll
       for (int i = 0; i < N; ++i) part += e[i];
       sum += (double)part;
@@ -190,7 +211,7 @@ __global__ void __launch_bounds__(kMaxThreads) row_kernel(
   if (wave == 0) {
     double S = 0.0;
     for (int i = 0; i < nw; ++i) S += lds.sum[i];
-    const double logp = ((double)za - (double)top) / (double)s.tau - log(S);
+    const double logp = ((double)za - (double)top) / (double)s.tau - exps.log_sum(S);
     const float rest = (float)-expm1(logp);
     if (lane == 0) {
       if (logp_out) logp_out[t] = (float)logp;
@@ -225,26 +246,22 @@ __global__ void __launch_bounds__(kMaxThreads) row_kernel(
       for (int i = 0; i < N; ++i)
         if (i == a % N) e[i] = A * lds.rest;
     }
-    store_row<OT, N>(drow, v, s.V, e);
+    store_row<OT, N>(drow, v, s.V, e, s.stream);
   };
   if (NV > 0) {
 #pragma unroll
     for (int u = 0; u < NV; ++u) {
       const int v = tid + u * nt;
       if (v >= nvec) continue;
+      held[u].forget();
       float e[N];
-      if (KEEP) {
-#pragma unroll
-        for (int i = 0; i < N; ++i) e[i] = kept[KEEP ? u : 0][i];
-      } else {
-        exps(held[u], top, s.c, e);
-      }
+      exps(held[u], e);
       put(v, e);
     }
   } else {
     for (int v = tid; v < nvec; v += nt) {
       float e[N];
-      exps(load_row(row, v, s.V), top, s.c, e);
+      exps(load_row(row, v, s.V), e);
       put(v, e);
     }
   }
@@ -265,14 +282,15 @@ __global__ void __launch_bounds__(kMaxThreads) logp_backward_kernel(
   const float g = dlogp[t];
   if (a < 0 || a >= s.V || g == 0.f) {
     const float zero[N] = {};
-    for (int v = tid; v < nvec; v += nt) store_row<OT, N>(drow, v, s.V, zero);
+    for (int v = tid; v < nvec; v += nt) store_row<OT, N>(drow, v, s.V, zero, s.stream);
     return;
   }
   const RowStats st = stats[t];
+  const Exps exps(st.zmax, s.c);
   const float A = g / s.tau, f = -A * st.inv_sum;
   for (int v = tid; v < nvec; v += nt) {
     float e[N];
-    exps(load_row(row, v, s.V), st.zmax, s.c, e);
+    exps(load_row(row, v, s.V), e);
 #pragma unroll
     for (int i = 0; i < N; ++i) e[i] *= f;
     if (v == a / N) {
@@ -280,7 +298,7 @@ __global__ void __launch_bounds__(kMaxThreads) logp_backward_kernel(
       for (int i = 0; i < N; ++i)
         if (i == a % N) e[i] = A * st.rest;
     }
-    store_row<OT, N>(drow, v, s.V, e);
+    store_row<OT, N>(drow, v, s.V, e, s.stream);
   }
 }
 
@@ -346,12 +364,14 @@ __global__ void __launch_bounds__(kPairThreads) preference_kernel(
   }
 }
 
-RowShape shape_of(int V, float tau) {
-  return RowShape{V, tau, (float)(1.4426950408889634074 / (double)tau)};
+RowShape shape_of(int V, float tau, const RowArgs& a) {
+  const int size = a.dz_dtype == MBOK_F32 ? 4 : 2;
+  const bool stream = ((uintptr_t)a.dZ & 15) == 0 && (a.lddz * size) % 16 == 0;
+  return RowShape{V, tau, (float)(1.4426950408889634074 / (double)tau), stream};
 }
 
-// Threads of a row's workgroup for `want` vectors each, 256 to 1024; a launch has
-// fewer than 2^32 threads (256 for each of MBOK_MAX_DISTILL_ROWS rows are 2^31).
+// Threads of a row's workgroup for `want` vectors each, 256 to 1024 (256 for each
+// of MBOK_MAX_DISTILL_ROWS rows are 2^31).
 int row_threads(int64_t T, int nvec, int want) {
   int threads = 256;
   while (threads < kMaxThreads && threads * want < nvec && T * threads * 2 <= UINT32_MAX)
@@ -359,23 +379,45 @@ int row_threads(int64_t T, int nvec, int want) {
   return threads;
 }
 
+// A row's workgroup: with many rows the fewest threads that hold it in 8 vectors
+// each (4 resident rows per compute unit hide one another's reductions: 1024 x
+// 32000 bf16 logits, policy step, 27.7 us with 512 threads, 30.5 with 1024); with
+// few the fewest that do in 4 (32000 bf16, 64 rows 8.9 us with 1024 threads, 10.4
+// with 512; 16000, 301 rows 9.5 with 512, 9.9 with 1024 of 2 vectors).
 template <typename ZT, typename OT, bool GRAD, typename Loss>
 int launch_rows(const RowArgs& a, const RowShape& s, float* logp, float* stats, const Loss& loss,
                 hipStream_t stream) {
   const int nvec = (s.V + RowVec<ZT>::N - 1) / RowVec<ZT>::N;
-  const int threads = row_threads(a.T, nvec, a.T < 512 ? 2 : 4);
-  const int per = (nvec + threads - 1) / threads;
-  auto go = [&](auto nv) {
-    hipLaunchKernelGGL((row_kernel<ZT, OT, decltype(nv)::value, GRAD, Loss>), dim3((unsigned)a.T),
-                       dim3(threads), 0, stream, reinterpret_cast<const ZT*>(a.Z), a.ldz, a.label,
-                       s, logp, reinterpret_cast<RowStats*>(stats),
-                       reinterpret_cast<OT*>(a.dZ), a.lddz, loss);
+  auto go = [&](auto nv, auto threads) {
+    hipLaunchKernelGGL(
+        (row_kernel<ZT, OT, decltype(nv)::value, decltype(threads)::value, GRAD, Loss>),
+        dim3((unsigned)a.T), dim3(decltype(threads)::value), 0, stream,
+        reinterpret_cast<const ZT*>(a.Z), a.ldz, a.label, s, logp,
+        reinterpret_cast<RowStats*>(stats), reinterpret_cast<OT*>(a.dZ), a.lddz, loss);
   };
-  if (per <= 2) go(std::integral_constant<int, 2>{});
-  else if (per <= 4) go(std::integral_constant<int, 4>{});
-  else if (per <= 8) go(std::integral_constant<int, 8>{});
-  else if (per <= 16) go(std::integral_constant<int, 16>{});
-  else go(std::integral_constant<int, 0>{});
+  auto row = [&](auto threads, auto nv) {
+    constexpr int64_t n = decltype(threads)::value;
+    if (nvec > n * decltype(nv)::value || a.T * n > UINT32_MAX) return false;
+    go(nv, threads);
+    return true;
+  };
+  using std::integral_constant;
+  const integral_constant<int, 256> t256;
+  const integral_constant<int, 512> t512;
+  const integral_constant<int, 1024> t1024;
+  const integral_constant<int, 2> v2;
+  const integral_constant<int, 4> v4;
+  const integral_constant<int, 8> v8;
+  const integral_constant<int, 16> v16;
+  const integral_constant<int, 0> again;
+  const bool many = a.T >= 512;
+  if (row(t256, v2) || row(t256, v4) || (many && row(t256, v8)) || row(t512, v4) ||
+      (many && row(t512, v8)) || row(t1024, v4) || row(t1024, v8) || row(t1024, v16)) {
+  } else if (a.T * 1024 <= UINT32_MAX) {
+    go(again, t1024);
+  } else {  // a launch has fewer than 2^32 threads
+    go(again, t256);
+  }
   return hipGetLastError() == hipSuccess ? MBOK_OK : MBOK_ERR_HIP;
 }
 
@@ -394,7 +436,7 @@ int by_types(const RowArgs& a, F&& f) {
 
 int launch_logp(const mbok_logp_desc* d, const RowArgs& a, float* logp, float* stats,
                 hipStream_t stream) {
-  const RowShape s = shape_of(d->vocab, d->temperature);
+  const RowShape s = shape_of(d->vocab, d->temperature, a);
   auto go = [&](auto z) {
     return launch_rows<decltype(z), decltype(z), false>(a, s, logp, stats, NoLoss{}, stream);
   };
@@ -408,7 +450,7 @@ int launch_logp(const mbok_logp_desc* d, const RowArgs& a, float* logp, float* s
 int launch_policy(const mbok_policy_desc* d, const RowArgs& a, const float* advantage,
                   const float* old_logp, const float* ref_logp, const float* weight, float* loss,
                   float* logp, float* stats, float* dlogp, hipStream_t stream) {
-  const RowShape s = shape_of(d->vocab, d->temperature);
+  const RowShape s = shape_of(d->vocab, d->temperature, a);
   const Policy p = {advantage, old_logp, ref_logp, weight, 1.0 - (double)d->clip_low,
                     1.0 + (double)d->clip_high, d->kl, loss, dlogp};
   return by_types(a, [&](auto z, auto o) {
@@ -419,7 +461,7 @@ int launch_policy(const mbok_policy_desc* d, const RowArgs& a, const float* adva
 
 int launch_logp_backward(const mbok_logp_desc* d, const RowArgs& a, const float* stats,
                          const float* dlogp, hipStream_t stream) {
-  const RowShape s = shape_of(d->vocab, d->temperature);
+  const RowShape s = shape_of(d->vocab, d->temperature, a);
   return by_types(a, [&](auto z, auto o) {
     using ZT = decltype(z);
     using OT = decltype(o);
