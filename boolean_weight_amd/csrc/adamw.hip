@@ -19,9 +19,11 @@
 // lies in [128, 256) of e4m3's 448.  The second moment is kept as r = sqrt(v),
 // which halves the range it needs.  Codes are rounded stochastically: a step
 // moves v by a thousandth, half an e4m3 step is a sixteenth to a thirty-second,
-// so nearest rounding would leave most of them where they are; the expected
-// value of a code is the value.  A value r that is not 0 keeps code 1 at least,
-// so that no m is divided by eps alone.
+// so nearest rounding would leave most of them where they are.  The expected
+// value of a code is the value: r, which the update divides by, follows its
+// decay in the mean (its square up to a sixteenth slower, by the codes'
+// variance).  A value r that is not 0 keeps code 1 at least, so that no m is
+// divided by eps alone.
 #include <math.h>
 
 #include <algorithm>
@@ -340,7 +342,7 @@ __device__ __forceinline__ void update_layer(const AdamTensor& t, const Rule& ru
     int row = (int)((uint32_t)(first + i) / (uint32_t)G), g = first + i - row * G;
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      if (e < live) lds[row * pitch + g] = p[e];
+      if (e < live) lds[row * pitch + g - first] = p[e];
       if (++g == G) {
         g = 0;
         ++row;
@@ -357,7 +359,7 @@ __device__ __forceinline__ void update_layer(const AdamTensor& t, const Rule& ru
     // the part's values of this row: groups g0 .. g1
     const int g0 = r == 0 ? first : 0, g1 = min(G, first + len - r * G);
     for (int g = g0 + wave; g < g1; g += kThreads / kWave) {
-      const float p = lds[r * pitch + g];
+      const float p = lds[r * pitch + g - first];
       AT* at = dst + (int64_t)g * t.kernels * kRowBlock;
       if constexpr (sizeof(AT) == 2) *at = (AT)p;
       else *at = p;
@@ -418,8 +420,9 @@ int adamw_part(int64_t values) {
   return part;
 }
 
-// LDS of a part of a layer of G groups
-int adamw_layer_lds(int G, int part) { return ((part + G - 1) / G + 1) * (G | 1) * 4; }
+// LDS of a part of a layer of G groups: its values, a word between rows where G is
+// even (a part meets at most (part - 2) / G + 2 rows)
+int adamw_layer_lds(int G, int part) { return (part + (part + G - 1) / G + 1) * 4; }
 
 int launch_adamw(const mbok_adamw_plan* plan, const void* table, const mbok_adamw_step* step,
                  const float* live, hipStream_t stream) {
