@@ -34,6 +34,7 @@
 #include "mbok_device.h"
 #include "mbok_launch.h"
 #include "mbok_levels.h"
+#include "mbok_sums.h"
 
 namespace mbok {
 namespace {
@@ -396,11 +397,16 @@ __global__ void __launch_bounds__(kThreads) gemmt_kernel(
 }
 
 // The tiles that were sliced: the slices' partial sums added in order and rounded
-// once; 4 columns per thread.
+// once; 4 columns per thread.  Blocks past theirs take a caller's column sums.
 __global__ void __launch_bounds__(256) gemmt_reduce_kernel(const float* __restrict__ part,
                                                            uint16_t* __restrict__ dX,
                                                            int64_t lddx, int T, int n, int bt,
-                                                           int full, int rest, int slices) {
+                                                           int full, int rest, int slices,
+                                                           ColumnSums sums) {
+  if ((int)blockIdx.y >= rest) {
+    column_sums(sums, ((int)blockIdx.y - rest) * (int)gridDim.x + (int)blockIdx.x);
+    return;
+  }
   // a block takes 4 rows of one tile; all offsets are below kUnits tiles' worth
   const int idx = blockIdx.y, rows = min(T, bt), stride = rest * rows * kBN;
   const int row = blockIdx.x * 4 + (threadIdx.x >> 6), col = (threadIdx.x & 63) * 4;
@@ -424,6 +430,10 @@ __global__ void __launch_bounds__(256) gemmt_reduce_kernel(const float* __restri
   if (t >= T || j >= n) return;
   *reinterpret_cast<uint2*>(dX + (int64_t)t * lddx + j) =
       make_uint2(bf16_pair(s[0], s[1]), bf16_pair(s[2], s[3]));
+}
+
+__global__ void __launch_bounds__(256) column_sums_kernel(ColumnSums sums) {
+  column_sums(sums, (int)blockIdx.x);
 }
 
 constexpr int kUnits = 256;  // workgroups that fill the part (one per compute unit)
@@ -471,7 +481,7 @@ Split gemmt_split(const Geom& geo, int64_t T, bool workspace) {
 template <typename AT, int K>
 int launch_k(const Geom& geo, const void* packed, const uint16_t* dY, int64_t T, int64_t lddy,
              uint16_t* dX, int64_t lddx, float* part, const Split& s, bool two,
-             hipStream_t stream) {
+             const ColumnSums* sums, hipStream_t stream) {
   // straight copies to LDS take 16-byte aligned rows at 32-bit offsets
   const bool aligned =
       ((uintptr_t)dY & 15) == 0 && (lddy % 8) == 0 && lddy < (int64_t(1) << 32) / 512;
@@ -504,22 +514,27 @@ int launch_k(const Geom& geo, const void* packed, const uint16_t* dY, int64_t T,
   }
   if (s.slices > 1) {
     const int rows = T < s.bt ? (int)T : s.bt;
-    hipLaunchKernelGGL(gemmt_reduce_kernel, dim3((rows + 3) / 4, s.rest), dim3(256), 0, stream,
-                       part, dX, lddx, (int)T, geo.n, s.bt, s.full, s.rest, s.slices);
+    const int per = (rows + 3) / 4, more = sums ? (sum_blocks(*sums) + per - 1) / per : 0;
+    hipLaunchKernelGGL(gemmt_reduce_kernel, dim3(per, s.rest + more), dim3(256), 0, stream, part,
+                       dX, lddx, (int)T, geo.n, s.bt, s.full, s.rest, s.slices,
+                       sums ? *sums : ColumnSums{});
+  } else if (sums) {
+    return launch_column_sums(*sums, stream);
   }
   return hipGetLastError() == hipSuccess ? MBOK_OK : MBOK_ERR_HIP;
 }
 
 template <typename AT>
 int launch_t(const Geom& geo, const void* packed, const void* dY, int64_t T, int64_t lddy,
-             void* dX, int64_t lddx, float* part, const Split& s, bool two, hipStream_t stream) {
+             void* dX, int64_t lddx, float* part, const Split& s, bool two,
+             const ColumnSums* sums, hipStream_t stream) {
   const uint16_t* g = reinterpret_cast<const uint16_t*>(dY);
   uint16_t* o = reinterpret_cast<uint16_t*>(dX);
   switch (geo.K) {
-    case 1: return launch_k<AT, 1>(geo, packed, g, T, lddy, o, lddx, part, s, two, stream);
-    case 2: return launch_k<AT, 2>(geo, packed, g, T, lddy, o, lddx, part, s, two, stream);
-    case 3: return launch_k<AT, 3>(geo, packed, g, T, lddy, o, lddx, part, s, two, stream);
-    default: return launch_k<AT, 4>(geo, packed, g, T, lddy, o, lddx, part, s, two, stream);
+    case 1: return launch_k<AT, 1>(geo, packed, g, T, lddy, o, lddx, part, s, two, sums, stream);
+    case 2: return launch_k<AT, 2>(geo, packed, g, T, lddy, o, lddx, part, s, two, sums, stream);
+    case 3: return launch_k<AT, 3>(geo, packed, g, T, lddy, o, lddx, part, s, two, sums, stream);
+    default: return launch_k<AT, 4>(geo, packed, g, T, lddy, o, lddx, part, s, two, sums, stream);
   }
 }
 
@@ -530,15 +545,21 @@ size_t gemmt_workspace_bytes(const mbok_desc* d, int64_t T) {
   return s.slices > 1 ? (size_t)s.rest * s.slices * (T < s.bt ? T : s.bt) * kBN * sizeof(float) : 0;
 }
 
+int launch_column_sums(const ColumnSums& sums, hipStream_t stream) {
+  hipLaunchKernelGGL(column_sums_kernel, dim3(sum_blocks(sums)), dim3(256), 0, stream, sums);
+  return hipGetLastError() == hipSuccess ? MBOK_OK : MBOK_ERR_HIP;
+}
+
 int launch_gemmt(const mbok_desc* d, const void* packed, const void* dY, int64_t T, int64_t lddy,
-                 void* dX, int64_t lddx, void* ws, int passes, hipStream_t stream) {
+                 void* dX, int64_t lddx, void* ws, int passes, hipStream_t stream,
+                 const ColumnSums* sums) {
   const Geom geo = make_geom(d);
   const Split s = gemmt_split(geo, T, ws != nullptr);
   float* part = reinterpret_cast<float*>(ws);
   const bool two = passes == 2;
   if (d->alpha_dtype == MBOK_F16)
-    return launch_t<uint16_t>(geo, packed, dY, T, lddy, dX, lddx, part, s, two, stream);
-  return launch_t<float>(geo, packed, dY, T, lddy, dX, lddx, part, s, two, stream);
+    return launch_t<uint16_t>(geo, packed, dY, T, lddy, dX, lddx, part, s, two, sums, stream);
+  return launch_t<float>(geo, packed, dY, T, lddy, dX, lddx, part, s, two, sums, stream);
 }
 
 }  // namespace mbok

@@ -10,6 +10,7 @@
 #include "mbok_launch.h"
 #include "mbok_levels.h"
 #include "mbok_linear.h"
+#include "mbok_sums.h"
 
 namespace mbok {
 namespace {
@@ -89,30 +90,8 @@ __global__ void __launch_bounds__(kThreads) linear_backward_kernel(
   *out = accumulate ? *out + total : total;
 }
 
-// Adds the slices' sums: 32 columns per workgroup, whose 8 rows of threads take
-// every eighth slice each.
-constexpr int kJoinColumns = 32;
-__global__ void __launch_bounds__(256) bias_join_kernel(const float* __restrict__ sums, int slices,
-                                                        int m, float* __restrict__ dbias,
-                                                        int accumulate) {
-  __shared__ float part[8][kJoinColumns];
-  const int x = threadIdx.x % kJoinColumns, y = threadIdx.x / kJoinColumns;
-  const int c = (int)blockIdx.x * kJoinColumns + x;
-  float total = 0.f;
-  if (c < m) {
-#pragma unroll 4
-    for (int i = y; i < slices; i += 8) total += sums[(int64_t)i * m + c];
-  }
-  part[y][x] = total;
-  __syncthreads();
-  if (y || c >= m) return;
-#pragma unroll
-  for (int i = 1; i < 8; ++i) total += part[i][x];
-  dbias[c] = accumulate ? dbias[c] + total : total;
-}
-
-// Slices of the rows: about 1500 workgroups, of at least 64 rows each, so that
-// the sums of up to 127 rows need no second kernel; with a workspace only.
+// Slices of the rows: about 1500 workgroups, of at least 64 rows each; more than
+// one slice needs a workspace for its sums.
 struct RowSplit {
   int slices, step;
 };
@@ -141,39 +120,51 @@ int launch_linear(const mbok_desc* d, const void* packed, const void* X, int64_t
   return launch_linear_skinny(d, packed, X, T, ldx, out, stream);
 }
 
+// the product's partial sums, then the slices' sums of dbias, which its last kernel
+// adds
+size_t product_bytes(const mbok_desc* d, int64_t T) {
+  return (gemmt_workspace_bytes(d, T) + 255) / 256 * 256;
+}
+
 size_t linear_backward_workspace_bytes(const mbok_desc* d, int64_t T) {
   const RowSplit s = row_split(d->m, T, false);
-  const size_t sums = s.slices > 1 ? (size_t)s.slices * d->m * sizeof(float) : 0;
-  const size_t product = gemmt_workspace_bytes(d, T);
-  return sums > product ? sums : product;
+  if (s.slices == 1) return gemmt_workspace_bytes(d, T);
+  return product_bytes(d, T) + (size_t)s.slices * d->m * sizeof(float);
 }
 
 int launch_linear_backward(const mbok_desc* d, const void* packed, const LinearGrad& g, int64_t T,
                            int act, int accumulate, void* ws, int passes, hipStream_t stream) {
   const bool with_act = act != MBOK_ACT_NONE;
-  if (with_act || g.dbias) {
-    // without a sum the rows split freely
-    const RowSplit s = row_split(d->m, T, g.dbias && !ws);
-    float* sums = s.slices > 1 ? reinterpret_cast<float*>(ws) : g.dbias;
-    const int add = s.slices > 1 ? 0 : accumulate;
+  // without a sum the rows split freely
+  const RowSplit s = row_split(d->m, T, g.dbias && !ws);
+  const bool sliced = s.slices > 1;
+  // what is left of dbias after the first kernel: the slices' sums, or the rows of dY
+  // themselves where they are few and need no pass of their own
+  ColumnSums tail = {g.dY, g.lddy, 1, (int)T, d->m, accumulate, g.dbias};
+  bool has_tail = g.dbias && !with_act && !sliced;
+  if (with_act || (g.dbias && sliced)) {
+    float* sums = sliced && g.dbias
+                      ? reinterpret_cast<float*>(reinterpret_cast<char*>(ws) + product_bytes(d, T))
+                      : g.dbias;
     auto go = [&](auto kernel) {
       hipLaunchKernelGGL(kernel, dim3((d->m + kColumns - 1) / kColumns, s.slices), dim3(kThreads),
                          0, stream, reinterpret_cast<const uint16_t*>(g.pre), g.ldpre,
                          reinterpret_cast<const uint16_t*>(g.dY), g.lddy,
                          reinterpret_cast<uint16_t*>(g.dpre), g.lddpre, T, s.step, d->m, act, sums,
-                         add);
+                         sliced ? 0 : accumulate);
     };
     if (!with_act) go(linear_backward_kernel<false, true>);
     else if (g.dbias) go(linear_backward_kernel<true, true>);
     else go(linear_backward_kernel<true, false>);
-    if (g.dbias && s.slices > 1)
-      hipLaunchKernelGGL(bias_join_kernel, dim3((d->m + kJoinColumns - 1) / kJoinColumns),
-                         dim3(256), 0, stream, sums, s.slices, d->m, g.dbias, accumulate);
     if (hipGetLastError() != hipSuccess) return MBOK_ERR_HIP;
+    if (g.dbias && sliced) {
+      tail = {sums, d->m, 0, s.slices, d->m, accumulate, g.dbias};
+      has_tail = true;
+    }
   }
-  if (!g.dX) return MBOK_OK;
+  if (!g.dX) return has_tail ? launch_column_sums(tail, stream) : MBOK_OK;
   return launch_gemmt(d, packed, with_act ? g.dpre : g.dY, T, with_act ? g.lddpre : g.lddy, g.dX,
-                      g.lddx, ws, passes, stream);
+                      g.lddx, ws, passes, stream, has_tail ? &tail : nullptr);
 }
 
 }  // namespace mbok

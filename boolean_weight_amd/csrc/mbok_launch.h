@@ -59,8 +59,12 @@ int launch_gemm(const mbok_desc* d, const void* packed, const void* X, int64_t T
 
 // passes: 1 = weight levels rounded to bf16; 2 = plus their bf16 residues, here
 // and in the gated block's calls below
+// sums: column sums (mbok_sums.h) that run with the product's last kernel, or null
+struct ColumnSums;
 int launch_gemmt(const mbok_desc* d, const void* packed, const void* dY, int64_t T, int64_t lddy,
-                 void* dX, int64_t lddx, void* ws, int passes, hipStream_t stream);
+                 void* dX, int64_t lddx, void* ws, int passes, hipStream_t stream,
+                 const ColumnSums* sums = nullptr);
+int launch_column_sums(const ColumnSums& sums, hipStream_t stream);
 size_t gemmt_workspace_bytes(const mbok_desc* d, int64_t T);
 int launch_scale_grad(const mbok_desc* d, const void* packed, const void* dY, int64_t T,
                       int64_t lddy, const void* X, int64_t ldx, float* dalpha, bool accumulate,
