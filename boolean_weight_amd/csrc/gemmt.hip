@@ -205,11 +205,11 @@ __global__ void __launch_bounds__(kThreads) gemmt_kernel(
   const int wkey = (lane >> 2) & 3;
 
   // One step's W_hat, from its signs and scales to LDS, in kChunks pieces of a
-  // few vector instructions each (K = 4: in four): levels, selectors, then
+  // few vector instructions each: levels, selectors, then
   // half a quad at a time.
   constexpr int kChunks = 24;
   float af[K];
-  uint32_t pairs[2], V[4], lo = 0, hi = 0, out[4];
+  uint32_t pairs[4], flipped[3], V[4], lo = 0, hi = 0, out[4];
   Levels L;
   auto w_piece = [&](int b, int q) {
     *reinterpret_cast<u32x4*>(wbuf(b) + wput + 8 * (q ^ wkey)) =
@@ -229,25 +229,22 @@ __global__ void __launch_bounds__(kThreads) gemmt_kernel(
       if (c < 2) pairs[c] = lo_levels ? upper_pair<K, true>(af, c) : upper_pair<K>(af, c);
       if (c == 2) L = pack_levels<K>(pairs[0], pairs[1]);
       if (c >= 3 && c < 6) word_selectors_part<K>(R.w, V, c - 3);
-      if (c >= 8) {
-        const int quad = (c - 8) >> 1;  // of the word; piece quad / 2
-        if ((c & 1) == 0) {
-          const uint32_t sel = quad_selector<K>(V, quad >> 2, quad & 3);
-          lo = quad_low(L, sel);
-          hi = quad_high(L, sel);
-        } else {
-          quad_pairs(lo, hi, out + 2 * (quad & 1));
-          if (quad & 1) w_piece(b, quad >> 1);
-        }
+    } else {
+      if (c < 4) pairs[c] = lo_levels ? k4_pair<true>(af, c) : k4_pair(af, c);
+      if (c == 4) L = k4_levels(pairs);
+      if (c == 4) k4_words(R.w, flipped);
+      if (c >= 5 && c < 8) word_selectors_part<3>(flipped, V, c - 5);
+    }
+    if (c >= 8) {
+      const int quad = (c - 8) >> 1;  // of the word; piece quad / 2
+      if ((c & 1) == 0) {
+        const uint32_t sel = quad_selector<K <= 3 ? K : 3>(V, quad >> 2, quad & 3);
+        lo = quad_low(L, sel);
+        hi = K <= 3 ? quad_high(L, sel) : k4_high(L, sel, R.w[K - 1], quad);
+      } else {
+        quad_pairs(lo, hi, out + 2 * (quad & 1));
+        if (quad & 1) w_piece(b, quad >> 1);
       }
-    } else if (c >= 8 && (c & 3) == 0) {
-      uint32_t o32[16];
-      const int q = (c - 8) >> 2;
-      if (lo_levels) unpack_word_k4<true>(R.w, af, o32);
-      else unpack_word_k4<false>(R.w, af, o32);
-#pragma unroll
-      for (int e = 0; e < 4; ++e) out[e] = o32[4 * q + e];
-      w_piece(b, q);
     }
   };
   auto form_all = [&](int b, const StepRegs& R, bool lo_levels) {

@@ -42,7 +42,8 @@ __global__ void __launch_bounds__(kThreads) linear_backward_kernel(
       u32x4 s[U], z[U];
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        const int64_t t = min(r + u * kRowLanes, r1 - 1);
+        const int64_t t = r + u * kRowLanes;
+        if (t >= r1) continue;
         s[u] = load_piece(dY + t * lddy + col, live, m >= 8);
         if (ACT) z[u] = load_piece(pre + t * ldpre + col, live, m >= 8);
       }
@@ -90,17 +91,33 @@ __global__ void __launch_bounds__(kThreads) linear_backward_kernel(
   *out = accumulate ? *out + total : total;
 }
 
-// Slices of the rows: about 1500 workgroups, of at least 64 rows each; more than
-// one slice needs a workspace for its sums.
+// Slices of the rows: enough for about 1500 workgroups, of at least 16 rows, two
+// for each thread (a slope takes some 40 instructions: 109 rows of 94 columns in one
+// slice 19 us).  More than one slice needs a workspace for its sums, and their
+// adding: up to 32 rows stay one.
 struct RowSplit {
   int slices, step;
 };
 RowSplit row_split(int m, int64_t T, bool whole) {
   const int cols = (m + kColumns - 1) / kColumns;
-  const int64_t want = (1500 + cols - 1) / cols, most = T / 64;
-  const int64_t n = whole ? 1 : (most < 1 ? 1 : (want < most ? want : most));
+  const int64_t want = (1500 + cols - 1) / cols, most = T <= 32 ? 1 : T / 16;
+  const int64_t n = whole ? 1 : (want < most ? want : most);
   const int64_t step = (T + n - 1) / n;
   return RowSplit{(int)((T + step - 1) / step), (int)step};
+}
+
+// More than 16 tokens on the few-token kernel, 16 at a time.  A tile of the
+// many-token kernel walks its whole contraction, 0.42 us per 64 columns whatever the
+// token count, and a small layer has few tiles; the few-token kernel spreads the
+// contraction over wavefronts and takes about 7 us and the product's operations at 140
+// TFLOP/s (every 16 rows read the activations again).  Us, few-token kernel / tiles:
+// K = 3: 4096 x 4096 17 tokens 12.6 / 27.5, 64 28.2 / 29.2, 100 34.4 / 29.2; 2540 x 4480
+// 100 26.8 / 31.6, 166 37.1 / 31.7; 64 x 11008 1000 20.2 / 72.3; 11008 x 4096 17 26.6 /
+// 28.5, 33 37.0 / 29.0; 1045 x 384 6 / 6; K = 2: 1000 x 2048 300 13.6 / 15.9, 512 20.7 /
+// 15.2; K = 1: 724 x 1408 300 8.8 / 11.8, 1000 21.1 / 12.8.
+bool in_chunks(const mbok_desc* d, int64_t T, int passes) {
+  const int64_t tokens = (T + 15) / 16 * 16;
+  return tokens * d->m < (int64_t)430000 * passes - 200000000 / d->n;
 }
 
 }  // namespace
@@ -109,7 +126,16 @@ RowSplit row_split(int m, int64_t T, bool whole) {
 // at least 2^26 sign bits 3 to 6, of 2^27 7 and 8 tokens on the fp4 x fp8 forms.
 int launch_linear(const mbok_desc* d, const void* packed, const void* X, int64_t T, int64_t ldx,
                   const LinearOut& out, int passes, hipStream_t stream) {
-  if (T > skinny_max_tokens()) return launch_linear_mfma(d, packed, X, T, ldx, out, passes, stream);
+  if (T > skinny_max_tokens()) {
+    // what both kernels' 32-bit offsets take, alike
+    if ((int64_t)d->K * ((d->m + kRowBlock - 1) / kRowBlock * kRowBlock) * (d->n / 32) >
+        (int64_t)UINT32_MAX)
+      return MBOK_ERR_SHAPE;
+    if (ldx >= (int64_t(1) << 32) / 512) return MBOK_ERR_INVALID_ARG;
+    if (in_chunks(d, T, passes))
+      return launch_linear_chunks(d, packed, X, T, ldx, out, stream);
+    return launch_linear_mfma(d, packed, X, T, ldx, out, passes, stream);
+  }
   if (T == 1) return launch_linear_f4(d, packed, X, T, ldx, out, stream);
   if ((T - 1) * ldx + d->n <= INT32_MAX) {
     const int64_t work = (int64_t)d->K * d->m * d->n;
@@ -138,11 +164,12 @@ int launch_linear_backward(const mbok_desc* d, const void* packed, const LinearG
   // without a sum the rows split freely
   const RowSplit s = row_split(d->m, T, g.dbias && !ws);
   const bool sliced = s.slices > 1;
-  // what is left of dbias after the first kernel: the slices' sums, or the rows of dY
-  // themselves where they are few and need no pass of their own
+  // what is left of dbias after the first kernel: the slices' sums, or, of up to 127
+  // rows without an activation (and without a workspace), the rows of dY themselves
   ColumnSums tail = {g.dY, g.lddy, 1, (int)T, d->m, accumulate, g.dbias};
-  bool has_tail = g.dbias && !with_act && !sliced;
-  if (with_act || (g.dbias && sliced)) {
+  const bool direct = !with_act && (T < 128 || !ws);
+  bool has_tail = g.dbias && direct;
+  if (with_act || (g.dbias && !direct)) {
     float* sums = sliced && g.dbias
                       ? reinterpret_cast<float*>(reinterpret_cast<char*>(ws) + product_bytes(d, T))
                       : g.dbias;

@@ -212,21 +212,49 @@ __device__ __forceinline__ void unpack_word(const uint32_t* w, const Levels& L, 
   for (int q = 0; q < 8; ++q) unpack_quad<K>(V, q >> 2, q & 3, L, out + 2 * q);
 }
 
-// K = 4 (16 levels): direct fp32 sums, then bf16 (LO: their residues).
+// K = 4 (16 levels).  Flipping every sign negates a level, so the 8 levels with the
+// fourth kernel's sign set are kept, as for K = 3; where it is not set the other three
+// signs are flipped (k4_words) and the level's sign too (k4_high).  The same sums, in
+// the kernels' order, as adding them one column at a time.
+// Levels 2 p and 2 p + 1 (bits: signs of kernels 0, 1, 2) as a bf16 pair.
+template <bool LO = false>
+__device__ __forceinline__ uint32_t k4_pair(const float* a, int p) {
+  float l[2];
+#pragma unroll
+  for (int e = 0; e < 2; ++e) {
+    const float s = (e ? a[0] : -a[0]) + ((p & 1) ? a[1] : -a[1]);
+    l[e] = (s + ((p & 2) ? a[2] : -a[2])) + a[3];
+  }
+  return LO ? bf16_pair(bf16_residue(l[0]), bf16_residue(l[1])) : bf16_pair(l[0], l[1]);
+}
+__device__ __forceinline__ Levels k4_levels(const uint32_t* p) {
+  Levels L;
+  L.lo_a = __builtin_amdgcn_perm(p[1], p[0], 0x06040200u);
+  L.hi_a = __builtin_amdgcn_perm(p[1], p[0], 0x07050301u);
+  L.lo_b = __builtin_amdgcn_perm(p[3], p[2], 0x06040200u);
+  L.hi_b = __builtin_amdgcn_perm(p[3], p[2], 0x07050301u);
+  return L;
+}
+__device__ __forceinline__ void k4_words(const uint32_t* w, uint32_t* x) {
+#pragma unroll
+  for (int k = 0; k < 3; ++k) x[k] = ~(w[k] ^ w[3]);
+}
+// High bytes of quad q
+__device__ __forceinline__ uint32_t k4_high(const Levels& L, uint32_t sel, uint32_t w3, int q) {
+  return quad_high(L, sel) ^ ((~w3 << (7 - q)) & 0x80808080u);
+}
 template <bool LO = false>
 __device__ __forceinline__ void unpack_word_k4(const uint32_t* w, const float* a, uint32_t* out) {
+  uint32_t p[4], x[3], V[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) p[i] = k4_pair<LO>(a, i);
+  const Levels L = k4_levels(p);
+  k4_words(w, x);
+  word_selectors<3>(x, V);
 #pragma unroll
   for (int q = 0; q < 8; ++q) {
-    float v[4];
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      float s = 0.f;
-#pragma unroll
-      for (int k = 0; k < 4; ++k) s += ((w[k] >> (8 * e + q)) & 1u) ? a[k] : -a[k];
-      v[e] = LO ? bf16_residue(s) : s;
-    }
-    out[2 * q] = bf16_pair(v[0], v[1]);
-    out[2 * q + 1] = bf16_pair(v[2], v[3]);
+    const uint32_t sel = quad_selector<3>(V, q >> 2, q & 3);
+    quad_pairs(quad_low(L, sel), k4_high(L, sel, w[3], q), out + 2 * q);
   }
 }
 

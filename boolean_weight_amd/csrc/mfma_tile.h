@@ -126,7 +126,7 @@ __device__ __forceinline__ void product_tile(const uint32_t* __restrict__ bits,
   // a scale group serve its two steps (TWO: are formed for each of the four)
   constexpr int kChunks = 24;
   float af[K];
-  uint32_t pairs[2], V[4], lo = 0, hi = 0, o4[4];
+  uint32_t pairs[4], flipped[3], V[4], lo = 0, hi = 0, o4[4];
   Levels L;
   auto put = [&](int b, int p) {
     *reinterpret_cast<u32x4*>(wbuf(b) + wput + 8 * ((4 * word + p) ^ wkey)) =
@@ -142,25 +142,22 @@ __device__ __forceinline__ void product_tile(const uint32_t* __restrict__ bits,
         pairs[c] = lo_levels ? upper_pair<K, true>(af, c) : upper_pair<K>(af, c);
       if (levels && c == 2) L = pack_levels<K>(pairs[0], pairs[1]);
       if (c >= 3 && c < 6) word_selectors_part<K>(R.w, V, c - 3);
+    } else {
+      if (levels && c < 4) pairs[c] = lo_levels ? k4_pair<true>(af, c) : k4_pair(af, c);
+      if (levels && c == 4) L = k4_levels(pairs);
+      if (c == 4) k4_words(R.w, flipped);
+      if (c >= 5 && c < 8) word_selectors_part<3>(flipped, V, c - 5);
+    }
+    if (c >= 8) {
       const int h = (c - 8) >> 1;  // quad of the word
-      if (c >= 8) {
-        if ((c & 1) == 0) {
-          const uint32_t sel = quad_selector<K>(V, h >> 2, h & 3);
-          lo = quad_low(L, sel);
-          hi = quad_high(L, sel);
-        } else {
-          quad_pairs(lo, hi, o4 + 2 * (h & 1));
-          if (h & 1) put(b, h >> 1);
-        }
+      if ((c & 1) == 0) {
+        const uint32_t sel = quad_selector<K <= 3 ? K : 3>(V, h >> 2, h & 3);
+        lo = quad_low(L, sel);
+        hi = K <= 3 ? quad_high(L, sel) : k4_high(L, sel, R.w[K - 1], h);
+      } else {
+        quad_pairs(lo, hi, o4 + 2 * (h & 1));
+        if (h & 1) put(b, h >> 1);
       }
-    } else if (c >= 8 && (c & 3) == 0) {
-      const int p = (c - 8) >> 2;
-      uint32_t o32[16];
-      if (lo_levels) unpack_word_k4<true>(R.w, af, o32);
-      else unpack_word_k4<false>(R.w, af, o32);
-#pragma unroll
-      for (int e = 0; e < 4; ++e) o4[e] = o32[4 * p + e];
-      put(b, p);
     }
   };
 

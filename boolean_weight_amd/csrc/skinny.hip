@@ -194,6 +194,17 @@ __global__ void __launch_bounds__(1024) out_skinny_kernel(
   skinny_body<AT, K>(bits, scales, X, ldx, out, T, G);
 }
 
+// the layer with its epilogue for more tokens than one product holds: 16 per
+// workgroup row of the grid
+template <typename AT, int K>
+__global__ void __launch_bounds__(1024) linear_chunks_kernel(
+    const u32x4* __restrict__ bits, const AT* __restrict__ scales,
+    const uint16_t* __restrict__ X, int64_t ldx, int T, int G, LinearOut out) {
+  const int t0 = (int)blockIdx.y * kMaxSkinnyTokens;
+  skinny_body<AT, K>(bits, scales, X + t0 * ldx, ldx, out.from(t0),
+                     min(T - t0, kMaxSkinnyTokens), G);
+}
+
 // Streaming form (the default): one persistent workgroup per compute unit.
 // Wavefront w owns group block w of the slab (groups 4w .. 4w+3, at most 8
 // blocks: slabs of up to 32 groups), loads the activation fragments of its
@@ -588,6 +599,40 @@ int launch_gated_skinny(const mbok_desc* d, const void* packed, const void* X, i
 int launch_linear_skinny(const mbok_desc* d, const void* packed, const void* X, int64_t T,
                          int64_t ldx, const LinearOut& out, hipStream_t stream) {
   return launch_out_skinny(d, packed, X, T, ldx, out, stream);
+}
+
+template <typename AT>
+static void launch_chunks(const Geom& geo, const void* packed, const void* X, int64_t T,
+                          int64_t ldx, const LinearOut& out, hipStream_t stream) {
+  const u32x4* bits = reinterpret_cast<const u32x4*>(packed);
+  const AT* scales = reinterpret_cast<const AT*>(reinterpret_cast<const char*>(packed) +
+                                                 geo.bits_bytes);
+  const int64_t chunks = (T + kMaxSkinnyTokens - 1) / kMaxSkinnyTokens;
+  // as launch_at: about 4800 wavefronts
+  const int64_t blocks = geo.RB * 4 * chunks;
+  const int64_t want = (4800 + blocks / 2) / blocks;
+  const int NW = (int)(want < 1 ? 1 : want > 16 ? (geo.G < 16 ? geo.G : 16)
+                                                : (want > geo.G ? geo.G : want));
+  auto go = [&](auto k) {
+    hipLaunchKernelGGL((linear_chunks_kernel<AT, decltype(k)::value>),
+                       dim3(geo.RB * 4, (unsigned)chunks), dim3(64 * NW),
+                       (size_t)NW * 256 * sizeof(float), stream, bits, scales,
+                       reinterpret_cast<const uint16_t*>(X), ldx, (int)T, geo.G, out);
+  };
+  switch (geo.K) {
+    case 1: go(std::integral_constant<int, 1>{}); break;
+    case 2: go(std::integral_constant<int, 2>{}); break;
+    case 3: go(std::integral_constant<int, 3>{}); break;
+    default: go(std::integral_constant<int, 4>{}); break;
+  }
+}
+
+int launch_linear_chunks(const mbok_desc* d, const void* packed, const void* X, int64_t T,
+                         int64_t ldx, const LinearOut& out, hipStream_t stream) {
+  const Geom geo = make_geom(d);
+  if (d->alpha_dtype == MBOK_F16) launch_chunks<uint16_t>(geo, packed, X, T, ldx, out, stream);
+  else launch_chunks<float>(geo, packed, X, T, ldx, out, stream);
+  return hipGetLastError() == hipSuccess ? MBOK_OK : MBOK_ERR_HIP;
 }
 
 }  // namespace mbok

@@ -688,8 +688,8 @@ int mbok_gated_backward_precise(const mbok_desc* d, const void* packed, const vo
  *     z[t, i] = sum_j W_hat[i, j] X[t, j] + bias[i]
  *     Y[t, i] = residual[t, i] + act(z[t, i])
  * The product as mbok_gated computes its own for T rows (exact per scale for T
- * <= 16, levels rounded to bf16 for larger T), then bias, activation and
- * residual in fp32 and one rounding to Y's type.
+ * <= 16 and, on small layers, for more; levels rounded to bf16 otherwise), then
+ * bias, activation and residual in fp32 and one rounding to Y's type.
  *  packed    device, MBOK_LAYOUT_L64 buffer of this descriptor.
  *  X         device bf16 [T, ldx], ldx >= n, ldx % 8 == 0, 16-byte aligned.
  *  T         1 .. MBOK_MAX_T.
@@ -705,8 +705,8 @@ int mbok_gated_backward_precise(const mbok_desc* d, const void* packed, const vo
  * faster).  Y and pre must not overlap X or each other.  Non-finite activations
  * as for mbok_gated.
  * Errors: INVALID_ARG (NULL, act, leading dimensions, residual = Y with another
- * one; ldx >= 2^23 for T > 16), SHAPE (T; a layer of 2^32 or more sign words, or
- * an output of 2^32 or more tiles' threads, for T > 16), DTYPE (x_dtype other
+ * one; ldx >= 2^23 for T > 16), SHAPE (T; a layer of 2^32 or more sign words for
+ * T > 16), DTYPE (x_dtype other
  * than MBOK_BF16, y_dtype, bias_dtype), ALIGN (packed and X 16 bytes, ldx % 8,
  * the others to their element), HIP, and the descriptor's.
  */

@@ -190,10 +190,14 @@ def test_linear_backward_workspace(lib):
     fn = lib.mbok_linear_backward_workspace_bytes
     assert fn(None, 4) == 0 and fn(ctypes.byref(BAD_DESC), 4) == 0
     assert fn(ctypes.byref(d), 0) == 0 and fn(ctypes.byref(d), bw.MBOK_MAX_T + 1) == 0
-    # whole rounds of the product: the slices' sums of dbias alone, 64 rows or more each
-    assert bw.mbok_linear_backward_workspace_bytes(d, 4096) == 64 * 4096 * 4
-    # fewer than 128 rows are one slice: the product's workspace
-    assert bw.mbok_linear_backward_workspace_bytes(d, 127) == bw.mbok_gemmt_workspace_bytes(d, 127)
+    # whole rounds of the product: the sums of 94 slices of 44 rows for dbias alone
+    assert bw.mbok_linear_backward_workspace_bytes(d, 4096) == 94 * 4096 * 4
+    # beside the product's own: slices of 16 rows at least
+    own = bw.mbok_gemmt_workspace_bytes(d, 64)
+    assert own % 256 == 0
+    assert bw.mbok_linear_backward_workspace_bytes(d, 64) == own + 4 * 4096 * 4
+    # up to 32 rows are one slice: the product's workspace
+    assert bw.mbok_linear_backward_workspace_bytes(d, 32) == bw.mbok_gemmt_workspace_bytes(d, 32)
 
 
 def logp_args(backward):
