@@ -106,18 +106,17 @@ RowSplit row_split(int m, int64_t T, bool whole) {
   return RowSplit{(int)((T + step - 1) / step), (int)step};
 }
 
-// More than 16 tokens on the few-token kernel, 16 at a time.  A tile of the
-// many-token kernel walks its whole contraction, 0.42 us per 64 columns whatever the
-// token count, and a small layer has few tiles; the few-token kernel spreads the
-// contraction over wavefronts and takes about 7 us and the product's operations at 140
-// TFLOP/s (every 16 rows read the activations again).  Us, few-token kernel / tiles:
-// K = 3: 4096 x 4096 17 tokens 12.6 / 27.5, 64 28.2 / 29.2, 100 34.4 / 29.2; 2540 x 4480
-// 100 26.8 / 31.6, 166 37.1 / 31.7; 64 x 11008 1000 20.2 / 72.3; 11008 x 4096 17 26.6 /
-// 28.5, 33 37.0 / 29.0; 1045 x 384 6 / 6; K = 2: 1000 x 2048 300 13.6 / 15.9, 512 20.7 /
-// 15.2; K = 1: 724 x 1408 300 8.8 / 11.8, 1000 21.1 / 12.8.
+// More than 16 tokens on the few-token products.  A tile of the many-token kernel
+// walks its whole contraction, 0.42 us per 64 columns whatever the token count, and a
+// small layer has few tiles; the few-token kernel spreads the contraction over
+// wavefronts.  560: what the tiles take at least, 656e-5 us per column, less what the
+// estimate is off by; 300000 / n: 3 us a call more.  (us, few-token products / tiles,
+// K = 3: 2540 x 4480 33 tokens 9.9 / 29.3, 166 20.9 / 31.6, 300 37.0 / 32.3; 4096 x 11008
+// 64 27.7 / 72.0, 166 74.9 / 75.2; 11008 x 4096 33 32.4 / 29.1; 64 x 11008 300 14.8 /
+// 71.5; K = 2: 4096 x 4096 64 11.2 / 27.9, 166 25.3 / 28.4, 300 39.2 / 36.0; 1000 x 2048
+// 300 9.6 / 16.0.)
 bool in_chunks(const mbok_desc* d, int64_t T, int passes) {
-  const int64_t tokens = (T + 15) / 16 * 16;
-  return tokens * d->m < (int64_t)430000 * passes - 200000000 / d->n;
+  return linear_chunks_cost(d, T) < 560 * passes - 300000 / d->n;
 }
 
 }  // namespace

@@ -32,16 +32,6 @@ struct LinearOut {
   int m, act;
   int y_f32, bias_dtype;
 
-  // the same for tokens from t0 on
-  __device__ __forceinline__ LinearOut from(int64_t t0) const {
-    LinearOut o = *this;
-    const int64_t size = y_f32 ? 4 : 2;
-    o.Y = reinterpret_cast<char*>(Y) + t0 * ldy * size;
-    if (R) o.R = reinterpret_cast<const char*>(R) + t0 * ldr * size;
-    if (pre) o.pre = pre + t0 * ldpre;
-    return o;
-  }
-
   __device__ __forceinline__ float bias_at(int row) const {
     if (!bias) return 0.f;
     if (bias_dtype == MBOK_F32) return reinterpret_cast<const float*>(bias)[row];

@@ -194,15 +194,134 @@ __global__ void __launch_bounds__(1024) out_skinny_kernel(
   skinny_body<AT, K>(bits, scales, X, ldx, out, T, G);
 }
 
-// the layer with its epilogue for more tokens than one product holds: 16 per
-// workgroup row of the grid
-template <typename AT, int K>
-__global__ void __launch_bounds__(1024) linear_chunks_kernel(
+// The layer with its epilogue for more tokens: a workgroup takes 16 C of them and R
+// tiles of one row block, its wavefronts share the contraction.  A group's
+// activations serve R tiles and an expanded sign word serves C products, so the
+// activations' reads from L2 and the expansion, what bounds one tile and 16 tokens at a
+// time, fall to 1 / R and 1 / C.
+constexpr int chunk_waves(int R, int C) { return R * C <= 2 ? 16 : 8; }  // registers
+template <typename AT, int K, int R, int C>
+__global__ void __launch_bounds__(64 * chunk_waves(R, C)) linear_chunks_kernel(
     const u32x4* __restrict__ bits, const AT* __restrict__ scales,
     const uint16_t* __restrict__ X, int64_t ldx, int T, int G, LinearOut out) {
-  const int t0 = (int)blockIdx.y * kMaxSkinnyTokens;
-  skinny_body<AT, K>(bits, scales, X + t0 * ldx, ldx, out.from(t0),
-                     min(T - t0, kMaxSkinnyTokens), G);
+  extern __shared__ float red[];  // [NW][R][C][4][64] partial sums
+  const int lane = threadIdx.x & 63;
+  const int wave = threadIdx.x >> 6;
+  const int NW = blockDim.x >> 6;
+  const int i = lane & 15, q = lane >> 4;
+  const int tile0 = (int)blockIdx.x * R, t0 = (int)blockIdx.y * 16 * C;
+  const int rb = tile0 >> 2;
+  const int rin = ((tile0 & 3) << 4) + i;
+  const int g0 = (int)((int64_t)wave * G / NW);
+  const int g1 = (int)((int64_t)(wave + 1) * G / NW);
+  const uint16_t* xrow[C];
+#pragma unroll
+  for (int c = 0; c < C; ++c)  // tokens past T read the last one (never stored)
+    xrow[c] = X + (int64_t)min(t0 + 16 * c + i, T - 1) * ldx + 32 * q;
+
+  const uint32_t mask = __builtin_amdgcn_readfirstlane(0x80008000u);
+  uint32_t ones;
+  asm("v_mov_b32 %0, 0x3f803f80" : "=v"(ones));
+
+  f32x4 yacc[R][C];
+#pragma unroll
+  for (int r = 0; r < R; ++r)
+#pragma unroll
+    for (int c = 0; c < C; ++c) yacc[r][c] = f32x4{0.f, 0.f, 0.f, 0.f};
+
+  struct Acts {
+    u32x4 v[C][4];
+  };
+  auto load_x = [&](int g) {
+    Acts x;
+#pragma unroll
+    for (int c = 0; c < C; ++c)
+#pragma unroll
+      for (int s = 0; s < 4; ++s)
+        x.v[c][s] = *reinterpret_cast<const u32x4*>(xrow[c] + (int64_t)kGroup * g + 8 * s);
+    return x;
+  };
+  for (int gb = g0; gb < g1; gb += 4) {
+    const int nj = min(4, g1 - gb);             // groups in this block
+    const int gq = gb + (q < nj ? q : nj - 1);  // group loaded by block q
+    const int64_t at = (int64_t)(rb * G + gq) * K * 64 + rin;
+    uint32_t w[R][K][4], a[R][K][4];
+    u32x4 wv[R][K];
+    AT av[R][K];
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+#pragma unroll
+      for (int k = 0; k < K; ++k) {
+        wv[r][k] = bits[at + 16 * r + k * 64];
+        av[r][k] = scales[at + 16 * r + k * 64];
+      }
+    Acts x = load_x(gb);
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+#pragma unroll
+      for (int k = 0; k < K; ++k) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) w[r][k][e] = wv[r][k][e];
+        transpose4(w[r][k]);                          // word q of row i, group gb + j
+        spread4(scale_bits<AT>(av[r][k]), a[r][k]);   // scale of row i, group gb + j
+      }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      if (j >= nj) break;
+      const Acts cur = x;
+      if (j + 1 < nj) x = load_x(gb + j + 1);
+#pragma unroll
+      for (int r = 0; r < R; ++r)
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+          const uint32_t p01 = __builtin_amdgcn_perm(w[r][k][j], w[r][k][j], 0x01010000u);
+          const uint32_t p23 = __builtin_amdgcn_perm(w[r][k][j], w[r][k][j], 0x03030202u);
+          f32x4 S[C];
+#pragma unroll
+          for (int c = 0; c < C; ++c) S[c] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int s = 0; s < 4; ++s) {
+            const int se = 7 - 2 * s, so = 6 - 2 * s;  // columns 8s + 0..3, 8s + 4..7
+            const u32x4 b = u32x4{signed_ones(p01 << se, mask, ones),
+                                  signed_ones(p23 << se, mask, ones),
+                                  signed_ones(p01 << so, mask, ones),
+                                  signed_ones(p23 << so, mask, ones)};
+#pragma unroll
+            for (int c = 0; c < C; ++c)
+              S[c] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                  __builtin_bit_cast(bf16x8, cur.v[c][s]), __builtin_bit_cast(bf16x8, b), S[c], 0,
+                  0, 0);
+          }
+          const float sc = scale_value<AT>(a[r][k][j]);
+#pragma unroll
+          for (int c = 0; c < C; ++c)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              yacc[r][c][e] = __builtin_fmaf(-sc, S[c][e], yacc[r][c][e]);
+        }
+    }
+  }
+
+#pragma unroll
+  for (int r = 0; r < R; ++r)
+#pragma unroll
+    for (int c = 0; c < C; ++c)
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        red[(((wave * R + r) * C + c) * 4 + e) * 64 + lane] = yacc[r][c][e];
+  __syncthreads();
+  for (int idx = threadIdx.x; idx < R * C * 256; idx += blockDim.x) {
+    const int part = idx >> 8, c = part % C, r = part / C;
+    const int p = (idx & 255) >> 4;  // as skinny_item
+    const int tok = 4 * (p & 3) + (p >> 2), t = t0 + 16 * c + tok;
+    if (t < T)
+      out.item(t, tile0 + r, idx & 15, [&](int row) {
+        float sum = 0.f;
+        for (int v = 0; v < NW; ++v)
+          sum += red[((v * R + r) * C + c) * 256 + skinny_part(tok, row)];
+        return sum;
+      });
+  }
 }
 
 // Streaming form (the default): one persistent workgroup per compute unit.
@@ -601,29 +720,57 @@ int launch_linear_skinny(const mbok_desc* d, const void* packed, const void* X, 
   return launch_out_skinny(d, packed, X, T, ldx, out, stream);
 }
 
+// Tiles and 16-token chunks of a workgroup, one to a compute unit, and the time of the
+// call's rounds of them per column and kernel, in 1e-5 us (measured, 1408 to 11008
+// columns: a round takes that and about 5 us): the shape that takes least.
+struct ChunkShape {
+  int R, C;
+  int64_t cost;
+};
+static ChunkShape chunk_shape(const Geom& geo, int64_t T) {
+  const ChunkShape shapes[] = {{1, 1, 28}, {2, 1, 42}, {2, 2, 67}, {4, 2, 97}};
+  ChunkShape best = {0, 0, INT64_MAX};
+  for (ChunkShape s : shapes) {
+    const int64_t blocks = geo.RB * 4 / s.R * ((T + 16 * s.C - 1) / (16 * s.C));
+    s.cost *= (blocks + 255) / 256;
+    if (s.cost < best.cost) best = s;
+  }
+  return best;
+}
+
+int64_t linear_chunks_cost(const mbok_desc* d, int64_t T) {
+  return chunk_shape(make_geom(d), T).cost * d->K;
+}
+
 template <typename AT>
 static void launch_chunks(const Geom& geo, const void* packed, const void* X, int64_t T,
                           int64_t ldx, const LinearOut& out, hipStream_t stream) {
   const u32x4* bits = reinterpret_cast<const u32x4*>(packed);
   const AT* scales = reinterpret_cast<const AT*>(reinterpret_cast<const char*>(packed) +
                                                  geo.bits_bytes);
-  const int64_t chunks = (T + kMaxSkinnyTokens - 1) / kMaxSkinnyTokens;
-  // as launch_at: about 4800 wavefronts
-  const int64_t blocks = geo.RB * 4 * chunks;
-  const int64_t want = (4800 + blocks / 2) / blocks;
-  const int NW = (int)(want < 1 ? 1 : want > 16 ? (geo.G < 16 ? geo.G : 16)
-                                                : (want > geo.G ? geo.G : want));
-  auto go = [&](auto k) {
-    hipLaunchKernelGGL((linear_chunks_kernel<AT, decltype(k)::value>),
-                       dim3(geo.RB * 4, (unsigned)chunks), dim3(64 * NW),
-                       (size_t)NW * 256 * sizeof(float), stream, bits, scales,
-                       reinterpret_cast<const uint16_t*>(X), ldx, (int)T, geo.G, out);
+  const ChunkShape s = chunk_shape(geo, T);
+  auto go = [&](auto k, auto rows, auto chunks) {
+    constexpr int R = decltype(rows)::value, C = decltype(chunks)::value;
+    const int NW = geo.G < chunk_waves(R, C) ? geo.G : chunk_waves(R, C);
+    hipLaunchKernelGGL((linear_chunks_kernel<AT, decltype(k)::value, R, C>),
+                       dim3(geo.RB * 4 / R, (unsigned)((T + 16 * C - 1) / (16 * C))),
+                       dim3(64 * NW), (size_t)NW * R * C * 256 * sizeof(float), stream, bits,
+                       scales, reinterpret_cast<const uint16_t*>(X), ldx, (int)T, geo.G, out);
+  };
+  auto by_shape = [&](auto k) {
+    const std::integral_constant<int, 1> one;
+    const std::integral_constant<int, 2> two;
+    const std::integral_constant<int, 4> four;
+    if (s.R == 1) go(k, one, one);
+    else if (s.C == 1) go(k, two, one);
+    else if (s.R == 2) go(k, two, two);
+    else go(k, four, two);
   };
   switch (geo.K) {
-    case 1: go(std::integral_constant<int, 1>{}); break;
-    case 2: go(std::integral_constant<int, 2>{}); break;
-    case 3: go(std::integral_constant<int, 3>{}); break;
-    default: go(std::integral_constant<int, 4>{}); break;
+    case 1: by_shape(std::integral_constant<int, 1>{}); break;
+    case 2: by_shape(std::integral_constant<int, 2>{}); break;
+    case 3: by_shape(std::integral_constant<int, 3>{}); break;
+    default: by_shape(std::integral_constant<int, 4>{}); break;
   }
 }
 
