@@ -54,13 +54,25 @@ typedef __attribute__((ext_vector_type(4))) uint32_t u32x4;
 
 constexpr int kMaxSkinnyTokens = 16;
 
-// Two bf16 values of magnitude 1 whose sign bits are bits 15 and 31 of src:
-// (src & mask) | ones in one v_and_or_b32, mask = 0x80008000 in an SGPR and
-// ones = 0x3F803F80 in a VGPR (a VOP3 encoding takes no literal constants).
+// Two bf16 values of magnitude 1 whose sign bits are bits 15 and 31 of src: one
+// v_and_or_b32 with mask = 0x80008000 in an SGPR and ones = 0x3F803F80 in a VGPR (a
+// VOP3 encoding takes no literal constants).  The compiler's own instruction, not
+// assembly: it knows which registers matrix instructions in flight still read or write
+// and waits for them before it uses one again (as assembly, a result was overwritten by
+// a product that had not ended).
 __device__ __forceinline__ uint32_t signed_ones(uint32_t src, uint32_t mask, uint32_t ones) {
-  uint32_t d;
-  asm("v_and_or_b32 %0, %1, %2, %3" : "=v"(d) : "v"(src), "s"(mask), "v"(ones));
-  return d;
+  return (src & mask) | ones;
+}
+// the constants, unknown to the compiler
+__device__ __forceinline__ uint32_t sign_mask() {
+  uint32_t m;
+  asm("s_mov_b32 %0, 0x80008000" : "=s"(m));
+  return m;
+}
+__device__ __forceinline__ uint32_t bf16_ones() {
+  uint32_t m;
+  asm("v_mov_b32 %0, 0x3f803f80" : "=v"(m));
+  return m;
 }
 
 template <typename AT>
@@ -113,9 +125,7 @@ __device__ __forceinline__ void skinny_body(const u32x4* __restrict__ bits,
   const bool tok_ok = i < T;
   const uint16_t* xrow = X + (int64_t)(tok_ok ? i : 0) * ldx + 32 * q;
 
-  const uint32_t mask = __builtin_amdgcn_readfirstlane(0x80008000u);
-  uint32_t ones;
-  asm("v_mov_b32 %0, 0x3f803f80" : "=v"(ones));
+  const uint32_t mask = sign_mask(), ones = bf16_ones();
 
   f32x4 yacc = f32x4{0.f, 0.f, 0.f, 0.f};
   for (int gb = g0; gb < g1; gb += 4) {
@@ -219,9 +229,7 @@ __global__ void __launch_bounds__(64 * chunk_waves(R, C)) linear_chunks_kernel(
   for (int c = 0; c < C; ++c)  // tokens past T read the last one (never stored)
     xrow[c] = X + (int64_t)min(t0 + 16 * c + i, T - 1) * ldx + 32 * q;
 
-  const uint32_t mask = __builtin_amdgcn_readfirstlane(0x80008000u);
-  uint32_t ones;
-  asm("v_mov_b32 %0, 0x3f803f80" : "=v"(ones));
+  const uint32_t mask = sign_mask(), ones = bf16_ones();
 
   f32x4 yacc[R][C];
 #pragma unroll
@@ -407,9 +415,7 @@ __device__ __forceinline__ void skinny_stream_body(
   uint16_t* frag = SV ? reinterpret_cast<uint16_t*>(red + JMAX * NW * 256) +
                             wave * (4 * K * 2 * kGroup)
                       : nullptr;
-  const uint32_t mask = __builtin_amdgcn_readfirstlane(0x80008000u);
-  uint32_t ones;
-  asm("v_mov_b32 %0, 0x3f803f80" : "=v"(ones));
+  const uint32_t mask = sign_mask(), ones = bf16_ones();
 
   f32x4 yacc[JMAX];
 #pragma unroll

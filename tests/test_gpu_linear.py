@@ -81,6 +81,32 @@ def test_linear_exact(T, m, n):
         assert torch.equal(r.cpu().to(F64), want if yt == torch.float32 else bf16_of(want))
 
 
+# each shape of the few-token products for more than 16 tokens (tiles and chunks of a
+# workgroup: 1 x 1, 2 x 1, 2 x 2, 4 x 2), ragged tokens and rows, tall contractions
+@pytest.mark.parametrize("T,m,n", [(17, 30, 2048), (100, 9, 5120), (33, 2500, 2048),
+                                   (64, 2490, 2048), (100, 2497, 2048), (33, 4096, 2176),
+                                   (250, 1000, 2048)])
+@pytest.mark.parametrize("K", [1, 2, 3, 4])
+def test_linear_small_layers_exact(T, m, n, K):
+    say(f"linear small layer T={T} m={m} n={n} K={K}")
+    dt = "f16" if K % 2 else "f32"
+    S, A = exact_layer(m, n, K, dt, m + n + K)
+    d, packed = pack_on_gpu(S, A, dt)
+    X, R = ints(T, n, T + n), ints(T, m, T + m)
+    buf = torch.full((T, m + 9), -5.0, device=DEV)
+    pbuf = torch.full((T, m + 7), -5.0, dtype=BF, device=DEV)
+    y, pre = buf[:, 4:4 + m], pbuf[:, 3:3 + m]
+    x = wide(X, n + 8, off=0)
+    bw.mbok_linear(d, packed, x, y, residual=R.to(DEV), pre=pre)
+    want, z = ref.linear(finetune_ref.dense(S, A), X, None, "none", R)
+    assert torch.equal(y.cpu().to(F64), want)
+    assert torch.equal(pre.cpu().to(F64), bf16_of(z))
+    assert guards_hold(buf, 4, m) and guards_hold(pbuf, 3, m)
+    again = torch.empty(T, m, device=DEV)
+    bw.mbok_linear_precise(d, packed, x, again, residual=R.to(DEV))
+    assert torch.equal(again, y)
+
+
 def bound_of(T, W, X, z):
     few = T <= 16
     # T <= 16: every scale exact in fp32, activations to 2^-16 at worst (f4 forms)
