@@ -1303,7 +1303,8 @@ def mbok_adamw_plan_init(tensors) -> mbok_adamw_plan:
     8-bit v holds the second moment's root), optionally out (a copy in fp32, fp16 or
     bf16; with layer, a mbok_desc, the layer's packed buffer, whose scales the step
     writes from param [K, m, n/128]) and weight_decay.  The plan holds their
-    addresses: gradients are expected in the same tensors at every step."""
+    addresses: gradients are expected in the same tensors at every step, and a graph
+    that captured a step needs the plan as long as it is replayed."""
     tensors = [dict(t) for t in tensors]
     if not tensors:
         raise ValueError("a plan needs at least one tensor")

@@ -511,11 +511,15 @@ int launch_k(const Geom& geo, const void* packed, const uint16_t* dY, int64_t T,
   }
   if (s.slices > 1) {
     const int rows = T < s.bt ? (int)T : s.bt;
-    const int per = (rows + 3) / 4, more = sums ? (sum_blocks(*sums) + per - 1) / per : 0;
+    const int per = (rows + 3) / 4;
+    int more = sums ? (sum_blocks(*sums) + per - 1) / per : 0;
+    if (s.rest + more > 65535) more = 0;  // a grid has that many rows: a launch of their own
     hipLaunchKernelGGL(gemmt_reduce_kernel, dim3(per, s.rest + more), dim3(256), 0, stream, part,
                        dX, lddx, (int)T, geo.n, s.bt, s.full, s.rest, s.slices,
                        sums ? *sums : ColumnSums{});
-  } else if (sums) {
+    if (more) sums = nullptr;
+  }
+  if (sums) {
     return launch_column_sums(*sums, stream);
   }
   return hipGetLastError() == hipSuccess ? MBOK_OK : MBOK_ERR_HIP;

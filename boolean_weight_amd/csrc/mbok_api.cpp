@@ -8,6 +8,7 @@
 
 #include <algorithm>
 #include <cmath>
+#include <new>
 #include <vector>
 
 #include "../../include/mbok.h"
@@ -747,7 +748,8 @@ int check_adamw_tensor(const mbok_adamw_tensor& t, std::vector<Range>& written,
 
 // Checks the tensors; the values a workgroup takes, the number of workgroups and
 // their LDS.
-int plan_adamw(const mbok_adamw_tensor* tensors, int32_t n, mbok_adamw_plan* plan, int* part) {
+int plan_adamw(const mbok_adamw_tensor* tensors, int32_t n, mbok_adamw_plan* plan,
+               int* part) try {
   if (!tensors) return MBOK_ERR_INVALID_ARG;
   if (n < 1 || n > MBOK_MAX_ADAMW_TENSORS) return MBOK_ERR_SHAPE;
   std::vector<Range> written, read;
@@ -773,6 +775,8 @@ int plan_adamw(const mbok_adamw_tensor* tensors, int32_t n, mbok_adamw_plan* pla
   plan->table_bytes =
       (int64_t)n * sizeof(mbok::AdamTensor) + parts * (int64_t)sizeof(mbok::AdamPart);
   return MBOK_OK;
+} catch (const std::bad_alloc&) {  // the lists of ranges
+  return MBOK_ERR_SCRATCH;
 }
 
 }  // namespace

@@ -702,7 +702,8 @@ int mbok_gated_backward_precise(const mbok_desc* d, const void* packed, const vo
  *  pre       device bf16 [T, ldpre], ldpre >= m, or NULL: z rounded once, for
  *            mbok_linear_backward.
  * residual, Y and pre rows start at any element (16-byte aligned rows run
- * faster).  Y and pre must not overlap X or each other.  Non-finite activations
+ * faster).  Y and pre must not overlap X or each other, and the residual no other
+ * way than by being Y.  Non-finite activations
  * as for mbok_gated.
  * Errors: INVALID_ARG (NULL, act, leading dimensions, residual = Y with another
  * one; ldx >= 2^23 for T > 16), SHAPE (T; a layer of 2^32 or more sign words for
@@ -1042,7 +1043,7 @@ size_t mbok_adamw_table_bytes(const mbok_adamw_tensor* tensors, int32_t n);
  * ranges, of one tensor or of two, that overlap, or one written that is another's
  * gradient), SHAPE (n; more than MBOK_MAX_ADAMW_VALUES values; count is not the
  * layer's), DTYPE, ALIGN (each pointer to its element, out of a layer 16 bytes),
- * and the layer descriptor's.
+ * SCRATCH (no host memory for the check), and the layer descriptor's.
  */
 int mbok_adamw_plan_init(mbok_adamw_plan* plan, const mbok_adamw_tensor* tensors, int32_t n,
                          void* table);
@@ -1065,7 +1066,8 @@ typedef struct mbok_adamw_step {
  * tensor's place in the plan and the value's.  A value that is not finite makes
  * its block's scale NaN.  A root of the second moment that is not 0 never becomes
  * 0.  Scales are at least 2^-87.
- *  table  device, the plan's table, 16-byte aligned.
+ *  table  device, the plan's table, 16-byte aligned; it and the tensors are read when
+ *         the step runs, so a captured step needs them as long as its graph lives.
  *  live   device fp32 [4] or NULL: lr, grad_scale, t (a whole number below 2^24)
  *         and a flag, read when the step runs (so that a captured step follows
  *         them) instead of the constants of `step`; a flag other than 0 (an

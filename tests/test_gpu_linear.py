@@ -211,6 +211,22 @@ def test_backward_without_activation_exact(T, m, n, ws):
         assert torch.equal(only, out[:, 8:8 + n])
 
 
+def test_backward_bias_of_more_columns_than_a_grid_has_rows():
+    """One token, 2.2 million outputs: the bias sums do not fit beside the product's
+    joining kernel."""
+    say("linear backward, many columns")
+    m, n = 2200000, 128
+    S, A = exact_layer(m, n, 1, "f16", 3)
+    d, packed = pack_on_gpu(S, A, "f16")
+    dY = ints(1, m, 4)
+    db, dX = torch.empty(m, device=DEV), torch.empty(1, n, dtype=BF, device=DEV)
+    bw.mbok_linear_backward(d, packed, wide(dY, m), dbias=db, dX=dX)
+    assert torch.equal(db.cpu().to(F64), dY[0].to(F64))
+    want = torch.empty(1, n, dtype=BF, device=DEV)
+    bw.mbok_gemmt(d, packed, wide(dY, m), want)
+    assert torch.equal(dX, want)
+
+
 @pytest.mark.parametrize("T,m,n,K", [(1, 300, 128, 2), (5, 9, 128, 1), (37, 1001, 640, 2),
                                      (200, 4096, 256, 3), (2048, 1000, 384, 3), (129, 7, 256, 4)])
 @pytest.mark.parametrize("kind", ["silu", "gelu"])
