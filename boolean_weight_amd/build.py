@@ -22,7 +22,8 @@ CEILINGS_SOURCES = ["ceilings.hip"]
 
 SOURCES = ["mbok_api.cpp", "allocate.cpp", "quantize.hip", "refit.hip", "svid.hip", "pack.hip", "gemv.hip", "gemv_f4.hip", "gemvt.hip", "gemm.hip", "skinny.hip", "gated.hip",
            "gated_f4.hip", "gated_mfma.hip", "gemmt.hip", "scale_grad.hip", "distill.hip",
-           "linear.hip", "linear_f4.hip", "linear_mfma.hip", "policy.hip", "adamw.hip"]
+           "linear.hip", "linear_f4.hip", "linear_mfma.hip", "linear_shares.hip",
+           "policy.hip", "adamw.hip"]
 ARCH = "gfx950"
 
 COMMON = [

@@ -96,7 +96,7 @@ __global__ void __launch_bounds__(P::threads) gated_mfma_kernel(
   const int tile = tile_of_block(blockIdx.x, ntx, nty);
   const int t0 = (tile / ntx) * P::BT, n0 = (tile % ntx) * P::BN;
   product_tile<AT, K, P, TWO, true>(bits, scales, X, ldx, T, m_pad, G, t0, n0, smem,
-                                    [&](const f32x16 (&acc)[P::TI][2], int wt, int wn) {
+                                    [&](const f32x16 (&acc)[P::TI][2], int wt, int wn, int) {
                                       gated_outputs<P>(acc, wt, wn, out, T, t0, n0, smem);
                                     });
 }

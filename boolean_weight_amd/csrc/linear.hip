@@ -106,17 +106,17 @@ RowSplit row_split(int m, int64_t T, bool whole) {
   return RowSplit{(int)((T + step - 1) / step), (int)step};
 }
 
-// More than 16 tokens on the few-token products.  A tile of the many-token kernel
-// walks its whole contraction, 0.42 us per 64 columns whatever the token count, and a
-// small layer has few tiles; the few-token kernel spreads the contraction over
-// wavefronts.  560: what the tiles take at least, 656e-5 us per column, less what the
-// estimate is off by; 300000 / n: 3 us a call more.  (us, few-token products / tiles,
-// K = 3: 2540 x 4480 33 tokens 9.9 / 29.3, 166 20.9 / 31.6, 300 37.0 / 32.3; 4096 x 11008
-// 64 27.7 / 72.0, 166 74.9 / 75.2; 11008 x 4096 33 32.4 / 29.1; 64 x 11008 300 14.8 /
-// 71.5; K = 2: 4096 x 4096 64 11.2 / 27.9, 166 25.3 / 28.4, 300 39.2 / 36.0; 1000 x 2048
-// 300 9.6 / 16.0.)
-bool in_chunks(const mbok_desc* d, int64_t T, int passes) {
-  return linear_chunks_cost(d, T) < 560 * passes - 300000 / d->n;
+// More than 16 tokens on the few-token products: the tiles' kernels walk their
+// contraction step by step whatever the token count, and a small layer has few tiles;
+// the few-token kernel spreads the contraction over wavefronts, of which each has at
+// least a group to take, so that below 8 groups it is no faster than with 8.  (us,
+// few-token products / tiles, K = 3: 4096 x 11008 33 and 64 tokens 29 / 43, 128 46 / 43,
+// 200 83 / 45; 11008 x 4096 33 33 / 19; 2000 x 640 200 9.7 / 6.9; K = 2: 4096 x 4096 128 15 /
+// 18, 200 28 / 19; 1000 x 2048 512 10.5 / 11.3, 700 18 / 12; 64 x 11008 1000 18 / 42; K = 4:
+// 724 x 1408 320 8.5 / 10.3, 450 14 / 10.)  560: tiles without shares.
+bool in_chunks(const mbok_desc* d, int64_t T, int passes, int shares) {
+  const int64_t tiles = (int64_t)(shares ? shares : 560) * passes;
+  return linear_chunks_cost(d, T) * (d->n < 1024 ? 1024 : d->n) < tiles * d->n;
 }
 
 }  // namespace
@@ -131,8 +131,10 @@ int launch_linear(const mbok_desc* d, const void* packed, const void* X, int64_t
         (int64_t)UINT32_MAX)
       return MBOK_ERR_SHAPE;
     if (ldx >= (int64_t(1) << 32) / 512) return MBOK_ERR_INVALID_ARG;
-    if (in_chunks(d, T, passes))
+    const int shares = linear_shares_cost(d, T);
+    if (in_chunks(d, T, passes, shares))
       return launch_linear_chunks(d, packed, X, T, ldx, out, stream);
+    if (shares) return launch_linear_shares(d, packed, X, T, ldx, out, passes, stream);
     return launch_linear_mfma(d, packed, X, T, ldx, out, passes, stream);
   }
   if (T == 1) return launch_linear_f4(d, packed, X, T, ldx, out, stream);

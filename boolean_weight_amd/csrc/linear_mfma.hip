@@ -2,122 +2,11 @@
 // (gfx950): product_tile of mfma_tile.h with an epilogue that adds the bias,
 // applies the activation and adds the residual in fp32 and rounds once.
 //
-// Bound: the matrix cores.  The sums of 64 tokens at a time go through LDS as
-// fp32, so that a thread holds 8 consecutive outputs of a token: whole 16-byte
-// accesses to Y, R and the pre-activations, one set of bias values per thread.
-#include "mbok_linear.h"
-#include "mfma_tile.h"
+// Bound: the matrix cores.
+#include "linear_tile.h"
 
 namespace mbok {
 namespace {
-
-// 8 bf16 or fp32 values of a row from p, `live` of them inside it
-template <bool F32>
-__device__ __forceinline__ void load8(const void* base, int64_t at, int live, float (&v)[8]) {
-  if constexpr (F32) {
-    typedef float f32x4_any __attribute__((ext_vector_type(4), aligned(4)));
-    const float* p = reinterpret_cast<const float*>(base) + at;
-    if (live == 8) {
-      const f32x4_any a = *reinterpret_cast<const f32x4_any*>(p),
-                      b = *reinterpret_cast<const f32x4_any*>(p + 4);
-#pragma unroll
-      for (int e = 0; e < 4; ++e) v[e] = a[e], v[4 + e] = b[e];
-      return;
-    }
-#pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] = e < live ? p[e] : 0.f;
-  } else {
-    const u32x4 w = load_piece(reinterpret_cast<const uint16_t*>(base) + at, live, false);
-#pragma unroll
-    for (int e = 0; e < 8; ++e)
-      v[e] = __uint_as_float((e & 1) ? w[e >> 1] & 0xffff0000u : w[e >> 1] << 16);
-  }
-}
-
-template <bool F32>
-__device__ __forceinline__ void store8(void* base, int64_t at, int live, const float (&v)[8]) {
-  if constexpr (F32) {
-    typedef float f32x4_any __attribute__((ext_vector_type(4), aligned(4)));
-    float* p = reinterpret_cast<float*>(base) + at;
-    if (live == 8) {
-      *reinterpret_cast<f32x4_any*>(p) = f32x4_any{v[0], v[1], v[2], v[3]};
-      *reinterpret_cast<f32x4_any*>(p + 4) = f32x4_any{v[4], v[5], v[6], v[7]};
-      return;
-    }
-#pragma unroll
-    for (int e = 0; e < 8; ++e)
-      if (e < live) p[e] = v[e];
-  } else {
-    uint16_t* p = reinterpret_cast<uint16_t*>(base) + at;
-    if (live == 8) {
-      *reinterpret_cast<u32x4_any*>(p) = u32x4_any{bf16_pair(v[0], v[1]), bf16_pair(v[2], v[3]),
-                                                   bf16_pair(v[4], v[5]), bf16_pair(v[6], v[7])};
-      return;
-    }
-#pragma unroll
-    for (int e = 0; e < 8; ++e)
-      if (e < live) p[e] = to_bf16(v[e]);
-  }
-}
-
-// The outputs of a tile, 32 TI tokens of each wavefront row in TI passes.
-template <typename P, bool F32>
-__device__ __forceinline__ void linear_outputs(const f32x16 (&acc)[P::TI][2], int wt, int wn,
-                                               const LinearOut& out, int T, int t0, int n0,
-                                               float* smem) {
-  constexpr int kThreads = P::threads, kPieces = P::BN / 8, kRows = 32 * P::WT;
-  constexpr int kStep = kThreads / kPieces;  // rows the workgroup takes at a time
-  static_assert(kThreads % kPieces == 0 && kRows % kStep == 0, "tile shape");
-  static_assert(sizeof(float) * kRows * P::FS <= P::lds, "the pass fits in LDS");
-  const int tid = threadIdx.x, lane = tid & 63;
-  const int c = 8 * (tid % kPieces), col = n0 + c;
-  const int live = max(0, min(8, out.m - col));
-  float bias[8];
-#pragma unroll
-  for (int e = 0; e < 8; ++e) bias[e] = e < live ? out.bias_at(col + e) : 0.f;
-#pragma unroll
-  for (int i = 0; i < P::TI; ++i) {
-    if (i) __syncthreads();  // the pass before has been read
-#pragma unroll
-    for (int j = 0; j < 2; ++j)
-#pragma unroll
-      for (int r = 0; r < 16; ++r)
-        smem[(32 * wt + 8 * (r >> 2) + 4 * (lane >> 5) + (r & 3)) * P::FS + 32 * (2 * wn + j) +
-             (lane & 31)] = acc[i][j][r];
-    __syncthreads();
-#pragma unroll
-    for (int s = 0; s < kRows / kStep; ++s) {
-      const int row = s * kStep + tid / kPieces;
-      const int64_t t = t0 + 32 * (P::TI * (row >> 5) + i) + (row & 31);
-      if (t >= T || live == 0) continue;
-      float y[8], z[8];
-#pragma unroll
-      for (int e = 0; e < 8; ++e) z[e] = smem[row * P::FS + c + e] + bias[e];
-      if (out.R) load8<F32>(out.R, t * out.ldr + col, live, y);
-      if (out.pre) store8<false>(out.pre, t * out.ldpre + col, live, z);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        float unused;
-        const float a = layer_activation<false>(out.act, z[e], unused);
-        y[e] = out.R ? y[e] + a : a;
-      }
-      store8<F32>(out.Y, t * out.ldy + col, live, y);
-    }
-  }
-}
-
-template <typename AT, int K, typename P, bool TWO, bool F32>
-__device__ __forceinline__ void linear_tile(const uint32_t* __restrict__ bits,
-                                            const AT* __restrict__ scales,
-                                            const uint16_t* __restrict__ X, int64_t ldx,
-                                            const LinearOut& out, int T, int m_pad, int G, int t0,
-                                            int n0, uint16_t* smem) {
-  product_tile<AT, K, P, TWO, false>(bits, scales, X, ldx, T, m_pad, G, t0, n0, smem,
-                                     [&](const f32x16 (&acc)[P::TI][2], int wt, int wn) {
-                                       linear_outputs<P, F32>(acc, wt, wn, out, T, t0, n0,
-                                                              reinterpret_cast<float*>(smem));
-                                     });
-}
 
 using Whole = Tile<2, 4, 4>;
 using Half = Tile<2, 4, 2>;  // half of a whole tile's tokens, all of its rows
@@ -176,12 +65,13 @@ void launch_k(const Geom& geo, const void* packed, const uint16_t* X, int64_t T,
     using P = decltype(tile);
     go(tile, tiles(P::BT, P::BN), 0);
   };
-  // Up to 64 tokens take tiles of 64 x 64.  More: rounds of 256 whole tiles, then
-  // what is left of them in halves where those make one round (half a whole tile
-  // takes 63% of its time: 11008 x 4096, K = 3, 2048 tokens, 344 tiles, 218 -> 189
-  // us; 4096 x 11008, 128 tiles, 205 -> 189) or nearly fill it (11008 x 4096, 512
-  // tokens, 86 tiles: 79 -> 71 us; 5120 x 5120, K = 2, 1000 tokens, 80 tiles: 80 -> 76;
-  // 512 tokens, 40 tiles: 58 -> 74), else whole; without a whole round and with
+  // (Calls of few tiles run in shares of the contraction instead, linear_shares.hip.)  Up
+  // to 64 tokens take tiles of 64 x 64.  More: rounds of 256 whole tiles, then what is
+  // left of them in halves where those make one round (half a whole tile takes 63% of
+  // its time: 11008 x 4096, K = 3, 2048 tokens, 344 tiles, 218 -> 189 us; 4096 x 11008,
+  // 128 tiles, 205 -> 189) or nearly fill it (11008 x 4096, 512 tokens, 86 tiles: 79 -> 71
+  // us; 5120 x 5120, K = 2, 1000 tokens, 80 tiles: 80 -> 76; 8192 x 1024, K = 2, 1000 tokens,
+  // 128 tiles: 24, 128 x 128 in shares 28), else whole; without a whole round and with
   // fewer tiles, 128 x 128 where those fill the part, else 64 x 64.
   const int64_t whole = tiles(256, 256), rest = whole % kUnits;
   if (T <= 64) all(Tile<2, 1, 1>{});

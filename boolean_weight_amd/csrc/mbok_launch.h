@@ -124,6 +124,11 @@ int launch_linear_skinny(const mbok_desc* d, const void* packed, const void* X, 
 int launch_linear_chunks(const mbok_desc* d, const void* packed, const void* X, int64_t T,
                          int64_t ldx, const LinearOut& out, hipStream_t stream);
 int64_t linear_chunks_cost(const mbok_desc* d, int64_t T);  // 1e-5 us per column
+// some hundred tokens, whose tiles leave much of the part idle; the cost (1e-5 us per
+// column) is 0 for calls that it does not take
+int linear_shares_cost(const mbok_desc* d, int64_t T);
+int launch_linear_shares(const mbok_desc* d, const void* packed, const void* X, int64_t T,
+                         int64_t ldx, const LinearOut& out, int passes, hipStream_t stream);
 int launch_linear_mfma(const mbok_desc* d, const void* packed, const void* X, int64_t T,
                        int64_t ldx, const LinearOut& out, int passes, hipStream_t stream);
 // the caller's arrays of one backward call (pre, dpre, dbias, dX may be null)

@@ -53,20 +53,27 @@ struct Tile {
 // PAIRS: the layer is a stacked one and a wavefront's two 32-row blocks become 32
 // gate rows and the same 32 up rows: the unpacking thread of stacked row 64 b +
 // 16 u + 8 h + r writes its weights to LDS row 64 b + 32 h + 8 u + r.
-// done(acc, wt, wn): the sums of the wavefront (wt, wn).  acc[i][j], register r of
+// C: workgroups of C times the tile's threads, each C-th of the wavefronts with its
+// own LDS and its share of the scale groups (G >= C), for tiles too few to fill the
+// part; the shares' sums are done's to add.
+// done(acc, wt, wn, part): the sums of the wavefront (wt, wn).  acc[i][j], register r of
 // lane l: token 32 (TI wt + i) + 8 (r / 4) + 4 (l / 32) + r % 4 of the tile, LDS
 // row 32 (2 wn + j) + l % 32.  LDS is free by then, behind a barrier.
-template <typename AT, int K, typename P, bool TWO, bool PAIRS, typename Done>
+template <typename AT, int K, typename P, bool TWO, bool PAIRS, int C = 1, typename Done>
 __device__ __forceinline__ void product_tile(const uint32_t* __restrict__ bits,
                                              const AT* __restrict__ scales,
                                              const uint16_t* __restrict__ X, int64_t ldx, int T,
                                              int m_pad, int G, int t0, int n0, uint16_t* smem,
                                              Done&& done) {
   constexpr int TI = P::TI, NU = P::NU, kThreads = P::threads;
-  const int tid = threadIdx.x, lane = tid & 63;
+  const int part = C == 1 ? 0 : __builtin_amdgcn_readfirstlane((int)threadIdx.x / kThreads);
+  const int tid = C == 1 ? (int)threadIdx.x : (int)threadIdx.x % kThreads, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int S = (TWO ? 4 : 2) * G;  // steps
-  auto block = [](int s) { return TWO ? s >> 1 : s; };  // 64 columns of a step
+  smem += part * (P::lds / 2);
+  const int g0 = part * G / C, g1 = (part + 1) * G / C;
+  const int S = (TWO ? 4 : 2) * (g1 - g0);  // steps
+  // 64 columns of a step
+  auto block = [g0](int s) { return (C == 1 ? 0 : 2 * g0) + (TWO ? s >> 1 : s); };
   auto xbuf = [&](int b) { return smem + b * (P::kX + P::kW); };
   auto wbuf = [&](int b) { return smem + b * (P::kX + P::kW) + P::kX; };
 
@@ -234,10 +241,12 @@ __device__ __forceinline__ void product_tile(const uint32_t* __restrict__ bits,
     step(s, 0, R1);
     step(s + 1, 1, R0);
   }
+  if constexpr (C > 1)  // the barriers of a longer share
+    for (int s = S; s < (TWO ? 4 : 2) * ((G + C - 1) / C); ++s) __syncthreads();
   copies_done();
 
   __syncthreads();
-  done(acc, wt, wn);
+  done(acc, wt, wn, part);
 }
 
 // The tile of workgroup b: XCD b % 8 takes consecutive positions of the tile order

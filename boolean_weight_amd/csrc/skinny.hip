@@ -726,9 +726,10 @@ int launch_linear_skinny(const mbok_desc* d, const void* packed, const void* X, 
   return launch_out_skinny(d, packed, X, T, ldx, out, stream);
 }
 
-// Tiles and 16-token chunks of a workgroup, one to a compute unit, and the time of the
-// call's rounds of them per column and kernel, in 1e-5 us (measured, 1408 to 11008
-// columns: a round takes that and about 5 us): the shape that takes least.
+// Tiles and 16-token chunks of a workgroup, one to a compute unit, and what a round of
+// them takes (relative; measured, 1408 to 11008 columns): the shape that takes least.
+// Per column a round takes that times 2.4, 2.9, 3.4 or 3.9 e-5 us at 1 to 4 kernels, and
+// the call 3 to 4 us more.
 struct ChunkShape {
   int R, C;
   int64_t cost;
@@ -745,7 +746,7 @@ static ChunkShape chunk_shape(const Geom& geo, int64_t T) {
 }
 
 int64_t linear_chunks_cost(const mbok_desc* d, int64_t T) {
-  return chunk_shape(make_geom(d), T).cost * d->K;
+  return chunk_shape(make_geom(d), T).cost * (19 + 5 * d->K) / 10;
 }
 
 template <typename AT>

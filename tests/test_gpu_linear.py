@@ -107,6 +107,33 @@ def test_linear_small_layers_exact(T, m, n, K):
     assert torch.equal(again, y)
 
 
+# the many-token forms: 64 x 64 tiles in 4 and in 2 shares of the contraction (groups
+# that do not divide by them, fewer groups than shares), 128 x 128 in 2, and tiles of 64
+# and 128 whole
+@pytest.mark.parametrize("T,m,n", [(100, 300, 640), (65, 9, 896), (250, 1030, 1408), (40, 70, 384),
+                                   (260, 4100, 512), (1000, 2300, 384), (129, 9000, 256),
+                                   (300, 300, 128), (50, 33000, 128), (2048, 2300, 128)])
+@pytest.mark.parametrize("K", [1, 2, 3, 4])
+def test_linear_few_tiles_exact(T, m, n, K):
+    say(f"linear few tiles T={T} m={m} n={n} K={K}")
+    dt = "f32" if K % 2 else "f16"
+    S, A = exact_layer(m, n, K, dt, m + n + K)
+    d, packed = pack_on_gpu(S, A, dt)
+    X, R = ints(T, n, T + n), ints(T, m, T + m)
+    buf = torch.full((T, m + 9), -5.0, device=DEV)
+    pbuf = torch.full((T, m + 7), -5.0, dtype=BF, device=DEV)
+    y, pre = buf[:, 4:4 + m], pbuf[:, 3:3 + m]
+    x = wide(X, n + 8, off=0)
+    bw.mbok_linear(d, packed, x, y, residual=R.to(DEV), pre=pre)
+    want, z = ref.linear(finetune_ref.dense(S, A), X, None, "none", R)
+    assert torch.equal(y.cpu().to(F64), want)
+    assert torch.equal(pre.cpu().to(F64), bf16_of(z))
+    assert guards_hold(buf, 4, m) and guards_hold(pbuf, 3, m)
+    again = torch.empty(T, m, dtype=BF, device=DEV)
+    bw.mbok_linear_precise(d, packed, x, again, residual=R.to(DEV, BF))
+    assert torch.equal(again.cpu().to(F64), bf16_of(want))
+
+
 def bound_of(T, W, X, z):
     few = T <= 16
     # T <= 16: every scale exact in fp32, activations to 2^-16 at worst (f4 forms)
