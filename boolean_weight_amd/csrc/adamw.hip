@@ -13,7 +13,7 @@
 //
 // Bound: memory, 28 bytes a parameter with fp32 states and gradients, 16 with
 // 8-bit ones, beside the copy.  (29.5 M scales of 48 layers, fp32
-// gradients: 200 us of 0.89 GB, 4.4 TB/s; 8-bit states 129 us of 0.54 GB, 4.2 TB/s, and
+// gradients: 204 us of 0.89 GB, 4.4 TB/s; 8-bit states 131 us of 0.54 GB, 4.1 TB/s, and
 // 60 M vector instructions, which alone take 100.)
 //
 // 8-bit states: 256 consecutive values, one wavefront's 64 lanes x 4, share a
@@ -231,7 +231,7 @@ __device__ __forceinline__ float new_param(const Rule& rule, float p, float m, f
 template <bool EIGHT, typename GT, typename Put>
 __device__ __forceinline__ void update(const AdamTensor& t, const Rule& rule, int64_t start,
                                        int len, Put&& put) {
-  constexpr int U = 1;  // accesses in flight; of 2, 5 wavefronts per SIMD instead of 6: 140 -> 129 us
+  constexpr int U = 1;  // accesses in flight; 2: 5 wavefronts per SIMD, not 6 (8 bits 141 us, not 131)
   const GT* grad = reinterpret_cast<const GT*>(t.grad) + start;
   float* param = t.param + start;
   const int lane = threadIdx.x & (kWave - 1);
