@@ -96,7 +96,8 @@ struct Policy {
   // the loss of row t and d loss / d logp, without the weight
   __device__ __forceinline__ double of(int64_t t, double logp, double& slope) const {
     const double A = (double)adv[t];
-    const double r = old ? exp(logp - (double)old[t]) : 1.0;
+    // without old the present logp is its own: 1, or NaN where there is none
+    const double r = old ? exp(logp - (double)old[t]) : logp != logp ? logp : 1.0;
     // an advantage of 0 gains nothing at any ratio, an infinite one included
     double gain = 0.0;
     slope = 0.0;

@@ -920,11 +920,13 @@ int mbok_policy_desc_init(mbok_policy_desc* d, int32_t vocab, float temperature,
  * r = 1 + clip_high and r = 1 - clip_low count as not clipped.  An advantage of 0
  * gains nothing at any ratio.  A row without a token has loss, logp and gradient
  * 0; a row of weight 0 has loss and gradient 0 and is read only where logp or
- * stats are asked for.  Non-finite logits as for mbok_logp.
+ * stats are asked for.  Non-finite logits as for mbok_logp: a row whose logp is NaN
+ * has loss, dlogp and all of dZ NaN.
  *  Z, z_dtype, T, ldz, label, logp (or NULL), stats (or NULL): as for mbok_logp.
  *  advantage  device fp32 [T], A.
  *  old_logp   device fp32 [T] or NULL: the log-probabilities when the tokens were
- *             sampled; NULL takes the present ones (r = 1, its slope kept).
+ *             sampled; NULL takes the present ones (r = 1, its slope kept; NaN where
+ *             logp is NaN).
  *  ref_logp   device fp32 [T] or NULL: a reference model's (NULL: no KL term).
  *  weight     device fp32 [T] or NULL (all 1): w.
  *  loss       device fp32 [T]; overwritten.

@@ -1,0 +1,59 @@
+"""GPU tests of the policy loss on rows that hold no numbers: what the formula gives
+in float64, not-a-number and infinities included."""
+import math
+
+import pytest
+import torch
+
+import boolean_weight_amd as bw
+from gpu_util import DEV, say
+
+pytestmark = pytest.mark.gpu
+
+NAN, INF = math.nan, math.inf
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _gpu():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    bw.load_library()
+    yield
+    torch.cuda.synchronize()
+
+
+def broken_rows(V, dtype, T=7):
+    """Rows 0 to 2 have no log-probability (a NaN, a +inf, -inf alone); the others do."""
+    gen = torch.Generator().manual_seed(V)
+    Z = torch.randn(T, V, generator=gen).to(dtype)
+    Z[0, V // 2] = NAN
+    Z[1, V - 1] = INF
+    Z[2] = -INF
+    return Z.to(DEV), torch.full((T,), 1, dtype=torch.int32, device=DEV)
+
+
+def outputs(T, Z):
+    return dict(loss=torch.full((T,), -5.0, device=DEV), dlogp=torch.full((T,), -5.0, device=DEV),
+                dZ=torch.full_like(Z, -7.0))
+
+
+# vocabularies of the register forms of few and of many rows, and past them
+@pytest.mark.parametrize("T,V", [(7, 40), (600, 9000), (7, 140003)])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("advantage", [1.5, 0.0, -2.0])
+@pytest.mark.parametrize("with_ref", [False, True])
+def test_broken_rows_without_old_logp(T, V, dtype, advantage, with_ref):
+    """exp(logp - logp) of a NaN is NaN: loss, slope and gradient say so, and no other
+    row does."""
+    say(f"policy broken rows T={T} V={V} {dtype} A={advantage} ref={with_ref}")
+    Z, label = broken_rows(V, dtype, T)
+    A = torch.full((T,), advantage, device=DEV)
+    out = outputs(T, Z)
+    ref = torch.full((T,), -3.0, device=DEV) if with_ref else None
+    bw.mbok_policy(bw.mbok_policy_desc_init(V, kl=0.1), Z, label, A, ref_logp=ref, **out)
+    for name, x in out.items():
+        bad = torch.isnan(x.float()).view(T, -1)
+        assert bad[:3].all(), name
+        assert torch.isfinite(x.float()).view(T, -1)[3:].all(), name
+    if not with_ref:  # a ratio of 1
+        assert (out["loss"][3:] == -advantage).all() and (out["dlogp"][3:] == -advantage).all()
