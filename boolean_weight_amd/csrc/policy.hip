@@ -107,7 +107,7 @@ struct Policy {
       if (!clipped) slope = -r * A;
     }
     double loss = -gain;
-    if (ref) {
+    if (ref && kl != 0.f) {  // 0 times an infinite divergence is no KL term
       const double x = (double)ref[t] - logp, y = expm1(x);
       loss += (double)kl * (y - x);
       slope -= (double)kl * y;

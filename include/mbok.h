@@ -927,7 +927,8 @@ int mbok_policy_desc_init(mbok_policy_desc* d, int32_t vocab, float temperature,
  *  old_logp   device fp32 [T] or NULL: the log-probabilities when the tokens were
  *             sampled; NULL takes the present ones (r = 1, its slope kept; NaN where
  *             logp is NaN).
- *  ref_logp   device fp32 [T] or NULL: a reference model's (NULL: no KL term).
+ *  ref_logp   device fp32 [T] or NULL: a reference model's.  NULL, or beta 0: no KL
+ *             term, whatever it holds.
  *  weight     device fp32 [T] or NULL (all 1): w.
  *  loss       device fp32 [T]; overwritten.
  *  dlogp      device fp32 [T] or NULL; overwritten: with stats, what

@@ -57,3 +57,26 @@ def test_broken_rows_without_old_logp(T, V, dtype, advantage, with_ref):
         assert torch.isfinite(x.float()).view(T, -1)[3:].all(), name
     if not with_ref:  # a ratio of 1
         assert (out["loss"][3:] == -advantage).all() and (out["dlogp"][3:] == -advantage).all()
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("with_old", [False, True])
+def test_no_kl_term_at_weight_zero(dtype, with_old):
+    """With kl = 0 there is no KL term, whatever the reference model's values are: the
+    bits of the call without them."""
+    say(f"policy kl=0 {dtype} old={with_old}")
+    T, V = 8, 50
+    gen = torch.Generator().manual_seed(3)
+    Z = torch.randn(T, V, generator=gen).to(dtype)
+    Z[1, 1] = -INF  # the row's token: logp -inf
+    Z, label = Z.to(DEV), torch.full((T,), 1, dtype=torch.int32, device=DEV)
+    A = torch.tensor([1.0, 1.0, -1.0, 0.0, 2.0, -2.0, 1.0, 1.0], device=DEV)
+    old = torch.full((T,), -4.0, device=DEV) if with_old else None
+    ref = torch.tensor([-INF, -2.0, 2000.0, NAN, INF, -1e30, 3e38, 0.0], device=DEV)
+    d = bw.mbok_policy_desc_init(V, kl=0.0)
+    got, want = outputs(T, Z), outputs(T, Z)
+    bw.mbok_policy(d, Z, label, A, old_logp=old, ref_logp=ref, **got)
+    bw.mbok_policy(d, Z, label, A, old_logp=old, **want)
+    for name in got:
+        assert torch.isfinite(got[name].float()).all(), name
+        assert torch.equal(got[name], want[name]), name
