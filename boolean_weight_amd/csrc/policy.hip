@@ -108,8 +108,9 @@ struct Policy {
     }
     double loss = -gain;
     if (ref && kl != 0.f) {  // 0 times an infinite divergence is no KL term
+      // x of +inf: a token at -inf that the reference finds possible (y - x is no number)
       const double x = (double)ref[t] - logp, y = expm1(x);
-      loss += (double)kl * (y - x);
+      loss += (double)kl * (y == INFINITY ? y : y - x);
       slope -= (double)kl * y;
     }
     return loss;

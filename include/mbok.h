@@ -921,7 +921,8 @@ int mbok_policy_desc_init(mbok_policy_desc* d, int32_t vocab, float temperature,
  * gains nothing at any ratio.  A row without a token has loss, logp and gradient
  * 0; a row of weight 0 has loss and gradient 0 and is read only where logp or
  * stats are asked for.  Non-finite logits as for mbok_logp: a row whose logp is NaN
- * has loss, dlogp and all of dZ NaN.
+ * has loss, dlogp and all of dZ NaN.  A token at -inf beside a finite ref_logp has
+ * loss +inf, dlogp -inf and a row of dZ that is not finite; at -inf in both, NaN.
  *  Z, z_dtype, T, ldz, label, logp (or NULL), stats (or NULL): as for mbok_logp.
  *  advantage  device fp32 [T], A.
  *  old_logp   device fp32 [T] or NULL: the log-probabilities when the tokens were

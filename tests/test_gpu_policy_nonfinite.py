@@ -80,3 +80,38 @@ def test_no_kl_term_at_weight_zero(dtype, with_old):
     for name in got:
         assert torch.isfinite(got[name].float()).all(), name
         assert torch.equal(got[name], want[name]), name
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("with_old", [False, True])
+def test_kl_term_of_a_masked_token(dtype, with_old):
+    """x = ref - logp: exp(x) - x - 1 grows without bound both ways.  A token at -inf that
+    the reference model finds possible costs +inf, with slope -inf; one that both rule out
+    has no x (NaN); one that only the reference rules out costs +inf too, with slope beta
+    beside the ratio's."""
+    say(f"policy token at -inf {dtype} old={with_old}")
+    T, V, kl = 6, 50, 0.25
+    gen = torch.Generator().manual_seed(4)
+    Z = torch.randn(T, V, generator=gen).to(dtype)
+    Z[:3, 1] = -INF
+    Z, label = Z.to(DEV), torch.full((T,), 1, dtype=torch.int32, device=DEV)
+    A = torch.ones(T, device=DEV)
+    # the ratio of a masked token is 0, or 1 without old_logp
+    old = torch.full((T,), -4.0, device=DEV) if with_old else None
+    ref = torch.tensor([-2.0, -1e4, -INF, -INF, 2000.0, -3.0], device=DEV)
+    out = outputs(T, Z)
+    logp = torch.empty(T, device=DEV)
+    bw.mbok_policy(bw.mbok_policy_desc_init(V, clip_high=INF, kl=kl), Z, label, A, old_logp=old,
+                   ref_logp=ref, logp=logp, **out)
+    loss, slope, lp = out["loss"].cpu(), out["dlogp"].cpu(), logp.cpu().double()
+    assert (lp[:3] == -INF).all() and torch.isfinite(lp[3:]).all()
+    assert (loss[:2] == INF).all() and (slope[:2] == -INF).all()
+    assert torch.isnan(loss[2]) and torch.isnan(slope[2])
+    assert loss[3] == INF and loss[4] == INF and slope[4] == -INF
+    r = (lp + 4.0).exp() if with_old else torch.ones(T, dtype=torch.float64)
+    # logp's 2^-16 (see test_gpu_policy.py) in a slope of |r A| <= e^4 and in x
+    tol = 2.0 ** -15 * (r[3] + 1)
+    assert abs(float(slope[3]) - float(kl - r[3])) <= tol
+    x = -3.0 - float(lp[5])
+    want = -float(r[5]) + kl * (math.expm1(x) - x)
+    assert abs(float(loss[5]) - want) <= 2.0 ** -15 * (float(r[5]) + kl * (math.exp(x) + 1))
