@@ -74,6 +74,11 @@ __device__ __forceinline__ float lanes_max(float v) {
   for (int s = 32; s; s >>= 1) v = fmaxf(v, __shfl_xor(v, s));
   return v;
 }
+__device__ __forceinline__ int lanes_max(int v) {
+#pragma unroll
+  for (int s = 32; s; s >>= 1) v = max(v, __shfl_xor(v, s));
+  return v;
+}
 __device__ __forceinline__ double lanes_sum(double v) {
 #pragma unroll
   for (int s = 32; s; s >>= 1) v += __shfl_xor(v, s);

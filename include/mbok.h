@@ -971,7 +971,8 @@ int mbok_preference_desc_init(mbok_preference_desc* d, float beta, float smoothi
  * dlogp goes to mbok_logp_backward; its rows outside every sequence are left as
  * they were.
  *  offsets  device int32 [2 pairs + 1], not decreasing, within 0 .. T (values
- *           outside are cut to that range, a decreasing one to the one before).
+ *           outside are cut to that range, a decreasing one is read as the largest
+ *           before it: no two sequences share a row).
  *  pairs    1 .. MBOK_MAX_PAIRS.
  *  logp     device fp32 [T], of mbok_logp.
  *  ref_logp device fp32 [T] or NULL (all 0): the reference model's.
