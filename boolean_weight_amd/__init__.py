@@ -14,6 +14,7 @@ import ctypes
 import functools
 import os
 import threading
+import warnings
 
 import torch
 
@@ -111,6 +112,7 @@ class mbok_policy_desc(ctypes.Structure):
 class mbok_preference_desc(ctypes.Structure):
     _fields_ = [("beta", ctypes.c_float), ("smoothing", ctypes.c_float),
                 ("margin", ctypes.c_float), ("mean", ctypes.c_int32), ("vocab", ctypes.c_int32)]
+    vocab_left_out = False  # see mbok_preference_desc_init
 
     def __repr__(self):
         return (f"mbok_preference_desc(beta={self.beta}, smoothing={self.smoothing}, "
@@ -1197,11 +1199,15 @@ def mbok_policy(d: mbok_policy_desc, Z: torch.Tensor, label: torch.Tensor,
 
 def mbok_preference_desc_init(beta: float, smoothing: float = 0.0, margin: float = 0.0,
                               mean: bool = False,
-                              vocab: int = MBOK_MAX_VOCAB) -> mbok_preference_desc:
+                              vocab: int | None = None) -> mbok_preference_desc:
+    """vocab: the logits' V, as mbok_logp's descriptor has it.  Left out, every label of
+    0 to MBOK_MAX_VOCAB - 1 counts as a token, a padding id of V or more too, whose row
+    mbok_logp gives no log-probability: mbok_preference warns if it is given labels then."""
     d = mbok_preference_desc()
-    _check(load_library().mbok_preference_desc_init(ctypes.byref(d), beta, smoothing, margin,
-                                                    int(bool(mean)), vocab),
-           "mbok_preference_desc_init")
+    _check(load_library().mbok_preference_desc_init(
+        ctypes.byref(d), beta, smoothing, margin, int(bool(mean)),
+        MBOK_MAX_VOCAB if vocab is None else vocab), "mbok_preference_desc_init")
+    d.vocab_left_out = vocab is None
     return d
 
 
@@ -1212,7 +1218,7 @@ def mbok_preference(d: mbok_preference_desc, offsets: torch.Tensor, logp: torch.
     """loss[pairs] (fp32, overwritten) of paired log ratios: sequences 2p (chosen)
     and 2p + 1 (rejected) are rows offsets[s] .. offsets[s + 1] - 1 (int32 [2 pairs +
     1]) of logp [T], less the reference model's ref_logp [T]; rows without a token
-    (label) do not count.  dlogp [T] receives the gradient for mbok_logp_backward."""
+    (label negative, or the descriptor's vocab or more) do not count.  dlogp [T] receives the gradient for mbok_logp_backward."""
     dev = _first(logp, "logp")
     T = logp.numel()
     if not isinstance(offsets, torch.Tensor):
@@ -1220,6 +1226,10 @@ def mbok_preference(d: mbok_preference_desc, offsets: torch.Tensor, logp: torch.
     if offsets.dim() != 1 or offsets.numel() < 3 or offsets.numel() % 2 == 0:
         raise ValueError("offsets must be [2 pairs + 1]")
     pairs = offsets.numel() // 2
+    if label is not None and d.vocab_left_out:
+        d.vocab_left_out = False  # once
+        warnings.warn("mbok_preference: the descriptor has no vocabulary, so labels of V or more "
+                      "count as tokens; pass vocab to mbok_preference_desc_init", stacklevel=2)
     _launch(load_library().mbok_preference, "mbok_preference", dev, stream, ctypes.byref(d),
             _vector(offsets, "offsets", dev, 2 * pairs + 1, torch.int32), pairs,
             _vector(logp, "logp", dev, T, torch.float32),

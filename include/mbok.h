@@ -976,7 +976,9 @@ int mbok_preference_desc_init(mbok_preference_desc* d, float beta, float smoothi
  *  pairs    1 .. MBOK_MAX_PAIRS.
  *  logp     device fp32 [T], of mbok_logp.
  *  ref_logp device fp32 [T] or NULL (all 0): the reference model's.
- *  label    device int32 [T] or NULL (every row holds a token), as for mbok_logp.
+ *  label    device int32 [T] or NULL (every row holds a token), as for mbok_logp with
+ *           the descriptor's vocab: the logits' own, or rows that mbok_logp finds no
+ *           token in (labels of V or more) count.
  *  T        1 .. MBOK_MAX_DISTILL_ROWS.
  *  weight   device fp32 [pairs] or NULL (all 1): w.  A pair of weight 0 has loss
  *           and dlogp 0.
