@@ -1340,7 +1340,7 @@ def mbok_adamw(plan: mbok_adamw_plan, lr: float, step: int, beta1: float = 0.9,
     """One AdamW step on every tensor of the plan, in one launch; step counts from
     1.  Gradients are multiplied by grad_scale.  live fp32 [4] on the device (lr,
     grad_scale, step, skip) is read in place of those arguments when the step runs,
-    for steps captured into a graph."""
+    for steps captured into a graph; a step below 1 there is skipped."""
     if not isinstance(plan, mbok_adamw_plan):
         raise TypeError("plan must be mbok_adamw_plan_init's")
     dev = plan.device

@@ -376,14 +376,15 @@ __device__ __forceinline__ void update_layer(const AdamTensor& t, const Rule& ru
   }
 }
 
-// the step's own numbers, from the host or (live) from device memory
+// the step's own numbers, from the host or (live) from device memory; false: no step (the
+// skip flag, or a count below 1, as a zeroed buffer holds it: 1 - b^0 would divide by 0)
 __device__ __forceinline__ bool step_of(const AdamStep& s, const float* live, const AdamTensor& t,
                                         Rule& rule) {
   double lr = s.lr, c1 = s.correct1, c2 = s.correct2;
   float scale = s.grad_scale;
   uint32_t key = s.key;
   if (live) {
-    if (live[3] != 0.f) return false;
+    if (live[3] != 0.f || !(live[2] >= 1.f)) return false;
     lr = (double)live[0];
     scale = live[1];
     const double n = (double)live[2];

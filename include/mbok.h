@@ -1075,10 +1075,11 @@ typedef struct mbok_adamw_step {
  * 0.  Scales are at least 2^-87.
  *  table  device, the plan's table, 16-byte aligned; it and the tensors are read when
  *         the step runs, so a captured step needs them as long as its graph lives.
- *  live   device fp32 [4] or NULL: lr, grad_scale, t (a whole number below 2^24)
+ *  live   device fp32 [4] or NULL: lr, grad_scale, t (a whole number from 1, below 2^24)
  *         and a flag, read when the step runs (so that a captured step follows
  *         them) instead of the constants of `step`; a flag other than 0 (an
- *         overflow was found) skips the step: nothing is written.
+ *         overflow was found) or t below 1 or NaN (a buffer not filled yet) skips the
+ *         step: nothing is written.
  * Errors: INVALID_ARG (NULL, constants out of range, a plan that is none), ALIGN
  * (table 16 bytes, live 4), HIP.
  */
