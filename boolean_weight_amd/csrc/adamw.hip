@@ -25,7 +25,8 @@
 // value of a code is the value: r, which the update divides by, follows its
 // decay in the mean (its square up to a sixteenth slower, by the codes'
 // variance).  A value r that is not 0 keeps code 1 at least, so that no m is
-// divided by eps alone.
+// divided by eps alone, down to the r whose squares are 0 in fp32 (2^-75; with fp32
+// states v is 0 there, too).
 #include <math.h>
 
 #include <algorithm>

@@ -1071,8 +1071,9 @@ typedef struct mbok_adamw_step {
  * stochastically to e4m3 with a power-of-two scale per block that puts its
  * largest magnitude in [128, 256); the random bits are a hash of seed, t, the
  * tensor's place in the plan and the value's.  A value that is not finite makes
- * its block's scale NaN.  A root of the second moment that is not 0 never becomes
- * 0.  Scales are at least 2^-87.
+ * its block's scale NaN.  A root of the second moment of 2^-74 or more is not 0 after
+ * a step with beta2 of 1/2 or more (the square of a smaller one is 0 in fp32, as it is
+ * with fp32 states).  Scales are at least 2^-87.
  *  table  device, the plan's table, 16-byte aligned; it and the tensors are read when
  *         the step runs, so a captured step needs them as long as its graph lives.
  *  live   device fp32 [4] or NULL: lr, grad_scale, t (a whole number from 1, below 2^24)
