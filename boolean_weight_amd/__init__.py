@@ -1243,12 +1243,25 @@ def mbok_preference(d: mbok_preference_desc, offsets: torch.Tensor, logp: torch.
 
 class mbok_adamw_plan:
     """The tensors of an optimizer step (mbok_adamw_plan_init): the library's plan,
-    its table on the device, and the tensors, which it keeps alive."""
+    its table on the device, and the tensors, which it keeps alive.
+
+    The plan may be dropped while a step that it was given to still runs on one of
+    torch's streams: the table's memory is not given away before.  On a stream that is
+    not torch's (which may end first) the step has to have run by then."""
 
     def __init__(self, plan, table: torch.Tensor, tensors: list):
         self._plan, self.table, self.tensors = plan, table, tensors
         self._args = (ctypes.byref(plan), table.data_ptr())
         self.device = table.get_device()
+        self._streams = set()  # handles that the table's memory waits for
+
+    def _read_on(self, handle: int, stream) -> None:
+        """The table is read on a stream other, perhaps, than the one it is tied to."""
+        s = _torch_stream(torch.device("cuda", self.device), stream)
+        # a stream of another owner has its handle for an id
+        if handle == 0 or s.stream_id != handle:
+            self.table.record_stream(s)
+        self._streams.add(handle)
 
     def __repr__(self):
         return f"mbok_adamw_plan({self._plan.tensors} tensors, {self._plan.parts} parts)"
@@ -1314,7 +1327,8 @@ def mbok_adamw_plan_init(tensors) -> mbok_adamw_plan:
     bf16; with layer, a mbok_desc, the layer's packed buffer, whose scales the step
     writes from param [K, m, n/128]) and weight_decay.  The plan holds their
     addresses: gradients are expected in the same tensors at every step, and a graph
-    that captured a step needs the plan as long as it is replayed."""
+    that captured a step needs the plan as long as it is replayed (after eager steps it
+    may be dropped, see mbok_adamw_plan)."""
     tensors = [dict(t) for t in tensors]
     if not tensors:
         raise ValueError("a plan needs at least one tensor")
@@ -1346,7 +1360,10 @@ def mbok_adamw(plan: mbok_adamw_plan, lr: float, step: int, beta1: float = 0.9,
     dev = plan.device
     ptr = None if live is None else _vector(live, "live", dev, 4, torch.float32)
     s = _AdamwStep(lr, beta1, beta2, eps, step, grad_scale, seed & 0xffffffff)
-    _launch(load_library().mbok_adamw, "mbok_adamw", dev, stream, *plan._args, ctypes.byref(s),
+    handle = _raw_stream(dev) if stream is None else _stream(stream)
+    if handle not in plan._streams:
+        plan._read_on(handle, stream)
+    _launch(load_library().mbok_adamw, "mbok_adamw", dev, handle, *plan._args, ctypes.byref(s),
             ptr)
 
 
