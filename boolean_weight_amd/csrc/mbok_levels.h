@@ -138,10 +138,11 @@ __device__ __forceinline__ Levels make_levels(const float* a) {
 // V[b]'s nibble 2e + a are the level index of quad q = 4a + b, element e (the
 // nibble's other bits are other quads').  Two words are merged for two b at a
 // time.
+// (a & mask) | (b & ~mask), the compiler's own instruction: it knows which registers
+// matrix instructions in flight still read or write, which it does not for assembly
+// (see skinny.hip).  (0xE4: the truth table; written out, it is taken apart into three.)
 __device__ __forceinline__ uint32_t bit_select(uint32_t mask, uint32_t a, uint32_t b) {
-  uint32_t d;  // (a & mask) | (b & ~mask); the compiler takes it apart into three
-  asm("v_bfi_b32 %0, %1, %2, %3" : "=v"(d) : "s"(mask), "v"(a), "v"(b));
-  return d;
+  return __builtin_amdgcn_bitop3_b32(a, b, mask, 0xE4);
 }
 // Holds loaded signs and scales in registers at this point of the program, so
 // that their loads are not moved past a later barrier.
