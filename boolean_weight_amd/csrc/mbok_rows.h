@@ -47,7 +47,7 @@ __device__ __forceinline__ RowVec<T> load_row(const T* row, int v, int V) {
 
 // The gradient of one vector of logits: N values of OT, 8 or 16 bytes.  stream:
 // past the caches, for rows that start 16-byte aligned (2048 x 32000 bf16 policy
-// step 57.7 -> 53.1 us; rows at any element, 2048 x 12345 fp32, 45.2 -> 47.1).
+// step 61.8 -> 56.6 us; rows at any element, 2048 x 12345 fp32, 45.2 -> 47.1).
 template <typename OT, int N>
 __device__ __forceinline__ void store_row(OT* row, int v, int V, const float (&d)[N],
                                           bool stream) {

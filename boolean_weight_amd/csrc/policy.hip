@@ -15,8 +15,9 @@
 // Bound: the row of logits, read once and (gradient) written once.  As in the
 // distillation loss one workgroup takes a row and keeps it in registers, so
 // maximum, sum and gradient cost one read.  (2048 rows of 32000 bf16 logits with the
-// gradient: 53-59 us, 4.4-4.9 TB/s of the 262 MB; logp alone 28 us, its gradient 37-41;
-// 301 rows of 12345 fp32 ones 10 us.)
+// gradient: 56-60 us, 4.4-4.7 TB/s of the 262 MB; logp alone 28-32 us, its gradient 37
+// behind it, 49 where nothing of the row is cached; 301 rows of 12345 fp32 ones 10-11 us;
+// 512 rows of 128000 bf16 ones, 16 vectors per thread, 63, of 152000, read again, 94.)
 // The ratio stands next to a border (1 + hi), so what is formed from the row's
 // sum is float64.
 #include <math.h>
@@ -118,9 +119,21 @@ struct Policy {
 };
 struct NoLoss {};
 
+// Wavefronts per SIMD.  A held row of 8 vectors and the loss in float64 take 72 registers,
+// 7 of them; 8 spill 2 values of fp32 logits, 3 of bf16 and 82 of fp16 ones.  (Policy
+// step, us, 7 / 8: 2048 x 32000 fp16 55 / 102, bf16 57 / 60, 600 x 9000 bf16 9.1 / 9.8, 2048 x
+// 16000 fp32 55 / 54.  Of 1024 threads 7 leave one row on a compute unit instead of two:
+// 2048 x 60000 bf16 130 / 107, fp16 127 / 179.)
+template <typename ZT>
+constexpr int row_waves(int nv, int threads, bool grad) {
+  if (nv > 8) return 4;
+  const bool f16 = std::is_same<ZT, _Float16>::value;
+  return grad && nv == 8 && (f16 || (sizeof(ZT) == 2 && threads < 1024)) ? 7 : 8;
+}
+
 // LOSS: Policy or NoLoss (log-probabilities alone).  GRAD: with dZ.
 template <typename ZT, typename OT, int NV, int THREADS, bool GRAD, typename Loss>
-__global__ void __launch_bounds__(THREADS, NV <= 8 ? 8 : 4) row_kernel(
+__global__ void __launch_bounds__(THREADS, row_waves<ZT>(NV, THREADS, GRAD)) row_kernel(
     const ZT* Z, int64_t ldz, const int32_t* __restrict__ label, RowShape s,
     float* __restrict__ logp_out, RowStats* __restrict__ stats, OT* dZ, int64_t lddz, Loss loss) {
   constexpr int N = RowVec<ZT>::N;
@@ -462,8 +475,8 @@ int row_threads(int64_t T, int nvec, int want) {
 }
 
 // A row's workgroup: with many rows the fewest threads that hold it in 8 vectors
-// each (4 resident rows per compute unit hide one another's reductions: 1024 x
-// 32000 bf16 logits, policy step, 27.7 us with 512 threads, 30.5 with 1024); with
+// each (3 or 4 resident rows per compute unit hide one another's reductions: 1024 x
+// 32000 bf16 logits, policy step, 27.3 us with 512 threads, 30.5 with 1024); with
 // few the fewest that do in 4 (32000 bf16, 64 rows 8.9 us with 1024 threads, 10.4
 // with 512; 16000, 301 rows 9.5 with 512, 9.9 with 1024 of 2 vectors).
 template <typename ZT, typename OT, bool GRAD, typename Loss>
