@@ -1093,7 +1093,8 @@ def mbok_linear_backward_precise(d: mbok_desc, packed: torch.Tensor, dY: torch.T
                                  accumulate: bool = False,
                                  workspace: torch.Tensor | None | bool = True,
                                  stream=None) -> None:
-    """mbok_linear_backward with dX as mbok_gemmt_precise computes it."""
+    """mbok_linear_backward with dX as mbok_gemmt_precise computes it (of the same bf16
+    dpre)."""
     _linear_backward_call("mbok_linear_backward_precise", d, packed, dY, pre, dpre, dbias, dX,
                           act, accumulate, workspace, stream)
 

@@ -13,7 +13,7 @@
 //
 // Bound: memory, 28 bytes a parameter with fp32 states and gradients, 16 with
 // 8-bit ones, beside the copy.  (29.5 M scales of 48 layers, fp32
-// gradients: 204 us of 0.89 GB, 4.4 TB/s; 8-bit states 131 us of 0.54 GB, 4.1 TB/s, and
+// gradients: 203 us of 0.89 GB, 4.4 TB/s; 8-bit states 130 us of 0.54 GB, 4.1 TB/s, and
 // 60 M vector instructions, which alone take 100.)
 //
 // 8-bit states: 256 consecutive values, one wavefront's 64 lanes x 4, share a

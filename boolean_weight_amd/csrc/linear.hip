@@ -5,9 +5,11 @@
 //     dz = s act'(z),  db = sum_t dz,  dX = dz W_hat,  dR = s.
 // The first two are one pass over s and z (bound by memory: two values read and
 // one written per output) that adds each column's values in fp32 before they
-// are rounded; dX is the transposed product, whose operand is the rounded dz,
-// or s itself without an activation.  (2048 x 11008: 28 us, 4.9 TB/s; with dX of 4096
-// columns, K = 3, 195-200.)
+// are rounded; dX is the transposed product, whose operand is the rounded dz, or s
+// itself without an activation: bf16, as the matrix instructions and the scales'
+// gradients take it, half a step of 2^-8 beside the levels' and dX's own (the
+// two-term form leaves the levels' out).  (2048 x 11008: 28 us, 4.9 TB/s; with dX of
+// 4096 columns, K = 3, 195-200.)
 #include "mbok_launch.h"
 #include "mbok_levels.h"
 #include "mbok_linear.h"

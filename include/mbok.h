@@ -750,8 +750,8 @@ int mbok_linear_backward(const mbok_desc* d, const void* packed, const void* pre
                          int64_t lddpre, float* dbias, int32_t accumulate, void* dX,
                          int64_t lddx, void* workspace, void* stream);
 
-/* mbok_linear_backward with dX by mbok_gemmt_precise.  Same arguments, workspace
- * and errors. */
+/* mbok_linear_backward with dX by mbok_gemmt_precise, of the same dpre, rounded to
+ * bf16.  Same arguments, workspace and errors. */
 int mbok_linear_backward_precise(const mbok_desc* d, const void* packed, const void* pre,
                                  int64_t ldpre, const void* dY, int64_t lddy, int64_t T,
                                  int32_t act, void* dpre, int64_t lddpre, float* dbias,
