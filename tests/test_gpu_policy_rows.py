@@ -27,16 +27,18 @@ def _gpu():
 
 
 # 256, 512 and 1024 threads with 2, 4, 8 and 16 vectors each, and rows that are read again
-@pytest.mark.parametrize("T,V", [(600, 300), (520, 1500), (513, 9000), (600, 20000), (512, 32000),
-                                 (513, 40009), (512, 70000), (512, 140003)])
-@pytest.mark.parametrize("z,grad", [("bf16", "same"), ("f16", "same"), ("f32", "same"),
-                                    ("f16", "bf16"), ("f32", "bf16")])
+# (those in one type)
+ROWS = [(T, V, z, grad) for z, grad in (("bf16", "same"), ("f16", "same"), ("f32", "same"),
+                                        ("f16", "bf16"), ("f32", "bf16"))
+        for T, V in ((600, 300), (520, 1500), (513, 9000), (600, 20000), (512, 32000),
+                     (513, 40009), (512, 70000))] + [(512, 140003, "f32", "same")]
+
+
+@pytest.mark.parametrize("T,V,z,grad", ROWS)
 @pytest.mark.parametrize("aligned", [True, False])
 def test_many_rows_by_value(T, V, z, grad, aligned):
     """Loss, log-probability, slope and gradient of a sample of rows; what lies between
     the rows stays."""
-    if V > 100000 and (z != "f32" or grad != "same"):
-        pytest.skip("one type is enough where rows are read again")
     say(f"policy many rows T={T} V={V} {z} grad={grad} aligned={aligned}")
     tau, pad = 1.25, (-V) % 8 + (8 if aligned else 3)
     off = 8 if aligned else 1
