@@ -1248,7 +1248,8 @@ class mbok_adamw_plan:
 
     The plan may be dropped while a step that it was given to still runs on one of
     torch's streams: the table's memory is not given away before.  On a stream that is
-    not torch's (which may end first) the step has to have run by then."""
+    not torch's (which may end first), or that the call was given as a handle, the step
+    has to have run by then."""
 
     def __init__(self, plan, table: torch.Tensor, tensors: list):
         self._plan, self.table, self.tensors = plan, table, tensors
@@ -1262,7 +1263,7 @@ class mbok_adamw_plan:
         # a stream of another owner has its handle for an id
         if handle == 0 or s.stream_id != handle:
             self.table.record_stream(s)
-        self._streams.add(handle)
+            self._streams.add(handle)
 
     def __repr__(self):
         return f"mbok_adamw_plan({self._plan.tensors} tensors, {self._plan.parts} parts)"
@@ -1362,7 +1363,7 @@ def mbok_adamw(plan: mbok_adamw_plan, lr: float, step: int, beta1: float = 0.9,
     ptr = None if live is None else _vector(live, "live", dev, 4, torch.float32)
     s = _AdamwStep(lr, beta1, beta2, eps, step, grad_scale, seed & 0xffffffff)
     handle = _raw_stream(dev) if stream is None else _stream(stream)
-    if handle not in plan._streams:
+    if handle not in plan._streams and (handle == 0 or not isinstance(stream, int)):
         plan._read_on(handle, stream)
     _launch(load_library().mbok_adamw, "mbok_adamw", dev, handle, *plan._args, ctypes.byref(s),
             ptr)

@@ -69,4 +69,7 @@ def test_another_owners_stream_is_not_waited_for(gpu, stream):
     with gpu.use(Stream(0x99, own=False)):
         bw.mbok_adamw(p, lr=1e-3, step=2)
     assert p.table.recorded == []
-    assert [args[-1] for _, args in gpu.launched] == [0x99] * 2
+    with gpu.use(Stream(0x99)):  # ended, and its handle torch's since
+        bw.mbok_adamw(p, lr=1e-3, step=3)
+    assert p.table.recorded == [0x99]
+    assert [args[-1] for _, args in gpu.launched] == [0x99] * 3
